@@ -284,6 +284,88 @@ int e0_moe_layer_forward_noalloc(const e0_dims *dims, const e0_layer *layer, con
                                  const int32_t *route_idx, void *y_bf16, float *y_f32, int32_t *idx_out,
                                  float *gate_out, int *dev_status, void *stream);
 
+/* ---- Operators around the attention of a decoder layer --------------------------------
+ * The pages' LoRA placement names the attention projections next to the shared expert ([G]
+ * "Üç Aşamalı Eğitim"); attention itself is the caller's.  A decoder layer is served as
+ * add_rmsnorm -> int4_linear (queries, keys, values) -> attention -> int4_linear (output) ->
+ * moe_layer_few -> the next layer's add_rmsnorm.  None of the three needs a context, none
+ * allocates, each enqueues one kernel on `stream`, which belongs to the current device, and
+ * may be captured into a graph.  They compute for inference: none has a backward pass. */
+
+/* Formats of 8-bit activations (and of x in e0_int4_linear). */
+enum { E0_ACT_BF16 = 0, E0_ACT_INT8 = 1, E0_ACT_E4M3 = 2 };
+
+/* Residual addition and RMSNorm of T rows of d channels:
+ *   h' = bf16(h + delta), summed in float64
+ *   x  = bf16(h' norm_w / sqrt(mean(h'^2) + eps)), evaluated in float64, rounded once
+ *   per row and group of q8_group consecutive channels (0: the whole row; the last group may
+ *   be shorter): a = max |x|, q8_scale = fp32(a / M) with M = 127 (int8) or 448 (e4m3),
+ *   q8 = x M / a rounded to the nearest code, ties to even; a group of zeros has scale 0, one
+ *   with a NaN or an infinity scale NaN, both codes 0.
+ * h        bf16 [T, d], rows h_stride elements apart (as for every matrix here).
+ * delta    bf16 (delta_f32 = 0) or fp32 (1) [T, d], or NULL (h' = h).
+ * norm_w   bf16 [d]; may be NULL when only h_out is asked for.
+ * h_out    bf16 [T, d] or NULL; may be h (in place).
+ * x        bf16 [T, d] or NULL.
+ * q8       int8 or e4m3 [T, d] by q8_format, or NULL;  q8_scale fp32 [T, ceil(d / q8_group)]
+ *          contiguous.
+ * Other overlaps of outputs with inputs or one another are not allowed.  At least one output.
+ * Any d up to 32768, any strides and element alignment; rows of 16-byte aligned multiples of
+ * 8 channels run with wide accesses.  T = 0 does nothing.  Errors: INVALID_ARG, CUDA. */
+int e0_add_rmsnorm(const void *h, long long h_stride, const void *delta, int delta_f32, long long delta_stride,
+                   const void *norm_w, float eps, int T, int d, void *h_out, long long h_out_stride, void *x,
+                   long long x_stride, void *q8, int q8_format, long long q8_stride, int q8_group, float *q8_scale,
+                   void *stream);
+
+/* A matrix in the int4 affine group format of the experts (device pointers, the caller's):
+ * codes u8 [n, k/2] (element 2i in the low nibble of byte i), scale and min bf16
+ * [n, k/group], W = scale * code + min; group 64 or 128, k a multiple of it.  lora_A bf16
+ * [r, k] and lora_B bf16 [n, r] (both NULL: no LoRA), 1 <= r <= 32, lora_scale = alpha / r. */
+typedef struct {
+  const void *codes, *scale, *min;
+  int n, k, group;
+  const void *lora_A, *lora_B;
+  int lora_rank;
+  float lora_scale;
+} e0_int4_mat;
+
+/* y = W x + lora_scale B (A x) for T tokens ([G] "Birleştirilmemiş Adaptör Yürütme": the
+ * adapter stays unmerged).  Products are exact, sums fp32, y rounded once.  A token with a
+ * NaN or an infinity in x has outputs that are not finite; other tokens are not affected.
+ * x         [T, k]: bf16, or 8-bit codes (int8, e4m3) times x_scale; rows x_stride elements
+ *           apart, a multiple of 8; 16-byte aligned (8-bit: 8).
+ * x_scale   NULL for bf16, else fp32 [T, k / x_group] contiguous, x_group 64, 128 or 0 (one
+ *           scale a row): as e0_add_rmsnorm writes them.
+ * y         [T, n] bf16 (y_f32 = 0) or fp32 (1), rows y_stride elements apart; must not
+ *           overlap the inputs.
+ * Any n; any T up to 524,280, but made for few tokens: the weights are read once per 32 of
+ * them.  codes and lora_A are 16-byte aligned.  T = 0 does nothing.
+ * Errors: INVALID_ARG, CUDA. */
+int e0_int4_linear(const e0_int4_mat *w, const void *x, int x_format, long long x_stride, const float *x_scale,
+                   int x_group, int T, void *y, int y_f32, long long y_stride, void *stream);
+
+/* One MoE block of T = 1..64 tokens in one launch: h' = bf16(h + delta), then what
+ * e0_moe_layer_forward computes of h'.  The weights must be resident (layer->experts).
+ * dims, layer  host structs as for e0_create / e0_register_model, read during the call.
+ * h         [T, d] bf16;  delta [T, d] bf16 or NULL.
+ * route_idx NULL, or [T, k] int32 device: a row whose first entry is negative uses the
+ *           layer's own router.
+ * h_out     [T, d] bf16 or NULL: h'; may be h or delta.
+ * y_bf16    [T, d] bf16 (required);  y_f32 [T, d] fp32 or NULL;  idx_out [T, k] int32 or
+ *           NULL;  gate_out [T, k] fp32 or NULL.
+ * workspace device memory of the size that e0_moe_layer_few_workspace gives for (dims, T),
+ *           256-byte aligned.  Its contents do not matter before the call and mean nothing
+ *           after it.  Calls that may run at the same time (streams, graphs) need one each.
+ * dev_status device int or NULL: the kernel ORs its error bits into it (1 = index out of
+ *           range, taken as expert 0; 2 = duplicated index); the caller zeroes it.
+ * The launch is cooperative: it needs every SM of the device and waits for running kernels to
+ * leave them.  y is bit-reproducible: it depends on no order of execution.
+ * Errors: INVALID_ARG (arguments, dims outside e0_create's, T, workspace), CUDA. */
+int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, const void *h, const void *delta, int T,
+                     const int32_t *route_idx, void *h_out, void *y_bf16, float *y_f32, int32_t *idx_out,
+                     float *gate_out, void *workspace, size_t workspace_bytes, int *dev_status, void *stream);
+int e0_moe_layer_few_workspace(const e0_dims *dims, int T, size_t *bytes);
+
 /* Host-side fault injection for tests (no GPU fault is involved):
  * e0_debug_fail_staging_after(ctx, n): the (n+1)-th next staging copy is refused, so the
  *   staging call returns E0_ERR_STAGING.

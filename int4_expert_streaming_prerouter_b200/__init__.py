@@ -46,6 +46,13 @@ class Head(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w_lin", "fc1_w", "fc1_b", "fc2_w", "fc2_b")]
 
 
+class Int4Mat(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("min", ctypes.c_void_p),
+                ("n", ctypes.c_int), ("k", ctypes.c_int), ("group", ctypes.c_int),
+                ("lora_A", ctypes.c_void_p), ("lora_B", ctypes.c_void_p), ("lora_rank", ctypes.c_int),
+                ("lora_scale", ctypes.c_float)]
+
+
 class Stats(ctypes.Structure):
     _fields_ = [("steps", ctypes.c_uint64), ("staged_experts", ctypes.c_uint64),
                 ("staged_bytes", ctypes.c_uint64), ("prefetched_experts", ctypes.c_uint64),
@@ -58,6 +65,7 @@ class Stats(ctypes.Structure):
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_LL = ctypes.c_longlong
 
 # name -> (restype, argtypes); one entry per function declared in include/e0moe.h
 _SIGS = {
@@ -79,6 +87,12 @@ _SIGS = {
     "e0_last_error": (ctypes.c_char_p, []),
     "e0_moe_layer_forward_noalloc": (_I, [ctypes.POINTER(Dims), ctypes.POINTER(Layer), _P, _I, _P, _P, _P, _P,
                                           _P, _P, _P]),
+    "e0_add_rmsnorm": (_I, [_P, _LL, _P, _I, _LL, _P, ctypes.c_float, _I, _I, _P, _LL, _P, _LL, _P, _I, _LL, _I, _P,
+                            _P]),
+    "e0_int4_linear": (_I, [ctypes.POINTER(Int4Mat), _P, _I, _LL, _P, _I, _I, _P, _I, _LL, _P]),
+    "e0_moe_layer_few": (_I, [ctypes.POINTER(Dims), ctypes.POINTER(Layer), _P, _P, _I, _P, _P, _P, _P, _P, _P, _P,
+                              ctypes.c_size_t, _P, _P]),
+    "e0_moe_layer_few_workspace": (_I, [ctypes.POINTER(Dims), _I, ctypes.POINTER(ctypes.c_size_t)]),
     "e0_stream_mode": (_I, [_P, _I]),
     "e0_debug_stream_log": (_I, [_P, _P]),
     "e0_debug_pool_slot": (_I, [_P, _I, _I, ctypes.POINTER(_P)]),
@@ -168,6 +182,197 @@ def moe_layer_forward_noalloc(dims: Dims, layer: dict, h, route_idx=None, y=None
     return y
 
 
+# ---------------------------------------------------------------------------------------
+# Operators around the attention of a decoder layer (no context; see the C header)
+# ---------------------------------------------------------------------------------------
+ACT_BF16, ACT_INT8, ACT_E4M3 = 0, 1, 2
+
+
+def _act_format(t) -> int:
+    import torch
+    f = {torch.bfloat16: ACT_BF16, torch.int8: ACT_INT8, torch.float8_e4m3fn: ACT_E4M3}.get(t.dtype)
+    if f is None:
+        raise TypeError(f"expected a bfloat16, int8 or float8_e4m3fn tensor, got {t.dtype}")
+    return f
+
+
+def _rows(t, name, shape, dtypes, dev):
+    """(address, row stride in elements) of a matrix whose rows are contiguous; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unexpected type {t.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    rs, cs = t.stride()
+    if cs != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the channels of a row must be contiguous")
+    return t.data_ptr(), rs if shape[0] > 1 else max(rs, shape[1])
+
+
+def _flat(t, name, shape, dtype, dev) -> Optional[int]:
+    """Address of a contiguous tensor of the given shape and type; None for None."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _empty(shape, dtype, dev, stream):
+    """An uninitialised tensor of the pool of the stream that will write it first."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _few_workspace(dims, T, dev, stream=None):
+    import torch
+    n = ctypes.c_size_t(0)
+    _check(lib().e0_moe_layer_few_workspace(ctypes.byref(dims), T, ctypes.byref(n)))
+    return _empty(n.value, torch.uint8, dev, stream)
+
+
+def _call(dev, stream, fn, *args):
+    """Call a library function that enqueues on `stream` (default: the device's current one)
+    with the device of its tensors current."""
+    import torch
+    if dev.type != "cuda":
+        raise ValueError(f"the tensors are on {dev}: CUDA tensors are needed")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, stream.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, stream.cuda_stream))
+
+
+def add_rmsnorm(h, norm_w, delta=None, eps=1e-6, h_out=None, x=None, q8=None, q8_scale=None, q8_group=0, stream=None):
+    """h' = bf16(h + delta) and its RMSNorm, in bf16 and in 8 bits (see the C header).
+
+    h [T, d] bf16, norm_w [d] bf16, delta [T, d] bf16 or fp32 or None.  Outputs, each a tensor
+    to write or None: h_out [T, d] bf16 (may be h), x [T, d] bf16, q8 [T, d] int8 or
+    float8_e4m3fn with q8_scale [T, groups] fp32, one group for each q8_group = 64 or 128
+    channels or for a whole row (0).  x is allocated where none of the three is given, q8_scale
+    where only q8 is.  Returns (h_out, x, q8, q8_scale)."""
+    import torch
+    bf16, f32, dev = torch.bfloat16, torch.float32, h.device
+    T, d = shape = h.shape
+    if h_out is None and x is None and q8 is None:
+        x = _empty(shape, bf16, dev, stream)
+    fmt, groups = 0, 0
+    if q8 is not None:
+        fmt = _act_format(q8)
+        if fmt == ACT_BF16:
+            raise TypeError("q8: expected an int8 or float8_e4m3fn tensor")
+        if q8_group not in (0, 64, 128):
+            raise ValueError("q8_group must be 0, 64 or 128")
+        groups = -(-d // q8_group) if q8_group else 1
+        if q8_scale is None:
+            q8_scale = _empty((T, groups), f32, dev, stream)
+    hp, hs = _rows(h, "h", shape, (bf16,), dev)
+    dp, ds = _rows(delta, "delta", shape, (bf16, f32), dev)
+    op, os_ = _rows(h_out, "h_out", shape, (bf16,), dev)
+    xp, xs = _rows(x, "x", shape, (bf16,), dev)
+    qp, qs = _rows(q8, "q8", shape, (torch.int8, torch.float8_e4m3fn), dev)
+    _call(dev, stream, lib().e0_add_rmsnorm, hp, hs, dp, int(delta is not None and delta.dtype == f32), ds,
+          _flat(norm_w, "norm_w", (d,), bf16, dev), eps, T, d, op, os_, xp, xs, qp, fmt, qs, q8_group,
+          _flat(q8_scale, "q8_scale", (T, groups), f32, dev) if q8 is not None else None)
+    return h_out, x, q8, q8_scale
+
+
+class Int4Linear:
+    """A matrix in the int4 affine group format with an optional unmerged LoRA, applied to few
+    tokens (see e0_int4_linear in the C header): codes [n, k/2] uint8, scale and min [n, k/g]
+    bf16 with g = 64 or 128, lora_A [r, k] and lora_B [n, r] bf16.  Keeps the tensors."""
+
+    def __init__(self, codes, scale, min, lora_A=None, lora_B=None, lora_scale=1.0):
+        import torch
+        self.device, bf16 = codes.device, torch.bfloat16
+        self.n, self.k = codes.shape[0], 2 * codes.shape[1]
+        self.group = self.k // scale.shape[1] if scale.dim() == 2 and scale.shape[1] else 0
+        if self.group not in (64, 128) or self.k % self.group:
+            raise ValueError(f"scale [n, k/g] must have g = 64 or 128 for k = {self.k}, got {tuple(scale.shape)}")
+        if (lora_A is None) != (lora_B is None):
+            raise ValueError("LoRA needs both matrices")
+        r = lora_A.shape[0] if lora_A is not None else 0
+        dev, shape = self.device, (self.n, self.k // self.group)
+        self._keep = (codes, scale, min, lora_A, lora_B)
+        self._mat = Int4Mat(_flat(codes, "codes", (self.n, self.k // 2), torch.uint8, dev),
+                            _flat(scale, "scale", shape, bf16, dev), _flat(min, "min", shape, bf16, dev),
+                            self.n, self.k, self.group, _flat(lora_A, "lora_A", (r, self.k), bf16, dev),
+                            _flat(lora_B, "lora_B", (self.n, r), bf16, dev), r, lora_scale)
+
+    def __call__(self, x, x_scale=None, y=None, stream=None):
+        """x [T, k] bf16, or int8 / float8_e4m3fn with x_scale [T, 1], [T, k/64] or [T, k/128]
+        fp32 (as add_rmsnorm writes them) -> y [T, n], bf16 or fp32 (bf16 where it is
+        allocated here)."""
+        import torch
+        f32, dev = torch.float32, self.device
+        fmt, T = _act_format(x), x.shape[0]
+        x_group, sp = 0, None
+        if x_scale is not None:
+            groups = x_scale.shape[-1]
+            x_group = 0 if groups == 1 else self.k // max(groups, 1)
+            if x_group not in (0, 64, 128):
+                raise ValueError(f"x_scale: expected 1, k/64 or k/128 scales a row, got {groups}")
+            sp = _flat(x_scale, "x_scale", (T, self.k // x_group if x_group else 1), f32, dev)
+        if y is None:
+            y = _empty((T, self.n), torch.bfloat16, dev, stream)
+        xp, xs = _rows(x, "x", (T, self.k), (x.dtype,), dev)
+        yp, ys = _rows(y, "y", (T, self.n), (torch.bfloat16, f32), dev)
+        _call(dev, stream, lib().e0_int4_linear, ctypes.byref(self._mat), xp, fmt, xs, sp, x_group, T, yp,
+              int(y.dtype == f32), ys)
+        return y
+
+
+class MoeLayer:
+    """One MoE layer's resident weights, for few tokens without a context (see
+    e0_moe_layer_few in the C header).  `layer` is a dict of torch tensors as for
+    Context.register_model; it keeps them."""
+
+    def __init__(self, dims: Dims, layer: dict):
+        self.dims = dims
+        self._keep = dict(layer)
+        self._layer = Layer()
+        for f, _ in Layer._fields_:
+            setattr(self._layer, f, _ptr(layer.get(f)))
+
+    def few_workspace(self, T: int):
+        """A workspace for calls of at most T tokens (calls that may overlap need one each)."""
+        return _few_workspace(self.dims, T, self._keep["router_w"].device)
+
+    def few(self, h, delta=None, route_idx=None, h_out=None, y=None, y_f32=None, idx=None, gates=None, workspace=None,
+            dev_status=None, stream=None):
+        """The MoE block of 1..64 tokens in one launch: h' = bf16(h + delta) [T, d] (to h_out
+        where given; it may be h), y [T, d] bf16 = the block's output for h'.  Without
+        `workspace` one is allocated for the call."""
+        return _moe_layer_few(self.dims, self._layer, h, delta, route_idx, h_out, y, y_f32, idx, gates,
+                              workspace, dev_status, stream)
+
+
+def _moe_layer_few(dims, layer, h, delta, route_idx, h_out, y, y_f32, idx, gates, workspace, dev_status, stream):
+    import torch
+    bf16, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, h.device
+    T, shape, per_k = h.shape[0], (h.shape[0], dims.d_model), (h.shape[0], dims.top_k)
+    if y is None:
+        y = _empty(shape, bf16, dev, stream)
+    if workspace is None:
+        workspace = _few_workspace(dims, T, dev, stream)
+    _call(dev, stream, lib().e0_moe_layer_few, ctypes.byref(dims), ctypes.byref(layer), _flat(h, "h", shape, bf16, dev),
+          _flat(delta, "delta", shape, bf16, dev), T, _flat(route_idx, "route_idx", per_k, i32, dev),
+          _flat(h_out, "h_out", shape, bf16, dev), _flat(y, "y", shape, bf16, dev), _flat(y_f32, "y_f32", shape, f32, dev),
+          _flat(idx, "idx", per_k, i32, dev), _flat(gates, "gates", per_k, f32, dev),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(dev_status))
+    return y
+
+
 class Context:
     """One ``e0_ctx``: workspaces, routing tables and (optionally) the streaming pool."""
 
@@ -176,6 +381,7 @@ class Context:
         self.dims = make_dims(d, E, I, k, r, head_hidden, head_onehot, eps, lora_scale)
         self.n_layers, self.max_tokens = n_layers, max_tokens
         self._keep = []
+        self._layers = ()
         h = _P()
         _check(lib().e0_create(ctypes.byref(self.dims), n_layers, max_tokens, ctypes.byref(h)))
         self._h = h
@@ -211,6 +417,7 @@ class Context:
                 setattr(H[i], f, _ptr(t))
                 self._keep.append(t)
         _check(lib().e0_register_model(self._h, L, H))
+        self._layers = L
 
     # -- one MoE block ------------------------------------------------------------------
     def moe_layer_forward(self, layer, h, route_idx=None, y=None, y_f32=None, idx=None, gates=None,
@@ -223,6 +430,15 @@ class Context:
         _check(lib().e0_moe_layer_forward(self._h, layer, _ptr(h), T, _ptr(route_idx), _ptr(y), _ptr(y_f32),
                                           _ptr(idx), _ptr(gates), _stream(stream)))
         return y
+
+    def moe_layer_few(self, layer, h, delta=None, route_idx=None, h_out=None, y=None, y_f32=None, idx=None, gates=None,
+                      workspace=None, dev_status=None, stream=None):
+        """The MoE block of a registered layer for 1..64 tokens in one launch (see MoeLayer.few;
+        it uses none of the context's workspaces)."""
+        if not 0 <= layer < len(self._layers):
+            raise IndexError(f"layer {layer} of {len(self._layers)} registered")
+        return _moe_layer_few(self.dims, self._layers[layer], h, delta, route_idx, h_out, y, y_f32, idx, gates, workspace,
+                              dev_status, stream)
 
     def prerouter_predict(self, layer, x, cur=None, prev=None, pred=None, logits=None, stream=None):
         import torch

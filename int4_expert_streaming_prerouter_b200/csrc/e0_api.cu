@@ -7,6 +7,9 @@
 #include "e0_decode.cuh"
 #include "e0_phased.cuh"
 #include "e0_prefill.cuh"
+#include "e0_addnorm.cuh"
+#include "e0_int4.cuh"
+#include "e0_few.cuh"
 
 #include <cudaTypedefs.h>
 
@@ -2035,5 +2038,187 @@ extern "C" int e0_moe_layer_forward_noalloc(const e0_dims *dims, const e0_layer 
   k_down<<<grid_for(T * D.d_model, 4 * nsm), 256, 0, s>>>(W);
   NOALLOC_CKL("k_down");
 #undef NOALLOC_CKL
+  return E0_OK;
+}
+
+// ---------------------------------------------------------------------------------------
+// Operators around the attention of a decoder layer: residual addition + norm, int4 linear,
+// the MoE layer for few tokens.  None needs a context or allocates.
+// ---------------------------------------------------------------------------------------
+static bool misaligned(const void *p, uintptr_t to) { return ((uintptr_t)p & (to - 1)) != 0; }
+
+extern "C" int e0_add_rmsnorm(const void *h, long long h_stride, const void *delta, int delta_f32,
+                              long long delta_stride, const void *norm_w, float eps, int T, int d, void *h_out,
+                              long long h_out_stride, void *x, long long x_stride, void *q8, int q8_format,
+                              long long q8_stride, int q8_group, float *q8_scale, void *stream) {
+  if (T < 0 || d < 1) return fail(E0_ERR_INVALID_ARG, "add_rmsnorm: bad arguments");
+  if (T == 0) return E0_OK;               // the addresses of empty matrices do not matter
+  if (!h) return fail(E0_ERR_INVALID_ARG, "add_rmsnorm: h is required");
+  if (d > 32768) return fail(E0_ERR_INVALID_ARG, "add_rmsnorm: d = %d, at most 32768 is supported", d);
+  if (!h_out && !x && !q8) return fail(E0_ERR_INVALID_ARG, "add_rmsnorm: no output is asked for");
+  if ((x || q8) && !norm_w) return fail(E0_ERR_INVALID_ARG, "add_rmsnorm: norm_w is required for x and q8");
+  if (delta && delta_f32 != 0 && delta_f32 != 1) return fail(E0_ERR_INVALID_ARG, "add_rmsnorm: delta_f32 must be 0 or 1");
+  if (q8 && (!q8_scale || (q8_format != E0_ACT_INT8 && q8_format != E0_ACT_E4M3) ||
+             (q8_group != 0 && q8_group != 64 && q8_group != 128)))
+    return fail(E0_ERR_INVALID_ARG, "add_rmsnorm: q8 needs a format (int8, e4m3), a group (0, 64, 128) and q8_scale");
+  if (h_stride < d || (delta && delta_stride < d) || (h_out && h_out_stride < d) || (x && x_stride < d) ||
+      (q8 && q8_stride < d))
+    return fail(E0_ERR_INVALID_ARG, "add_rmsnorm: a row stride is below d");
+  AddNormArgs A{};
+  A.h = (const uint16_t *)h; A.h_stride = h_stride;
+  A.delta = delta; A.delta_f32 = delta_f32; A.delta_stride = delta_stride;
+  A.gamma = (const uint16_t *)norm_w; A.eps = eps; A.T = T; A.d = d;
+  A.h_out = (uint16_t *)h_out; A.h_out_stride = h_out_stride;
+  A.x = (uint16_t *)x; A.x_stride = x_stride;
+  A.q8 = (uint8_t *)q8; A.q8_stride = q8_stride; A.q8_e4m3 = q8_format == E0_ACT_E4M3; A.q8_group = q8_group;
+  A.q8_scale = q8_scale; A.groups = q8_group ? (d + q8_group - 1) / q8_group : 1;
+  // 16-byte accesses (8 for q8) where every row allows them
+  const bool vec = d % 8 == 0 && !misaligned(h, 16) && h_stride % 8 == 0 && !misaligned(norm_w, 16) &&
+                   (!delta || (!misaligned(delta, 16) && delta_stride % 8 == 0)) &&
+                   (!h_out || (!misaligned(h_out, 16) && h_out_stride % 8 == 0)) &&
+                   (!x || (!misaligned(x, 16) && x_stride % 8 == 0)) && (!q8 || (!misaligned(q8, 8) && q8_stride % 8 == 0));
+  const int chunks = (d + 7) / 8, V = chunks <= 256 ? 1 : chunks <= 2048 ? 2 : 4;
+  const int threads = ((chunks + V - 1) / V + 31) / 32 * 32;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (vec) {
+    if (V == 1) k_add_rmsnorm<1, true><<<T, threads, 0, s>>>(A);
+    else if (V == 2) k_add_rmsnorm<2, true><<<T, threads, 0, s>>>(A);
+    else k_add_rmsnorm<4, true><<<T, threads, 0, s>>>(A);
+  } else {
+    if (V == 1) k_add_rmsnorm<1, false><<<T, threads, 0, s>>>(A);
+    else if (V == 2) k_add_rmsnorm<2, false><<<T, threads, 0, s>>>(A);
+    else k_add_rmsnorm<4, false><<<T, threads, 0, s>>>(A);
+  }
+  CK(cudaGetLastError());
+  return E0_OK;
+}
+
+template <int NT>
+static int launch_linear(LinearArgs &L, cudaStream_t s) {
+  constexpr int TT = 8 * NT;
+  const int G = L.K / 64;
+  // activations of as many groups as 96 KB hold; an even number, so that scales per 128 start
+  // with a chunk
+  L.kc = std::min(G, ((96 * 1024 - TT * kActPad) / (TT * 136)) & ~1);
+  const size_t smem = std::max((size_t)TT * act_pitch(L.kc) + act_sv_bytes(L.kc, TT), (size_t)(kLinThreads / 32) * 16 * TT * 4);
+  CK(cudaFuncSetAttribute(k_int4_linear<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  const dim3 grid((L.N + kLinRows - 1) / kLinRows, (L.T + TT - 1) / TT);
+  k_int4_linear<NT><<<grid, kLinThreads, smem, s>>>(L);
+  CK(cudaGetLastError());
+  return E0_OK;
+}
+
+extern "C" int e0_int4_linear(const e0_int4_mat *w, const void *x, int x_format, long long x_stride,
+                              const float *x_scale, int x_group, int T, void *y, int y_f32, long long y_stride,
+                              void *stream) {
+  if (!w || T < 0) return fail(E0_ERR_INVALID_ARG, "int4_linear: bad arguments");
+  if (T == 0) return E0_OK;               // the addresses of empty matrices do not matter
+  if (!x || !y) return fail(E0_ERR_INVALID_ARG, "int4_linear: x and y are required");
+  if (!w->codes || !w->scale || !w->min || w->n < 1 || w->k < 1)
+    return fail(E0_ERR_INVALID_ARG, "int4_linear: codes, scale, min, n and k are required");
+  if (w->group != 64 && w->group != 128) return fail(E0_ERR_INVALID_ARG, "int4_linear: group must be 64 or 128");
+  if (w->k % w->group || w->k > (1 << 20))
+    return fail(E0_ERR_INVALID_ARG, "int4_linear: k = %d must be a multiple of the group and at most 2^20", w->k);
+  if (w->n > (1 << 26)) return fail(E0_ERR_INVALID_ARG, "int4_linear: n = %d, at most 2^26", w->n);
+  if (T > 65535 * 8) return fail(E0_ERR_INVALID_ARG, "int4_linear: T = %d, at most %d", T, 65535 * 8);
+  const bool lora = w->lora_A || w->lora_B;
+  if (lora && (!w->lora_A || !w->lora_B || w->lora_rank < 1 || w->lora_rank > kMaxR))
+    return fail(E0_ERR_INVALID_ARG, "int4_linear: LoRA needs both matrices and 1 <= lora_rank <= %d", kMaxR);
+  const bool bf16x = x_format == E0_ACT_BF16;
+  if (!bf16x && x_format != E0_ACT_INT8 && x_format != E0_ACT_E4M3)
+    return fail(E0_ERR_INVALID_ARG, "int4_linear: unknown x_format %d", x_format);
+  if (bf16x ? x_scale != nullptr : x_scale == nullptr)
+    return fail(E0_ERR_INVALID_ARG, "int4_linear: 8-bit activations need x_scale, bf16 ones take none");
+  if (!bf16x && x_group != 0 && ((x_group != 64 && x_group != 128) || w->k % x_group))
+    return fail(E0_ERR_INVALID_ARG, "int4_linear: x_group must be 0 (one scale a row), 64 or 128 and divide k");
+  if (y_f32 != 0 && y_f32 != 1) return fail(E0_ERR_INVALID_ARG, "int4_linear: y_f32 must be 0 or 1");
+  if (x_stride < w->k || y_stride < w->n) return fail(E0_ERR_INVALID_ARG, "int4_linear: a row stride is below its length");
+  if (misaligned(w->codes, 16) || misaligned(x, bf16x ? 16 : 8) || x_stride % 8 || misaligned(w->lora_A, 16))
+    return fail(E0_ERR_INVALID_ARG, "int4_linear: codes, lora_A and bf16 x are 16-byte aligned, 8-bit x 8-byte, x_stride a multiple of 8");
+  LinearArgs L{};
+  L.codes = (const uint8_t *)w->codes; L.scale = (const uint16_t *)w->scale; L.min = (const uint16_t *)w->min;
+  L.N = w->n; L.K = w->k; L.gs = w->group == 128;
+  L.A = (const uint16_t *)w->lora_A; L.B = (const uint16_t *)w->lora_B; L.r = w->lora_rank; L.c = w->lora_scale;
+  L.x = x; L.x_type = x_format; L.x_stride = x_stride; L.x_scale = x_scale; L.x_group = x_group ? x_group : w->k;
+  L.T = T; L.y = y; L.y_f32 = y_f32; L.y_stride = y_stride;
+  cudaStream_t s = (cudaStream_t)stream;
+  return T <= 8 ? launch_linear<1>(L, s) : T <= 16 ? launch_linear<2>(L, s) : launch_linear<4>(L, s);
+}
+
+// Workspace regions of e0_moe_layer_few, 256-byte aligned.
+struct FewSpace {
+  size_t xb, logits, lt, a, bytes;
+};
+static FewSpace few_space(const e0_dims &D, int T) {
+  const size_t d = D.d_model, E = D.n_experts, I = D.d_ff, k = D.top_k, r = D.lora_rank;
+  FewSpace S{};
+  S.xb = S.bytes;     S.bytes += noalloc_align((size_t)T * d * 2);
+  S.logits = S.bytes; S.bytes += noalloc_align((size_t)T * E * 4);
+  S.lt = S.bytes;     S.bytes += noalloc_align((size_t)T * 2 * r * 4);
+  S.a = S.bytes;      S.bytes += noalloc_align((size_t)T * (k + 1) * I * 2);
+  return S;
+}
+
+extern "C" int e0_moe_layer_few_workspace(const e0_dims *dims, int T, size_t *bytes) {
+  if (!dims || !bytes || T < 1 || T > kFewMaxT || !supported(*dims))
+    return fail(E0_ERR_INVALID_ARG, "moe_layer_few: unsupported dims, or T outside 1..%d", kFewMaxT);
+  *bytes = few_space(*dims, T).bytes;
+  return E0_OK;
+}
+
+extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, const void *h, const void *delta, int T,
+                                const int32_t *route_idx, void *h_out, void *y_bf16, float *y_f32, int32_t *idx_out,
+                                float *gate_out, void *workspace, size_t workspace_bytes, int *dev_status,
+                                void *stream) {
+  if (!dims || !layer || !h || !y_bf16) return fail(E0_ERR_INVALID_ARG, "moe_layer_few: bad arguments");
+  if (!supported(*dims)) return fail(E0_ERR_INVALID_ARG, "moe_layer_few: unsupported dims");
+  if (T < 1 || T > kFewMaxT) return fail(E0_ERR_INVALID_ARG, "moe_layer_few: T = %d, 1 to %d tokens are supported", T, kFewMaxT);
+  const e0_dims &D = *dims;
+  const e0_layer &Y = *layer;
+  if (!Y.experts || !Y.shared || !Y.router_w || !Y.norm_w)
+    return fail(E0_ERR_INVALID_ARG, "moe_layer_few: experts, shared, router_w and norm_w are required");
+  const bool any = Y.lora_Ag || Y.lora_Bg || Y.lora_Au || Y.lora_Bu || Y.lora_Ad || Y.lora_Bd;
+  const bool all = Y.lora_Ag && Y.lora_Bg && Y.lora_Au && Y.lora_Bu && Y.lora_Ad && Y.lora_Bd;
+  if (any && (!all || D.lora_rank < 1))
+    return fail(E0_ERR_INVALID_ARG, "moe_layer_few: LoRA needs all six matrices and lora_rank >= 1");
+  if (misaligned(Y.experts, 16) || misaligned(Y.shared, 16) || misaligned(Y.router_w, 16) || misaligned(Y.norm_w, 16) ||
+      misaligned(Y.lora_Ag, 16) || misaligned(Y.lora_Au, 16) || misaligned(Y.lora_Ad, 16) || misaligned(h, 16) ||
+      misaligned(delta, 16) || misaligned(h_out, 16))
+    return fail(E0_ERR_INVALID_ARG, "moe_layer_few: weights, h, delta and h_out are 16-byte aligned");
+  const FewSpace S = few_space(D, T);
+  if (!workspace || misaligned(workspace, 256) || workspace_bytes < S.bytes)
+    return fail(E0_ERR_INVALID_ARG, "moe_layer_few: %zu bytes of workspace are needed, 256-byte aligned", S.bytes);
+  FewArgs A{};
+  A.h = (const uint16_t *)h; A.delta = (const uint16_t *)delta;
+  A.gamma = (const uint16_t *)Y.norm_w; A.router = (const uint16_t *)Y.router_w;
+  A.experts = (const uint8_t *)Y.experts; A.shared = (const uint8_t *)Y.shared;
+  A.Ag = (const uint16_t *)Y.lora_Ag; A.Bg = (const uint16_t *)Y.lora_Bg; A.Au = (const uint16_t *)Y.lora_Au;
+  A.Bu = (const uint16_t *)Y.lora_Bu; A.Ad = (const uint16_t *)Y.lora_Ad; A.Bd = (const uint16_t *)Y.lora_Bd;
+  A.bl = blob_of(D.d_model, D.d_ff);
+  A.T = T; A.d = D.d_model; A.E = D.n_experts; A.I = D.d_ff; A.k = D.top_k; A.r = D.lora_rank;
+  A.eps = D.rms_eps; A.c = D.lora_scale; A.route = route_idx;
+  A.h_out = (uint16_t *)h_out; A.y = (uint16_t *)y_bf16; A.yf = y_f32; A.idx = idx_out; A.gates = gate_out;
+  uint8_t *ws = (uint8_t *)workspace;
+  A.xb = (uint16_t *)(ws + S.xb); A.logits = (float *)(ws + S.logits); A.lt = (float *)(ws + S.lt);
+  A.a = (uint16_t *)(ws + S.a);
+  A.err = dev_status;
+  int dev = 0, nsm = 0, coop = 0, most = 0;
+  CK(cudaGetDevice(&dev));
+  CK(cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev));
+  CK(cudaDeviceGetAttribute(&coop, cudaDevAttrCooperativeLaunch, dev));
+  CK(cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev));
+  if (!coop || nsm < (kFewMaxT + 7) / 8) return fail(E0_ERR_CUDA, "moe_layer_few: the device has no cooperative launch");
+  const int smem = most, area = smem - (int)few_plan_bytes() - kFewRedBytes;
+  // activation rows that fit the staging area, and so the tokens of a segment
+  const int places = T * (A.k + 1) + std::min(A.E, T * A.k) + 1;
+  A.parts_bytes = std::max(16384, (places * 64 + 127) / 128 * 128);
+  A.gu_rows = area / (A.d / 64 * 136 + kActPad);
+  A.dn_rows = (area - A.parts_bytes) / (A.I / 64 * 136 + kActPad);
+  const int rows = std::min(A.gu_rows, A.dn_rows);
+  A.seg_cap = rows >= 32 ? 32 : rows >= 16 ? 16 : 8;
+  if (rows < 8) return fail(E0_ERR_INVALID_ARG, "moe_layer_few: dims too large for the staging area");
+  CK(cudaFuncSetAttribute(k_moe_few, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  void *args[] = {&A};
+  CK(cudaLaunchCooperativeKernel((const void *)k_moe_few, dim3(nsm), dim3(kFewThreads), args, (size_t)smem, (cudaStream_t)stream));
   return E0_OK;
 }

@@ -1,0 +1,138 @@
+"""The operators around the attention (add_rmsnorm, int4_linear, moe_layer_few) refuse what
+they do not take before anything is enqueued.  CPU only: the addresses are never read."""
+import ctypes
+
+import pytest
+import torch
+
+import int4_expert_streaming_prerouter_b200 as e0
+
+P = 1 << 20          # an aligned address that no call reads
+
+
+def norm(**kw):
+    a = dict(h=P, h_stride=256, delta=None, delta_f32=0, delta_stride=0, norm_w=P, eps=1e-6, T=2, d=256, h_out=None,
+             h_out_stride=0, x=P, x_stride=256, q8=None, q8_format=0, q8_stride=0, q8_group=0, q8_scale=None, stream=None)
+    assert set(kw) <= set(a)
+    return e0.lib().e0_add_rmsnorm(*(a | kw).values())
+
+
+@pytest.mark.parametrize("bad", [
+    dict(h=None), dict(T=-1), dict(d=0), dict(d=32769, h_stride=40000, x_stride=40000), dict(x=None), dict(norm_w=None),
+    dict(h_stride=255), dict(x_stride=255), dict(delta=P, delta_stride=255), dict(delta=P, delta_stride=256, delta_f32=2),
+    dict(h_out=P, h_out_stride=0), dict(q8=P, q8_stride=256, q8_format=1),                      # no scales
+    dict(q8=P, q8_stride=256, q8_format=0, q8_scale=P), dict(q8=P, q8_stride=256, q8_format=3, q8_scale=P),
+    dict(q8=P, q8_stride=256, q8_format=1, q8_scale=P, q8_group=32), dict(q8=P, q8_stride=9, q8_format=1, q8_scale=P),
+])
+def test_add_rmsnorm_refuses(bad):
+    assert norm(**bad) == -1
+    assert b"add_rmsnorm" in e0.lib().e0_last_error()
+
+
+def test_add_rmsnorm_of_no_rows_is_nothing():
+    assert norm(T=0) == 0
+
+
+def linear(mat=None, **kw):
+    m = dict(codes=P, scale=P, min=P, n=48, k=256, group=64, lora_A=None, lora_B=None, lora_rank=0, lora_scale=1.0)
+    assert set(mat or {}) <= set(m)
+    m = e0.Int4Mat(*(m | (mat or {})).values())
+    a = dict(x=P, x_format=0, x_stride=256, x_scale=None, x_group=0, T=2, y=P, y_f32=0, y_stride=48, stream=None)
+    assert set(kw) <= set(a)
+    return e0.lib().e0_int4_linear(ctypes.byref(m), *(a | kw).values())
+
+
+@pytest.mark.parametrize("mat,bad", [
+    (dict(codes=None), {}), (dict(scale=None), {}), (dict(min=None), {}), (dict(n=0), {}), (dict(k=0), {}),
+    (dict(group=32), {}), (dict(k=192, group=128), {}), (dict(k=224), {}), (dict(codes=P + 8), {}),
+    (dict(lora_A=P), {}), (dict(lora_B=P, lora_rank=4), {}), (dict(lora_A=P, lora_B=P, lora_rank=33), {}),
+    (dict(lora_A=P, lora_B=P, lora_rank=0), {}), (dict(lora_A=P + 2, lora_B=P, lora_rank=4), {}),
+    ({}, dict(x=None)), ({}, dict(y=None)), ({}, dict(T=-1)), ({}, dict(x_format=3)), ({}, dict(x_format=-1)),
+    ({}, dict(x_scale=P)), ({}, dict(x_format=1)), ({}, dict(x_format=1, x_scale=P, x_group=32)),
+    (dict(k=192), dict(x_format=1, x_scale=P, x_group=128)), ({}, dict(x=P + 8)), ({}, dict(x_stride=255)),
+    ({}, dict(x_stride=260)), ({}, dict(y_stride=47)), ({}, dict(y_f32=2)), ({}, dict(T=524281)),
+])
+def test_int4_linear_refuses(mat, bad):
+    assert linear(mat, **bad) == -1
+    assert b"int4_linear" in e0.lib().e0_last_error()
+
+
+def test_int4_linear_of_no_tokens_is_nothing():
+    assert linear(T=0) == 0
+
+
+def few(dims=None, layer=None, **kw):
+    D = e0.make_dims(*(dims or (256, 16, 128, 4, 8)))
+    L = dict(experts=P, shared=P, lora_Ag=None, lora_Bg=None, lora_Au=None, lora_Bu=None, lora_Ad=None, lora_Bd=None,
+             router_w=P, norm_w=P)
+    assert set(layer or {}) <= set(L)
+    L = e0.Layer(*(L | (layer or {})).values())
+    a = dict(h=P, delta=None, T=2, route_idx=None, h_out=None, y=P, y_f32=None, idx=None, gates=None, workspace=P,
+             workspace_bytes=1 << 30, dev_status=None, stream=None)
+    assert set(kw) <= set(a)
+    return e0.lib().e0_moe_layer_few(ctypes.byref(D), ctypes.byref(L), *(a | kw).values())
+
+
+@pytest.mark.parametrize("dims,layer,bad", [
+    (None, None, dict(h=None)), (None, None, dict(y=None)), (None, None, dict(T=0)), (None, None, dict(T=65)),
+    (None, None, dict(T=-1)), (None, None, dict(workspace=None)), (None, None, dict(workspace=P + 16)),
+    (None, None, dict(workspace_bytes=100)), (None, None, dict(h=P + 2)), (None, None, dict(delta=P + 2)),
+    (None, None, dict(h_out=P + 2)), (None, dict(experts=None), {}), (None, dict(shared=None), {}),
+    (None, dict(router_w=None), {}), (None, dict(norm_w=None), {}), (None, dict(experts=P + 8), {}),
+    (None, dict(lora_Ag=P), {}), (None, dict(lora_Bd=P), {}), ((100, 16, 128, 4, 8), None, {}),
+    ((256, 257, 128, 4, 8), None, {}), ((256, 16, 100, 4, 8), None, {}), ((256, 16, 128, 9, 8), None, {}),
+    ((256, 3, 128, 4, 8), None, {}), ((256, 16, 128, 4, 33), None, {}), ((8192, 16, 128, 4, 8), None, {}),
+])
+def test_moe_layer_few_refuses(dims, layer, bad):
+    assert few(dims, layer, **bad) == -1
+    assert b"moe_layer_few" in e0.lib().e0_last_error()
+
+
+def test_moe_layer_few_workspace_size():
+    D, n, last = e0.make_dims(2048, 256, 512, 4, 16), ctypes.c_size_t(0), 0
+    for T in (1, 2, 8, 64):
+        assert e0.lib().e0_moe_layer_few_workspace(ctypes.byref(D), T, ctypes.byref(n)) == 0
+        # x, logits, LoRA intermediates and a of T tokens at least; no more with fewer tokens
+        assert n.value >= T * (2 * 2048 + 4 * 256 + 8 * 16 + 2 * 5 * 512) and n.value >= last
+        last = n.value
+    for T in (0, 65):
+        assert e0.lib().e0_moe_layer_few_workspace(ctypes.byref(D), T, ctypes.byref(n)) == -1
+
+
+def test_the_binding_refuses_what_does_not_fit():
+    bf16 = torch.bfloat16
+    h, w = torch.zeros(2, 64, dtype=bf16), torch.zeros(64, dtype=bf16)
+    with pytest.raises(ValueError):                       # not on a GPU
+        e0.add_rmsnorm(h, w, x=torch.zeros_like(h))
+    with pytest.raises(TypeError):
+        e0.add_rmsnorm(h.float(), w, x=torch.zeros_like(h))
+    with pytest.raises(ValueError):
+        e0.add_rmsnorm(h, w, delta=torch.zeros(2, 32, dtype=bf16), x=h)
+    with pytest.raises(ValueError):
+        e0.add_rmsnorm(h, w[:32], x=torch.zeros_like(h))
+    with pytest.raises(TypeError):
+        e0.add_rmsnorm(h, w, q8=torch.zeros(2, 64, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        e0.add_rmsnorm(h, w, q8=torch.zeros(2, 64, dtype=torch.int8), q8_group=32)
+    with pytest.raises(ValueError):                       # transposed: a row's channels are apart
+        e0.add_rmsnorm(torch.zeros(64, 2, dtype=bf16).T, w, x=h)
+    codes, s = torch.zeros(8, 64, dtype=torch.uint8), torch.zeros(8, 2, dtype=bf16)
+    with pytest.raises(ValueError):
+        e0.Int4Linear(codes, torch.zeros(8, 3, dtype=bf16), torch.zeros(8, 3, dtype=bf16))
+    with pytest.raises(ValueError):
+        e0.Int4Linear(codes, s, s[:4])
+    with pytest.raises(ValueError):
+        e0.Int4Linear(codes, s, s, lora_A=torch.zeros(4, 128, dtype=bf16))
+    lin = e0.Int4Linear(codes, s, s)
+    assert (lin.n, lin.k, lin.group) == (8, 128, 64)
+    with pytest.raises(TypeError):
+        lin(torch.zeros(1, 128))
+    with pytest.raises(ValueError):
+        lin(torch.zeros(1, 64, dtype=bf16), y=torch.zeros(1, 8, dtype=bf16))
+    with pytest.raises(ValueError):
+        lin(torch.zeros(1, 128, dtype=torch.int8), x_scale=torch.zeros(1, 3), y=torch.zeros(1, 8, dtype=bf16))
+    ml = e0.MoeLayer(e0.make_dims(256, 16, 128, 4, 8), {"router_w": torch.zeros(16, 256, dtype=bf16)})
+    with pytest.raises(ValueError):
+        ml.few(torch.zeros(1, 128, dtype=bf16), y=torch.zeros(1, 256, dtype=bf16), workspace=codes)
+    with pytest.raises(e0.E0Error):
+        ml.few_workspace(65)
