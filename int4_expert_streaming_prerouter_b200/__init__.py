@@ -188,69 +188,93 @@ def moe_layer_forward_noalloc(dims: Dims, layer: dict, h, route_idx=None, y=None
 ACT_BF16, ACT_INT8, ACT_E4M3 = 0, 1, 2
 
 
+class _Torch:
+    """What these calls need of torch, looked up once: they take a few microseconds in all, of
+    which every lookup is a part."""
+
+    def __init__(self):
+        import torch
+        self.bf16, self.f32, self.i32, self.u8 = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+        self.int8, self.e4m3 = torch.int8, torch.float8_e4m3fn
+        self.act = {self.bf16: ACT_BF16, self.int8: ACT_INT8, self.e4m3: ACT_E4M3}
+        self.empty, self.on_device, self.on_stream = torch.empty, torch.cuda.device, torch.cuda.stream
+        self.current_stream, self.current_device = torch.cuda.current_stream, torch.cuda.current_device
+        # the handle of a device's current stream, without an object around it
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+_torch_names = None
+
+
+def _torch() -> _Torch:
+    global _torch_names
+    if _torch_names is None:
+        _torch_names = _Torch()
+    return _torch_names
+
+
 def _act_format(t) -> int:
-    import torch
-    f = {torch.bfloat16: ACT_BF16, torch.int8: ACT_INT8, torch.float8_e4m3fn: ACT_E4M3}.get(t.dtype)
+    f = _torch().act.get(t.dtype)
     if f is None:
         raise TypeError(f"expected a bfloat16, int8 or float8_e4m3fn tensor, got {t.dtype}")
     return f
 
 
-def _rows(t, name, shape, dtypes, dev):
-    """(address, row stride in elements) of a matrix whose rows are contiguous; (None, 0) for None."""
-    if t is None:
-        return None, 0
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: unexpected type {t.dtype}")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+def _rows(t, name, shape, d, dtype, dev):
+    """(address, row stride in elements) of a matrix of `shape` whose rows of d are contiguous."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape or t.get_device() != dev:
+        raise ValueError(f"{name}: expected shape {tuple(shape)} on the device of the other tensors, got {tuple(t.shape)} on "
+                         f"{t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), d
     rs, cs = t.stride()
-    if cs != 1 and shape[1] > 1:
+    if cs != 1 and d > 1:
         raise ValueError(f"{name}: the channels of a row must be contiguous")
-    return t.data_ptr(), rs if shape[0] > 1 else max(rs, shape[1])
+    return t.data_ptr(), rs if t.shape[0] > 1 else max(rs, d)
 
 
 def _flat(t, name, shape, dtype, dev) -> Optional[int]:
     """Address of a contiguous tensor of the given shape and type; None for None."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on the device of the other "
+                         f"tensors, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _empty(shape, dtype, dev, stream):
+def _empty(shape, dtype, device, stream):
     """An uninitialised tensor of the pool of the stream that will write it first."""
-    import torch
+    X = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return X.empty(shape, dtype=dtype, device=device)
+    with X.on_stream(stream):
+        return X.empty(shape, dtype=dtype, device=device)
 
 
-def _few_workspace(dims, T, dev, stream=None):
-    import torch
+def _few_workspace(dims, T, device, stream=None):
     n = ctypes.c_size_t(0)
     _check(lib().e0_moe_layer_few_workspace(ctypes.byref(dims), T, ctypes.byref(n)))
-    return _empty(n.value, torch.uint8, dev, stream)
+    return _empty(n.value, _torch().u8, device, stream)
 
 
 def _call(dev, stream, fn, *args):
-    """Call a library function that enqueues on `stream` (default: the device's current one)
-    with the device of its tensors current."""
-    import torch
-    if dev.type != "cuda":
-        raise ValueError(f"the tensors are on {dev}: CUDA tensors are needed")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, stream.cuda_stream))
+    """Call a library function that enqueues on `stream` (default: the current one of device
+    `dev`) with that device current."""
+    X = _torch()
+    if dev < 0:
+        raise ValueError("CUDA tensors are needed")
+    raw = X.raw_stream(dev) if stream is None else stream.cuda_stream
+    if dev == X.current_device():
+        rc = fn(*args, raw)
     else:
-        with torch.cuda.device(dev):
-            _check(fn(*args, stream.cuda_stream))
+        with X.on_device(dev):
+            rc = fn(*args, raw)
+    if rc:
+        _check(rc)
 
 
 def add_rmsnorm(h, norm_w, delta=None, eps=1e-6, h_out=None, x=None, q8=None, q8_scale=None, q8_group=0, stream=None):
@@ -261,12 +285,21 @@ def add_rmsnorm(h, norm_w, delta=None, eps=1e-6, h_out=None, x=None, q8=None, q8
     float8_e4m3fn with q8_scale [T, groups] fp32, one group for each q8_group = 64 or 128
     channels or for a whole row (0).  x is allocated where none of the three is given, q8_scale
     where only q8 is.  Returns (h_out, x, q8, q8_scale)."""
-    import torch
-    bf16, f32, dev = torch.bfloat16, torch.float32, h.device
-    T, d = shape = h.shape
+    X = _torch()
+    bf16, dev = X.bf16, h.get_device()
+    shape = h.shape
+    T, d = shape
+    hp, hs = _rows(h, "h", shape, d, bf16, dev)
     if h_out is None and x is None and q8 is None:
-        x = _empty(shape, bf16, dev, stream)
-    fmt, groups = 0, 0
+        x = _empty(shape, bf16, h.device, stream)
+    dp = ds = f32 = op = os_ = xp = xs = qp = qs = fmt = sp = 0
+    if delta is not None:
+        f32 = delta.dtype is X.f32
+        dp, ds = _rows(delta, "delta", shape, d, X.f32 if f32 else bf16, dev)
+    if h_out is not None:
+        op, os_ = _rows(h_out, "h_out", shape, d, bf16, dev)
+    if x is not None:
+        xp, xs = _rows(x, "x", shape, d, bf16, dev)
     if q8 is not None:
         fmt = _act_format(q8)
         if fmt == ACT_BF16:
@@ -275,15 +308,11 @@ def add_rmsnorm(h, norm_w, delta=None, eps=1e-6, h_out=None, x=None, q8=None, q8
             raise ValueError("q8_group must be 0, 64 or 128")
         groups = -(-d // q8_group) if q8_group else 1
         if q8_scale is None:
-            q8_scale = _empty((T, groups), f32, dev, stream)
-    hp, hs = _rows(h, "h", shape, (bf16,), dev)
-    dp, ds = _rows(delta, "delta", shape, (bf16, f32), dev)
-    op, os_ = _rows(h_out, "h_out", shape, (bf16,), dev)
-    xp, xs = _rows(x, "x", shape, (bf16,), dev)
-    qp, qs = _rows(q8, "q8", shape, (torch.int8, torch.float8_e4m3fn), dev)
-    _call(dev, stream, lib().e0_add_rmsnorm, hp, hs, dp, int(delta is not None and delta.dtype == f32), ds,
-          _flat(norm_w, "norm_w", (d,), bf16, dev), eps, T, d, op, os_, xp, xs, qp, fmt, qs, q8_group,
-          _flat(q8_scale, "q8_scale", (T, groups), f32, dev) if q8 is not None else None)
+            q8_scale = _empty((T, groups), X.f32, h.device, stream)
+        qp, qs = _rows(q8, "q8", shape, d, q8.dtype, dev)
+        sp = _flat(q8_scale, "q8_scale", (T, groups), X.f32, dev)
+    _call(dev, stream, lib().e0_add_rmsnorm, hp, hs, dp, f32, ds, _flat(norm_w, "norm_w", (d,), bf16, dev), eps, T, d, op,
+          os_, xp, xs, qp, fmt, qs, q8_group, sp)
     return h_out, x, q8, q8_scale
 
 
@@ -293,42 +322,43 @@ class Int4Linear:
     bf16 with g = 64 or 128, lora_A [r, k] and lora_B [n, r] bf16.  Keeps the tensors."""
 
     def __init__(self, codes, scale, min, lora_A=None, lora_B=None, lora_scale=1.0):
-        import torch
-        self.device, bf16 = codes.device, torch.bfloat16
-        self.n, self.k = codes.shape[0], 2 * codes.shape[1]
+        X = _torch()
+        bf16, dev = X.bf16, codes.get_device()
+        self.device, self.n, self.k = codes.device, codes.shape[0], 2 * codes.shape[1]
         self.group = self.k // scale.shape[1] if scale.dim() == 2 and scale.shape[1] else 0
         if self.group not in (64, 128) or self.k % self.group:
             raise ValueError(f"scale [n, k/g] must have g = 64 or 128 for k = {self.k}, got {tuple(scale.shape)}")
         if (lora_A is None) != (lora_B is None):
             raise ValueError("LoRA needs both matrices")
         r = lora_A.shape[0] if lora_A is not None else 0
-        dev, shape = self.device, (self.n, self.k // self.group)
+        shape = (self.n, self.k // self.group)
         self._keep = (codes, scale, min, lora_A, lora_B)
-        self._mat = Int4Mat(_flat(codes, "codes", (self.n, self.k // 2), torch.uint8, dev),
+        self._mat = Int4Mat(_flat(codes, "codes", (self.n, self.k // 2), X.u8, dev),
                             _flat(scale, "scale", shape, bf16, dev), _flat(min, "min", shape, bf16, dev),
                             self.n, self.k, self.group, _flat(lora_A, "lora_A", (r, self.k), bf16, dev),
                             _flat(lora_B, "lora_B", (self.n, r), bf16, dev), r, lora_scale)
+        self._ref, self._dev = ctypes.byref(self._mat), dev
 
     def __call__(self, x, x_scale=None, y=None, stream=None):
         """x [T, k] bf16, or int8 / float8_e4m3fn with x_scale [T, 1], [T, k/64] or [T, k/128]
         fp32 (as add_rmsnorm writes them) -> y [T, n], bf16 or fp32 (bf16 where it is
         allocated here)."""
-        import torch
-        f32, dev = torch.float32, self.device
-        fmt, T = _act_format(x), x.shape[0]
+        X = _torch()
+        dev, k, n, T = self._dev, self.k, self.n, x.shape[0]
+        fmt = _act_format(x)
+        xp, xs = _rows(x, "x", (T, k), k, x.dtype, dev)
         x_group, sp = 0, None
         if x_scale is not None:
             groups = x_scale.shape[-1]
-            x_group = 0 if groups == 1 else self.k // max(groups, 1)
+            x_group = 0 if groups <= 1 else k // groups
             if x_group not in (0, 64, 128):
                 raise ValueError(f"x_scale: expected 1, k/64 or k/128 scales a row, got {groups}")
-            sp = _flat(x_scale, "x_scale", (T, self.k // x_group if x_group else 1), f32, dev)
+            sp = _flat(x_scale, "x_scale", (T, k // x_group if x_group else 1), X.f32, dev)
         if y is None:
-            y = _empty((T, self.n), torch.bfloat16, dev, stream)
-        xp, xs = _rows(x, "x", (T, self.k), (x.dtype,), dev)
-        yp, ys = _rows(y, "y", (T, self.n), (torch.bfloat16, f32), dev)
-        _call(dev, stream, lib().e0_int4_linear, ctypes.byref(self._mat), xp, fmt, xs, sp, x_group, T, yp,
-              int(y.dtype == f32), ys)
+            y = _empty((T, n), X.bf16, self.device, stream)
+        f32 = y.dtype is X.f32
+        yp, ys = _rows(y, "y", (T, n), n, X.f32 if f32 else X.bf16, dev)
+        _call(dev, stream, lib().e0_int4_linear, self._ref, xp, fmt, xs, sp, x_group, T, yp, f32, ys)
         return y
 
 
@@ -358,18 +388,20 @@ class MoeLayer:
 
 
 def _moe_layer_few(dims, layer, h, delta, route_idx, h_out, y, y_f32, idx, gates, workspace, dev_status, stream):
-    import torch
-    bf16, f32, i32, dev = torch.bfloat16, torch.float32, torch.int32, h.device
-    T, shape, per_k = h.shape[0], (h.shape[0], dims.d_model), (h.shape[0], dims.top_k)
+    X = _torch()
+    bf16, f32, i32, dev, T = X.bf16, X.f32, X.i32, h.get_device(), h.shape[0]
+    shape, per_k = (T, dims.d_model), (T, dims.top_k)
+    hp = _flat(h, "h", shape, bf16, dev)
     if y is None:
-        y = _empty(shape, bf16, dev, stream)
+        y = _empty(shape, bf16, h.device, stream)
     if workspace is None:
-        workspace = _few_workspace(dims, T, dev, stream)
-    _call(dev, stream, lib().e0_moe_layer_few, ctypes.byref(dims), ctypes.byref(layer), _flat(h, "h", shape, bf16, dev),
+        workspace = _few_workspace(dims, T, h.device, stream)
+    _call(dev, stream, lib().e0_moe_layer_few, ctypes.byref(dims), ctypes.byref(layer), hp,
           _flat(delta, "delta", shape, bf16, dev), T, _flat(route_idx, "route_idx", per_k, i32, dev),
           _flat(h_out, "h_out", shape, bf16, dev), _flat(y, "y", shape, bf16, dev), _flat(y_f32, "y_f32", shape, f32, dev),
           _flat(idx, "idx", per_k, i32, dev), _flat(gates, "gates", per_k, f32, dev),
-          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _ptr(dev_status))
+          _flat(workspace, "workspace", (workspace.numel(),), X.u8, dev), workspace.numel(),
+          _flat(dev_status, "dev_status", (1,), i32, dev))
     return y
 
 
