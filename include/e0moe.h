@@ -296,7 +296,7 @@ int e0_moe_layer_forward_noalloc(const e0_dims *dims, const e0_layer *layer, con
 enum { E0_ACT_BF16 = 0, E0_ACT_INT8 = 1, E0_ACT_E4M3 = 2 };
 
 /* Residual addition and RMSNorm of T rows of d channels:
- *   h' = bf16(h + delta), summed in float64
+ *   h' = bf16(h + delta), the exact sum rounded once
  *   x  = bf16(h' norm_w / sqrt(mean(h'^2) + eps)), evaluated in float64, rounded once
  *   per row and group of q8_group consecutive channels (0: the whole row; the last group may
  *   be shorter): a = max |x|, q8_scale = fp32(a / M) with M = 127 (int8) or 448 (e4m3),

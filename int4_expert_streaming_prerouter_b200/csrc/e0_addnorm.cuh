@@ -1,6 +1,6 @@
 // Residual addition + RMSNorm with an optional 8-bit output (e0_add_rmsnorm).
 //
-//   h' = bf16(h + delta)                              (summed in 64 bits, rounded once)
+//   h' = bf16(h + delta)                              (the exact sum rounded once)
 //   x  = bf16(h' gamma / sqrt(mean(h'^2) + eps))      (evaluated in 64 bits, rounded once)
 //   per token and group G of consecutive channels:  a = max |x_G|,  scale = a / M  (fp32),
 //   q = x M / a to the nearest int8 (M = 127) or e4m3 (M = 448), ties to even
@@ -37,23 +37,29 @@ struct AddNormArgs {
   int groups;
 };
 
-// bf16(a + b) of the exact sum.  fp32 addition followed by rounding to bf16 differs from it
-// only when the fp32 sum has fallen on a bf16 border (or outside the normal range).
+// bf16(a + b) of the exact sum.  Rounding the fp32 sum differs from it only where that sum is a
+// border between two bf16 values and not exact: what was lost (exact in fp32, by the order of the
+// subtractions) then tells the side.
 __device__ __forceinline__ uint16_t add_bf16(float a, float b) {
   const float s = a + b;
-  const uint32_t u = __float_as_uint(s);
-  const uint32_t e = (u >> 23) & 255u;
-  if ((u & 0xFFFFu) == 0x8000u || e < 2u || e > 253u) return d2bf((double)a + (double)b);
-  return f2bf(s);
+  uint32_t u = __float_as_uint(s);
+  if ((u & 0xFFFFu) == 0x8000u) {
+    const float bb = s - a, lost = (a - (s - bb)) + (b - bb);
+    if (lost != 0.f) u += (lost > 0.f) == (s > 0.f) ? 1u : 0xFFFFFFFFu;
+  }
+  return f2bf(__uint_as_float(u));
 }
 
 // bf16(h g rinv), rinv in 64 bits and rinv_f its fp32 rounding.  The fp32 product carries three
 // roundings of half an ulp each, so it is off by at most 3 ulp.
-__device__ __forceinline__ uint16_t norm_bf16(float h, float g, double rinv, float rinv_f) {
+// (The 64-bit form stays a call: inlined at every element it would be most of the code.)
+__device__ __noinline__ uint32_t norm_bf16_64(float h, float g, double rinv) { return d2bf((double)h * (double)g * rinv); }
+
+__device__ __forceinline__ uint32_t norm_bf16(float h, float g, double rinv, float rinv_f) {
   const float p = h * rinv_f * g;
   const uint32_t u = __float_as_uint(p);
   const uint32_t e = (u >> 23) & 255u;
-  if ((u & 0xFFFFu) - 0x7FFCu <= 8u || e - 16u > 222u) return d2bf((double)h * (double)g * rinv);
+  if ((u & 0xFFFFu) - 0x7FFCu <= 8u || e - 16u > 222u) return norm_bf16_64(h, g, rinv);
   return f2bf(p);
 }
 
@@ -210,7 +216,7 @@ __global__ void __launch_bounds__(1024) k_add_rmsnorm(AddNormArgs A) {
   __syncthreads();
   ss = 0.0;
   for (int w = 0; w < nwarp; w++) ss += red[w];         // the same order on every thread
-  const double rinv = 1.0 / sqrt(ss / d + (double)A.eps);
+  const double rinv = rsqrt(ss / d + (double)A.eps);
   const float rinv_f = (float)rinv;
   uint32_t rowmax = 0;
   uint32_t xb[V][4];

@@ -2147,15 +2147,17 @@ extern "C" int e0_int4_linear(const e0_int4_mat *w, const void *x, int x_format,
 
 // Workspace regions of e0_moe_layer_few, 256-byte aligned.
 struct FewSpace {
-  size_t xb, logits, lt, a, bytes;
+  size_t xb, xv, logits, lt, a, a8, bytes;
 };
 static FewSpace few_space(const e0_dims &D, int T) {
   const size_t d = D.d_model, E = D.n_experts, I = D.d_ff, k = D.top_k, r = D.lora_rank;
   FewSpace S{};
   S.xb = S.bytes;     S.bytes += noalloc_align((size_t)T * d * 2);
+  S.xv = S.bytes;     S.bytes += noalloc_align((size_t)T * (d / 64) * 4);
   S.logits = S.bytes; S.bytes += noalloc_align((size_t)T * E * 4);
   S.lt = S.bytes;     S.bytes += noalloc_align((size_t)T * 2 * r * 4);
   S.a = S.bytes;      S.bytes += noalloc_align((size_t)T * (k + 1) * I * 2);
+  S.a8 = S.bytes;     S.bytes += noalloc_align((size_t)T * (k + 1) * (I / 8) * 4);
   return S;
 }
 
@@ -2200,7 +2202,7 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
   A.h_out = (uint16_t *)h_out; A.y = (uint16_t *)y_bf16; A.yf = y_f32; A.idx = idx_out; A.gates = gate_out;
   uint8_t *ws = (uint8_t *)workspace;
   A.xb = (uint16_t *)(ws + S.xb); A.logits = (float *)(ws + S.logits); A.lt = (float *)(ws + S.lt);
-  A.a = (uint16_t *)(ws + S.a);
+  A.a = (uint16_t *)(ws + S.a); A.xv = (float *)(ws + S.xv); A.a8 = (float *)(ws + S.a8);
   A.err = dev_status;
   int dev = 0, nsm = 0, coop = 0, most = 0;
   CK(cudaGetDevice(&dev));
@@ -2208,14 +2210,14 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
   CK(cudaDeviceGetAttribute(&coop, cudaDevAttrCooperativeLaunch, dev));
   CK(cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev));
   if (!coop || nsm < (kFewMaxT + 7) / 8) return fail(E0_ERR_CUDA, "moe_layer_few: the device has no cooperative launch");
-  const int smem = most, area = smem - (int)few_plan_bytes() - kFewRedBytes;
+  const int smem = most, area = smem - (int)few_plan_bytes() - kFewZeroBytes - kFewRedBytes - kFewRingBytes;
   // activation rows that fit the staging area, and so the tokens of a segment
-  const int places = T * (A.k + 1) + std::min(A.E, T * A.k) + 1;
-  A.parts_bytes = std::max(16384, (places * 64 + 127) / 128 * 128);
-  A.gu_rows = area / (A.d / 64 * 136 + kActPad);
-  A.dn_rows = (area - A.parts_bytes) / (A.I / 64 * 136 + kActPad);
+  A.out_bytes = std::max(16384, T * (A.k + 1) * 64);
+  A.gu_rows = area / few_row_bytes(A.d);
+  A.dn_rows = (area - A.out_bytes) / few_row_bytes(A.I);
   const int rows = std::min(A.gu_rows, A.dn_rows);
-  A.seg_cap = rows >= 32 ? 32 : rows >= 16 ? 16 : 8;
+  A.seg_cap = rows >= 16 ? 16 : 8;
+  A.tpb = T <= 8 ? 1 : T <= 16 ? 2 : T <= 32 ? 4 : 8;
   if (rows < 8) return fail(E0_ERR_INVALID_ARG, "moe_layer_few: dims too large for the staging area");
   CK(cudaFuncSetAttribute(k_moe_few, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   void *args[] = {&A};

@@ -7,12 +7,27 @@
 //      [W_r; A_g; A_u] times them (mma.sync m16n8k16 bf16, K split over the warps).
 //   2. every block takes the top-k of all tokens and groups the (token, slot) assignments by
 //      expert into segments of at most `seg_cap` tokens (the shared expert is one more expert
-//      that every token has); it then computes an equal share of the intermediate indices of
-//      all segments: a gate and an up row each, SwiGLU, a = bf16(silu(g) u).
+//      that every token has); it then computes an equal share, by cost, of the tiles of 8
+//      intermediate indices of all segments: 8 gate and 8 up rows, SwiGLU, a = bf16(silu(g) u).
 //   3. every block computes an equal share of the output rows for all segments and combines
 //      them per token in slot order, routed experts first, so y does not depend on timing.
-// Each expert's weights are read once per 32 tokens that chose it (16 or 8 where wide
-// activations leave less shared memory).
+// Each expert's weights are read once per 16 tokens that chose it (8 where wide activations
+// leave less shared memory).
+//
+// A launch with few tokens is a chain of latencies, code fetches among them: the streaming loops
+// exist in three forms for each of the two products and no more, and what they call at the end
+// of a tile is a function.  (724 KB of code with 12 inlined forms took 42 us for 5 tokens of
+// d = 256, most of it waiting for instructions.)
+//
+// Products: bf16 matrix instructions on the activations as they are.  A weight code q is held as
+// the bf16 number 128 + q (0x4300 + q, one mask and one or with the shift that brings its nibble
+// down), so   sum w x = s sum (128 + q) x + (m - 128 s) sum x   per group of 64; the sums of x
+// come with the activations.  The products are exact; the sums carry 128 times the sum of x on
+// top, which costs 4 bits of fp32's 24 where the x of a group agree in sign.  (e0_int4_linear,
+// which may return fp32, uses fp16 operands without that term, and pays for it by bringing the
+// activations to fp16's range; here each block would have to do that for every expert's a.)
+// Rows of x and a are stored with each 8 channels in the order 0 4 1 5 2 6 3 7, so that 16 bytes
+// are the operands that meet one word of codes.
 #pragma once
 #include <cooperative_groups.h>
 #include "e0_addnorm.cuh"
@@ -26,7 +41,7 @@ constexpr int kFewThreads = 512;
 constexpr int kFewWarps = kFewThreads / 32;
 constexpr int kFewMaxA = kFewMaxT * (kMaxK + 1);                // assignments
 constexpr int kFewMaxSeg = kMaxE + 1 + kFewMaxA / 8;            // segments
-constexpr int kFewMaxPos = kFewMaxA + kFewMaxSeg + 1;           // places, each segment padded to even
+constexpr int kFewPad = 16;                                     // bytes between rows: 8 rows in distinct banks
 
 struct FewArgs {
   const uint16_t *h, *delta;
@@ -42,32 +57,40 @@ struct FewArgs {
   int32_t *idx;
   float *gates;
   // workspace
-  uint16_t *xb;               // [T][d]
+  uint16_t *xb;               // [T][d], channels in operand order
+  float *xv;                  // [T][d / 64] sums of x
   float *logits;              // [T][E]
   float *lt;                  // [T][2][r]
-  uint16_t *a;                // [T][k + 1][I]
+  uint16_t *a;                // [T][k + 1][I], channels in operand order
+  float *a8;                  // [T][k + 1][I / 8] sums of a
   int *err;
-  int seg_cap;                // tokens to a segment: 8, 16 or 32
+  int seg_cap;                // tokens to a segment: 8 or 16
+  int tpb;                    // tokens that a block of phase 1 norms
   int gu_rows, dn_rows;       // activation rows that fit the staging area in phases 2 and 3
-  int parts_bytes;            // bytes of the down-projection results in phase 3
+  int out_bytes;              // bytes of the down-projection results in phase 3
 };
 
 struct FewPlan {
+  FewArgs args;                   // a copy that functions read at shared memory's latency
   float gate[kFewMaxT * kMaxK];
-  uint16_t sel[kFewMaxT * kMaxK];
   unsigned long long tok[kMaxE];  // the tokens that chose an expert, one bit each
+  unsigned long long scan[kFewWarps];
+  uint16_t sel[kFewMaxT * kMaxK];
   uint16_t first[kMaxE + 1];      // place of an expert's first assignment
   uint16_t place[kFewMaxA];       // place of assignment t (k + 1) + j
-  int16_t asg[kFewMaxPos];        // assignment at a place, -1 for padding
+  uint16_t asg[kFewMaxA];         // assignment at a place
   uint16_t seg_exp[kFewMaxSeg];
   uint16_t seg_at[kFewMaxSeg + 1];
   uint16_t seg_n[kFewMaxSeg];
-  int nseg, nplace;
+  int cost_at[kFewMaxSeg + 1];    // cost of the segments before one, per tile column
+  int nseg, nplace, n4, n8;       // segments of experts with at most 4 and at most 8 tokens come first
   double part[kFewWarps];
 };
 
 __host__ __device__ inline size_t few_plan_bytes() { return (sizeof(FewPlan) + 127) & ~(size_t)127; }
-constexpr int kFewRedBytes = kFewWarps * 16 * 32 * 4;            // partial sums of 16 warps: 16 rows x 32 tokens
+constexpr int kFewZeroBytes = 128;
+constexpr int kFewRedBytes = kFewWarps * 16 * 16 * 4;            // partial sums of 16 warps: 16 rows x 16 tokens
+__host__ __device__ inline int few_row_bytes(int channels) { return channels * 2 + kFewPad + channels / 64 * 4; }
 
 __device__ __forceinline__ void bar_team(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -81,22 +104,182 @@ __device__ __forceinline__ void mma_bf16_acc(float (&d)[4], uint32_t a0, uint32_
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 bf16 rows times 8 bf16 columns over channels [k0, k1) (multiples of 32): ra, rb the
-// lane's rows l / 4 and l / 4 + 8, x its column, each at channel 8 (l & 3).
-__device__ __forceinline__ void bf16_rows(const uint16_t *ra, const uint16_t *rb, const uint16_t *x, int k0, int k1,
-                                          float (&acc)[4]) {
-#pragma unroll 4
-  for (int k = k0; k < k1; k += 32) {
-    const uint4 a = *reinterpret_cast<const uint4 *>(ra + k), b = *reinterpret_cast<const uint4 *>(rb + k);
-    const uint4 v = *reinterpret_cast<const uint4 *>(x + k);
-    mma_bf16_acc(acc, a.x, b.x, a.y, b.y, v.x, v.y);
-    mma_bf16_acc(acc, a.z, b.z, a.w, b.w, v.z, v.w);
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float lds32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t smem_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// 8 channels 0..7 -> 0 4 1 5 2 6 3 7 and back (pairs of a 16-byte chunk)
+__device__ __forceinline__ uint4 operand_order(uint4 v) {
+  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                    __byte_perm(v.y, v.w, 0x7632));
+}
+__device__ __forceinline__ uint4 natural_order(uint4 v) {
+  return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                    __byte_perm(v.z, v.w, 0x7632));
+}
+
+// 16 bf16 rows times 8 bf16 columns, 32 channels: a, b the lane's rows l / 4 and l / 4 + 8 at
+// channel 8 (l & 3), x its column there.
+__device__ __forceinline__ void bf16_mul(uint4 a, uint4 b, uint4 x, float (&acc)[4]) {
+  mma_bf16_acc(acc, a.x, b.x, a.y, b.y, x.x, x.y);
+  mma_bf16_acc(acc, a.z, b.z, a.w, b.w, x.z, x.w);
+}
+
+// ---------------------------------------------------------------------------------------
+// int4 rows times bf16 columns: 16 rows, blocks of 256 channels (the last may be 128)
+// ---------------------------------------------------------------------------------------
+// Two forms.  Pair: up to 8 tokens as N tiles of 4; the 8 columns of a matrix instruction are 4
+// tokens restricted to one group of 64 and the same 4 restricted to the next, so a lane takes 16
+// consecutive bytes of a row and one fold serves both groups.  Wide: N tiles of 8 tokens, 8 bytes
+// of a row a lane, a fold per group.  The accumulators of a lane are rows l / 4 and l / 4 + 8,
+// tokens 2 (l & 3), + 1 of a tile (pair: tokens 2 (l & 1), + 1, after adding lanes l and l + 2).
+//
+// Each warp streams its weights through a ring of its own in shared memory, a block to a stage, by
+// cp.async: 16 rows of 128 bytes of codes (their 16-byte chunks permuted by row, so that either
+// form reads without bank conflicts), then per row the scales and the mins of 4 groups.
+constexpr int kFewStage = 16 * 128 + 16 * 16;
+constexpr int kFewDepth = 3;
+constexpr int kFewRingBytes = kFewWarps * kFewDepth * kFewStage;
+
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+// chunk c of row r is at chunk c ^ few_swz(r)
+__device__ __forceinline__ int few_swz(int r) { return ((r & 1) << 2) ^ (r & 2); }
+
+// Activation rows in shared memory: bf16 rows `pitch` bytes apart, and their sums by group.
+struct FewOps {
+  uint32_t x, v;              // shared addresses
+  int pitch, vp;              // bytes between rows of x and of v
+};
+
+// A lane's columns: N tiles of tokens (wide: 8 each, pair: 4), n tokens in all, at row `at`.
+template <bool WIDE, int N>
+struct FewCol {
+  uint32_t x[N], v0[N], v1[N];
+  int step;
+  __device__ __forceinline__ void set(const FewOps &O, int at, int n, uint32_t zero) {
+    const int lane = threadIdx.x & 31, t = lane & 3, c = lane >> 2;
+    const bool mine = WIDE || (t >> 1) == (c >> 2);
+    step = mine ? 256 : 0;
+#pragma unroll
+    for (int q = 0; q < N; q++) {
+      const int tok = WIDE ? 8 * q + c : 4 * q + (c & 3), pair = WIDE ? 8 * q + 2 * t : 4 * q + 2 * (t & 1);
+      x[q] = mine ? O.x + (at + min(tok, n - 1)) * O.pitch + (WIDE ? t * 32 : t * 64) : zero;
+      v0[q] = O.v + (at + min(pair, n - 1)) * O.vp + (WIDE ? 0 : (t >> 1) * 4);
+      v1[q] = O.v + (at + min(pair + 1, n - 1)) * O.vp + (WIDE ? 0 : (t >> 1) * 4);
+    }
+  }
+};
+
+// 8 codes of a word as four pairs 128 + q, in operand order
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u; }
+
+// One fold: the sums p of a group (or, pair, of a lane's group of two) with its scale and min.
+// The scale is the low (0x1044) or high (0x3244) half of a word.
+template <int N>
+__device__ __forceinline__ void few_fold(const float (&p)[N][4], uint32_t wsa, uint32_t wma, uint32_t wsb, uint32_t wmb,
+                                         uint32_t sel, const uint32_t (&v0)[N], const uint32_t (&v1)[N], int at,
+                                         Int4Acc<N> &acc) {
+  auto pick = [&](uint32_t w) { return __uint_as_float(__byte_perm(w, 0u, sel)); };
+  const float sa = pick(wsa), sb = pick(wsb), ma = fmaf(-128.f, sa, pick(wma)), mb = fmaf(-128.f, sb, pick(wmb));
+  const unsigned long long sa2 = pk2(sa, sa), ma2 = pk2(ma, ma), sb2 = pk2(sb, sb), mb2 = pk2(mb, mb);
+#pragma unroll
+  for (int q = 0; q < N; q++) {
+    const unsigned long long v = pk2(lds32(v0[q] + at), lds32(v1[q] + at));
+    acc.a[q] = f2fma(sa2, pk2(p[q][0], p[q][1]), f2fma(ma2, v, acc.a[q]));
+    acc.b[q] = f2fma(sb2, pk2(p[q][2], p[q][3]), f2fma(mb2, v, acc.b[q]));
+  }
+}
+
+// Block b, at stage address st, times the columns.  whole: 256 channels, else 128.
+template <bool WIDE, int N>
+__device__ __forceinline__ void few_mul(uint32_t st, int b, bool whole, const FewCol<WIDE, N> &X, Int4Acc<N> &acc) {
+  const int lane = threadIdx.x & 31, t = lane & 3, r = lane >> 2;
+  const uint4 ca = lds128(st + 2048 + r * 16), cb = lds128(st + 2048 + r * 16 + 128);
+  const uint32_t row = st + r * 128, swz = few_swz(r);
+  if (WIDE) {
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      if (g == 2 && !whole) break;
+      const uint32_t at = row + (((2 * g + (t >> 1)) ^ swz) << 4) + (t & 1) * 8;
+      const uint2 wa = lds64(at), wb = lds64(at + 1024);
+      float p[N][4];
+#pragma unroll
+      for (int q = 0; q < N; q++) p[q][0] = p[q][1] = p[q][2] = p[q][3] = 0.f;
+#pragma unroll
+      for (int w = 0; w < 2; w++) {
+        const uint32_t xa = w ? wa.y : wa.x, xb = w ? wb.y : wb.x;
+        const uint32_t a0 = code_pair(xa, 0), a1 = code_pair(xa, 1), a2 = code_pair(xa, 2), a3 = code_pair(xa, 3);
+        const uint32_t b0 = code_pair(xb, 0), b1 = code_pair(xb, 1), b2 = code_pair(xb, 2), b3 = code_pair(xb, 3);
+#pragma unroll
+        for (int q = 0; q < N; q++) {
+          const uint4 x = lds128(X.x[q] + b * 512 + g * 128 + w * 16);
+          mma_bf16_acc(p[q], a0, b0, a1, b1, x.x, x.y);
+          mma_bf16_acc(p[q], a2, b2, a3, b3, x.z, x.w);
+        }
+      }
+      few_fold<N>(p, g < 2 ? ca.x : ca.y, g < 2 ? ca.z : ca.w, g < 2 ? cb.x : cb.y, g < 2 ? cb.z : cb.w,
+                  g & 1 ? 0x3244u : 0x1044u, X.v0, X.v1, (4 * b + g) * 4, acc);
+    }
+  } else {
+    const uint32_t sel = t >> 1 ? 0x3244u : 0x1044u;
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      if (j == 1 && !whole) break;
+      const uint32_t at = row + (((4 * j + t) ^ swz) << 4);
+      const uint4 wa = lds128(at), wb = lds128(at + 1024);
+      // two chains of matrix instructions, joined at the fold
+      float p[N][4], p2[N][4];
+#pragma unroll
+      for (int q = 0; q < N; q++) p[q][0] = p[q][1] = p[q][2] = p[q][3] = p2[q][0] = p2[q][1] = p2[q][2] = p2[q][3] = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; w++) {
+        const uint32_t xa = w == 0 ? wa.x : w == 1 ? wa.y : w == 2 ? wa.z : wa.w;
+        const uint32_t xb = w == 0 ? wb.x : w == 1 ? wb.y : w == 2 ? wb.z : wb.w;
+        const uint32_t a0 = code_pair(xa, 0), a1 = code_pair(xa, 1), a2 = code_pair(xa, 2), a3 = code_pair(xa, 3);
+        const uint32_t b0 = code_pair(xb, 0), b1 = code_pair(xb, 1), b2 = code_pair(xb, 2), b3 = code_pair(xb, 3);
+#pragma unroll
+        for (int q = 0; q < N; q++) {
+          const uint4 x = lds128(X.x[q] + (2 * b + j) * X.step + w * 16);
+          mma_bf16_acc(p[q], a0, b0, a1, b1, x.x, x.y);
+          mma_bf16_acc(p2[q], a2, b2, a3, b3, x.z, x.w);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < N; q++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) p[q][i] += p2[q][i];
+      few_fold<N>(p, j ? ca.y : ca.x, j ? ca.w : ca.z, j ? cb.y : cb.x, j ? cb.w : cb.z, sel, X.v0, X.v1, (4 * b + 2 * j) * 4,
+                  acc);
+    }
   }
 }
 
 // Top-k of E <= 256 logits over a warp, descending, equal values by lower index; a NaN counts
-// as the lowest value, so every index is valid.
-__device__ __forceinline__ void few_topk(const float *v, int E, int k, int lane, int *out) {
+// as the lowest value, so every index is valid.  Lane j < k gets the j-th.
+__device__ __forceinline__ int few_topk(const float *v, int E, int k, int lane) {
   float vals[kMaxE / 32];
   unsigned left = 0;
 #pragma unroll
@@ -109,9 +292,9 @@ __device__ __forceinline__ void few_topk(const float *v, int E, int k, int lane,
       left |= 1u << i;
     }
   }
-#pragma unroll
-  for (int s = 0; s < kMaxK; s++) {
-    if (s >= k) break;
+  int mine = 0;
+#pragma unroll 1
+  for (int s = 0; s < k; s++) {
     float bv = -INFINITY;
     int be = 0x7fffffff;
 #pragma unroll
@@ -129,92 +312,136 @@ __device__ __forceinline__ void few_topk(const float *v, int E, int k, int lane,
         be = oe;
       }
     }
-    out[s] = be;
+    if (lane == s) mine = be;
     if ((be & 31) == lane) left &= ~(1u << (be >> 5));
   }
+  return mine;
 }
 
-// Phase 1: the block's 8 tokens (8 tb ..) normed into xs, then its rows.
-__device__ __forceinline__ void few_phase1(const FewArgs &A, FewPlan &P, uint8_t *area, float *red) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int ntb = (A.T + 7) / 8, tb = blockIdx.x % ntb, member = blockIdx.x / ntb;
-  const int members = ((int)gridDim.x - tb + ntb - 1) / ntb;
-  const int t0 = tb * 8, nt = min(8, A.T - t0), d = A.d;
-  uint16_t *xs = reinterpret_cast<uint16_t *>(area);
-  const int pitch = d + kActPad / 2;
-  // 16 warps over nt tokens, 2 to 16 warps each
-  const int wpt = nt > 4 ? 2 : nt > 2 ? 4 : nt > 1 ? 8 : 16, tok = warp / wpt, sub = warp % wpt;
-  const bool mine = tok < nt;
-  const uint16_t *h = A.h + (size_t)(t0 + tok) * d, *dl = A.delta ? A.delta + (size_t)(t0 + tok) * d : nullptr;
-  auto load8 = [&](int c, float *v) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(h + c);
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; j++) {
-      v[2 * j] = __uint_as_float(ws[j] << 16);
-      v[2 * j + 1] = __uint_as_float(ws[j] & 0xFFFF0000u);
-    }
-  };
-  double ss = 0.0;
-  if (mine)
-    for (int c = (sub * 32 + lane) * 8; c < d; c += wpt * 256) {
-      float v[8];
-      load8(c, v);
-      if (dl) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(dl + c);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-          v[j] = bf(add_bf16(v[j], __uint_as_float(j & 1 ? ws[j >> 1] & 0xFFFF0000u : ws[j >> 1] << 16)));
-      }
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; j++) o[j] = (__float_as_uint(v[2 * j]) >> 16) | (__float_as_uint(v[2 * j + 1]) & 0xFFFF0000u);
-      const uint4 hv = make_uint4(o[0], o[1], o[2], o[3]);
-      *reinterpret_cast<uint4 *>(xs + (size_t)tok * pitch + c) = hv;
-#pragma unroll
-      for (int j = 0; j < 8; j++) ss = fma((double)v[j], (double)v[j], ss);
-    }
-  ss = warp_sum(ss);
-  if (lane == 0) P.part[warp] = ss;
-  __syncthreads();
-  if (mine) {
-    ss = 0.0;
-    for (int w = 0; w < wpt; w++) ss += P.part[tok * wpt + w];
-    const double rinv = 1.0 / sqrt(ss / d + (double)A.eps);
-    const float rinv_f = (float)rinv;
-    for (int c = (sub * 32 + lane) * 8; c < d; c += wpt * 256) {
-      uint4 *at = reinterpret_cast<uint4 *>(xs + (size_t)tok * pitch + c);
-      const uint4 w = *at, g = __ldg(reinterpret_cast<const uint4 *>(A.gamma + c));
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w}, gs[4] = {g.x, g.y, g.z, g.w};
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const uint32_t b0 = norm_bf16(__uint_as_float(ws[j] << 16), __uint_as_float(gs[j] << 16), rinv, rinv_f);
-        const uint32_t b1 = norm_bf16(__uint_as_float(ws[j] & 0xFFFF0000u), __uint_as_float(gs[j] & 0xFFFF0000u), rinv, rinv_f);
-        o[j] = b0 | (b1 << 16);
-      }
-      const uint4 xv = make_uint4(o[0], o[1], o[2], o[3]);
-      *at = xv;
-      if (member == 0) *reinterpret_cast<uint4 *>(A.xb + (size_t)(t0 + tok) * d + c) = xv;
-    }
+// ---------------------------------------------------------------------------------------
+// Phase 1
+// ---------------------------------------------------------------------------------------
+// The block's tokens (at most 8) normed into rows at `area` (operand order) with their sums, h'
+// behind them, then the block's rows of [router; A_g; A_u].  Every block of the same tokens norms
+// them again, which costs less than a grid-wide barrier; so a block has few tokens, and more rows,
+// as long as there are blocks (`tpb` is T / 8, rounded up to a power of two).
+struct FewTok {
+  int ntb, tb, member, members, t0, nt;
+  __device__ __forceinline__ explicit FewTok(const FewArgs &A) {
+    ntb = (A.T + A.tpb - 1) / A.tpb;
+    tb = blockIdx.x % ntb;
+    member = blockIdx.x / ntb;
+    members = ((int)gridDim.x - tb + ntb - 1) / ntb;
+    t0 = tb * A.tpb;
+    nt = min(A.tpb, A.T - t0);
   }
-  __syncthreads();
-  // rows [router; A_g; A_u] of this member
+};
+__device__ __forceinline__ void few_phase1(const FewArgs &A, FewPlan &P, uint8_t *area, float *red) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, d = A.d;
+  const FewTok K(A);
+  const int pitch = d * 2 + kFewPad, vbytes = d / 64 * 4;
+  uint8_t *hs = area + 8 * (pitch + vbytes);
+  // the first 16 rows are fetched before they are needed: 4 chunks of 32 channels a warp
   const int R = A.E + (A.Ag ? 2 * A.r : 0);
-  const int r0 = (int)((long long)R * member / members), r1 = (int)((long long)R * (member + 1) / members);
+  const int r0 = (int)((long long)R * K.member / K.members), r1 = (int)((long long)R * (K.member + 1) / K.members);
   auto row_ptr = [&](int row) -> const uint16_t * {
     if (row < A.E) return A.router + (size_t)row * d;
     row -= A.E;
     return row < A.r ? A.Ag + (size_t)row * d : A.Au + (size_t)(row - A.r) * d;
   };
-  const int nb = d / 32, k0 = nb * warp / kFewWarps * 32, k1 = nb * (warp + 1) / kFewWarps * 32;
-  const uint16_t *x = xs + (size_t)min(lane >> 2, nt - 1) * pitch + (lane & 3) * 8;
-  for (int q = r0; q < r1; q += 16) {
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  const int nb = d / 32, b0 = nb * warp / kFewWarps, b1 = nb * (warp + 1) / kFewWarps;
+  constexpr int PRE = 4;
+  uint4 wa[PRE], wb[PRE];
+  auto fetch = [&](int q, int b) {
     const uint16_t *ra = row_ptr(min(q + (lane >> 2), r1 - 1)) + (lane & 3) * 8;
     const uint16_t *rb = row_ptr(min(q + (lane >> 2) + 8, r1 - 1)) + (lane & 3) * 8;
-    bf16_rows(ra, rb, x, k0, k1, acc);
+    // rows past the share are not fetched: they would be the last row again
+    const bool two = q + 8 < r1;
+#pragma unroll
+    for (int i = 0; i < PRE; i++) {
+      wa[i] = wb[i] = make_uint4(0, 0, 0, 0);
+      if (b + i < b1) {
+        wa[i] = __ldg(reinterpret_cast<const uint4 *>(ra + (b + i) * 32));
+        if (two) wb[i] = __ldg(reinterpret_cast<const uint4 *>(rb + (b + i) * 32));
+      }
+    }
+  };
+  if (r0 < r1) fetch(r0, b0);
+  // 16 warps over nt tokens, 2 to 16 warps each
+  const int wpt = K.nt > 4 ? 2 : K.nt > 2 ? 4 : K.nt > 1 ? 8 : 16, tok = warp / wpt, sub = warp % wpt;
+  const bool mine = tok < K.nt;
+  uint8_t *xs = area + tok * pitch;
+  const int c0 = (sub * 32 + lane) * 8, cl = min(c0, d - 8);
+  uint4 gm = __ldg(reinterpret_cast<const uint4 *>(A.gamma + cl));
+  double ss = 0.0;
+  if (mine) {
+    const uint16_t *h = A.h + (size_t)(K.t0 + tok) * d, *dl = A.delta ? A.delta + (size_t)(K.t0 + tok) * d : nullptr;
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    uint4 hv = *reinterpret_cast<const uint4 *>(h + cl), dv = dl ? *reinterpret_cast<const uint4 *>(dl + cl) : none;
+#pragma unroll 1
+    for (int c = c0; c < d; c += wpt * 256) {
+      uint32_t ws[4] = {hv.x, hv.y, hv.z, hv.w};
+      const uint32_t es[4] = {dv.x, dv.y, dv.z, dv.w};
+      const int cn = min(c + wpt * 256, d - 8);     // the next, while this one is worked on
+      hv = *reinterpret_cast<const uint4 *>(h + cn);
+      if (dl) dv = *reinterpret_cast<const uint4 *>(dl + cn);
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        if (dl)
+          ws[j] = add_bf16(__uint_as_float(ws[j] << 16), __uint_as_float(es[j] << 16)) |
+                  (uint32_t)add_bf16(__uint_as_float(ws[j] & 0xFFFF0000u), __uint_as_float(es[j] & 0xFFFF0000u)) << 16;
+        const double lo = (double)__uint_as_float(ws[j] << 16), hi = (double)__uint_as_float(ws[j] & 0xFFFF0000u);
+        ss = fma(lo, lo, fma(hi, hi, ss));
+      }
+      *reinterpret_cast<uint4 *>(xs + c * 2) = make_uint4(ws[0], ws[1], ws[2], ws[3]);
+    }
+  }
+  ss = warp_sum(ss);
+  if (lane == 0) P.part[warp] = ss;
+  __syncthreads();
+  if (mine) {
+    ss = 0.0;
+#pragma unroll 2
+    for (int w = 0; w < wpt; w++) ss += P.part[tok * wpt + w];
+    const double rinv = rsqrt(ss / d + (double)A.eps);
+    const float rinv_f = (float)rinv;
+#pragma unroll 1
+    for (int c = c0; c < d; c += wpt * 256) {
+      const uint4 w = *reinterpret_cast<const uint4 *>(xs + c * 2);
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w}, gs[4] = {gm.x, gm.y, gm.z, gm.w};
+      gm = __ldg(reinterpret_cast<const uint4 *>(A.gamma + min(c + wpt * 256, d - 8)));
+      uint32_t o[4];
+      float v = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const uint32_t e0 = norm_bf16(__uint_as_float(ws[j] << 16), __uint_as_float(gs[j] << 16), rinv, rinv_f);
+        const uint32_t e1 = norm_bf16(__uint_as_float(ws[j] & 0xFFFF0000u), __uint_as_float(gs[j] & 0xFFFF0000u), rinv, rinv_f);
+        o[j] = e0 | (e1 << 16);
+        v += bf(e0) + bf(e1);
+      }
+      v = group_sum(v, 8);                          // d is a multiple of 256: whole warps
+      const uint4 xv = operand_order(make_uint4(o[0], o[1], o[2], o[3]));
+      *reinterpret_cast<uint4 *>(xs + c * 2) = xv;
+      if ((lane & 7) == 0) *reinterpret_cast<float *>(area + 8 * pitch + tok * vbytes + c / 64 * 4) = v;
+      if (K.member == 0) {
+        *reinterpret_cast<uint4 *>(A.xb + (size_t)(K.t0 + tok) * d + c) = xv;
+        if ((lane & 7) == 0) A.xv[(size_t)(K.t0 + tok) * (d / 64) + c / 64] = v;
+        if (A.h_out) *reinterpret_cast<uint4 *>(hs + ((size_t)tok * d + c) * 2) = w;
+      }
+    }
+  }
+  __syncthreads();
+  const uint32_t x = smem_at(area) + min(lane >> 2, K.nt - 1) * pitch + (lane & 3) * 16;
+#pragma unroll 1
+  for (int q = r0; q < r1; q += 16) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int b = b0; b < b1; b += PRE) {
+      if (q != r0 || b != b0) fetch(q, b);
+#pragma unroll
+      for (int i = 0; i < PRE; i++)
+        if (b + i < b1) bf16_mul(wa[i], wb[i], natural_order(lds128(x + (b + i) * 64)), acc);
+    }
     float *p = red + warp * 128 + (lane >> 2) * 8 + 2 * (lane & 3);
     p[0] = acc[0];
     p[1] = acc[1];
@@ -223,367 +450,522 @@ __device__ __forceinline__ void few_phase1(const FewArgs &A, FewPlan &P, uint8_t
     __syncthreads();
     if (tid < 128) {
       const int row = q + (tid >> 3), tk = tid & 7;
-      if (row < r1 && tk < nt) {
+      if (row < r1 && tk < K.nt) {
         float s = 0.f;
+#pragma unroll
         for (int w = 0; w < kFewWarps; w++) s += red[w * 128 + tid];
         if (row < A.E)
-          A.logits[(size_t)(t0 + tk) * A.E + row] = s;
+          A.logits[(size_t)(K.t0 + tk) * A.E + row] = s;
         else
-          A.lt[(size_t)(t0 + tk) * 2 * A.r + (row - A.E)] = s;
+          A.lt[(size_t)(K.t0 + tk) * 2 * A.r + (row - A.E)] = s;
       }
     }
     __syncthreads();
   }
 }
 
-// h' = bf16(h + delta) to h_out, after every block has read h (h_out may be h).
-__device__ __forceinline__ void few_residual(const FewArgs &A) {
-  const size_t n = (size_t)A.T * A.d;
-  for (size_t c = ((size_t)blockIdx.x * kFewThreads + threadIdx.x) * 8; c < n; c += (size_t)gridDim.x * kFewThreads * 8) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(A.h + c);
-    uint4 o = w;
-    if (A.delta) {
-      const uint4 e = *reinterpret_cast<const uint4 *>(A.delta + c);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w}, es[4] = {e.x, e.y, e.z, e.w};
-      uint32_t os[4];
-#pragma unroll
-      for (int j = 0; j < 4; j++)
-        os[j] = add_bf16(__uint_as_float(ws[j] << 16), __uint_as_float(es[j] << 16)) |
-                (uint32_t)add_bf16(__uint_as_float(ws[j] & 0xFFFF0000u), __uint_as_float(es[j] & 0xFFFF0000u)) << 16;
-      o = make_uint4(os[0], os[1], os[2], os[3]);
-    }
-    *reinterpret_cast<uint4 *>(A.h_out + c) = o;
-  }
+// h' of the block's tokens to h_out, after every block has read h (h_out may be h).
+__device__ __forceinline__ void few_residual(const FewArgs &A, const uint8_t *area) {
+  const FewTok K(A);
+  if (K.member) return;
+  const uint8_t *hs = area + 8 * (A.d * 2 + kFewPad + A.d / 64 * 4);
+#pragma unroll 1
+  for (int c = threadIdx.x * 8; c < K.nt * A.d; c += kFewThreads * 8)
+    *reinterpret_cast<uint4 *>(A.h_out + (size_t)K.t0 * A.d + c) = *reinterpret_cast<const uint4 *>(hs + c * 2);
 }
 
-// Routing of every token and the segments of (token, slot) assignments by expert.
+// ---------------------------------------------------------------------------------------
+// Routing of every token and the segments of (token, slot) assignments by expert
+// ---------------------------------------------------------------------------------------
+// Relative cost of a tile of a segment with n tokens in phase 2 (the weights bound the first).
+__device__ __forceinline__ int few_cost(int n) { return n <= 8 ? 4 : 6; }
+
 __device__ __forceinline__ void few_plan(const FewArgs &A, FewPlan &P) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int k = A.k, T = A.T, E = A.E;
-  for (int e = tid; e < kMaxE; e += kFewThreads) P.tok[e] = 0;
+  if (tid < kMaxE) P.tok[tid] = 0;
+#pragma unroll 1
   for (int t = warp; t < T; t += kFewWarps) {
     const float *lg = A.logits + (size_t)t * E;
-    int sel[kMaxK];
-    const bool own = A.route == nullptr || A.route[(size_t)t * k] < 0;
-    int bad = 0;
-    if (own) {
-      few_topk(lg, E, k, lane, sel);
+    // lane j < k has the token's j-th expert
+    int e = 0, bad = 0;
+    if (A.route != nullptr && lane < k) e = A.route[(size_t)t * k + lane];
+    if (A.route == nullptr || __shfl_sync(0xffffffffu, e, 0) < 0) {
+      e = few_topk(lg, E, k, lane);
     } else {
-#pragma unroll
-      for (int j = 0; j < kMaxK; j++) {
-        if (j >= k) break;
-        int e = A.route[(size_t)t * k + j];
-        if (e < 0 || e >= E) {
-          bad |= DERR_INDEX;
-          e = 0;
-        }
-        sel[j] = e;
+      if (e < 0 || e >= E) {
+        bad = DERR_INDEX;
+        e = 0;
       }
-#pragma unroll
-      for (int j = 0; j < kMaxK; j++)
-#pragma unroll
-        for (int q = 0; q < j; q++)
-          if (j < k && sel[j] == sel[q]) bad |= DERR_DUP;
+      const unsigned same = __match_any_sync(0xffffffffu, lane < k ? e : -1 - lane);
+      if (same & (same - 1)) bad |= DERR_DUP;
     }
-    float ex[kMaxK], mx = -INFINITY, sum = 0.f;
+    const float l = lane < k ? lg[e] : -INFINITY;
+    float mx = l;
 #pragma unroll
-    for (int j = 0; j < kMaxK; j++) {
-      if (j >= k) break;
-      ex[j] = lg[sel[j]];
-      mx = fmaxf(mx, ex[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < kMaxK; j++) {
-      if (j >= k) break;
-      ex[j] = expf(ex[j] - mx);
-      sum += ex[j];
-    }
-#pragma unroll
-    for (int j = 0; j < kMaxK; j++) {
-      if (j >= k || lane != j) continue;
-      const float g = ex[j] / sum;
-      P.sel[t * k + j] = (uint16_t)sel[j];
-      P.gate[t * k + j] = g;
+    for (int o = kMaxK / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float ex = lane < k ? expf(l - mx) : 0.f, g = ex / group_sum(ex, kMaxK);
+    if (lane < k) {
+      P.sel[t * k + lane] = (uint16_t)e;
+      P.gate[t * k + lane] = g;
       if (blockIdx.x == 0) {
-        if (A.idx) A.idx[(size_t)t * k + j] = sel[j];
-        if (A.gates) A.gates[(size_t)t * k + j] = g;
+        if (A.idx) A.idx[(size_t)t * k + lane] = e;
+        if (A.gates) A.gates[(size_t)t * k + lane] = g;
+        if (bad && A.err) atomicOr(A.err, bad);
       }
     }
-    if (bad && lane == 0 && blockIdx.x == 0 && A.err) atomicOr(A.err, bad);
   }
   __syncthreads();
   // The rank of a token among those of its expert is a count of bits, so every block comes to
   // the same segments (an expert with more tokens than a segment holds has several, which
   // different blocks work on).
-  for (int i = tid; i < T * k; i += kFewThreads) atomicOr(&P.tok[P.sel[i]], 1ull << (i / k));
+  static_assert(kFewMaxT * kMaxK <= kFewThreads && kMaxE < kFewThreads, "an assignment, an expert a thread");
+  if (tid < T * k) atomicOr(&P.tok[P.sel[tid]], 1ull << (tid / k));
   __syncthreads();
-  if (warp == 0) {
-    // places (each segment padded to even) and segments: prefix sums over the experts
-    int place = 0, seg = 0;
-    for (int e0 = 0; e0 <= E; e0 += 32) {
-      const int e = e0 + lane, n = e < E ? __popcll(P.tok[e]) : e == E ? T : 0;
-      const int ns = (n + A.seg_cap - 1) / A.seg_cap, np = (n + 1) & ~1;
-      int ps = np, ss = ns;
+  // Places and segments by one prefix sum over the experts, a thread each: experts of at most 4
+  // tokens first, then up to 8, then the others.  A class takes 20 bits: 10 of places, 10 of
+  // segments (at most 576 and 329).
+  const int n = tid < E ? __popcll(P.tok[tid]) : tid == E ? T : 0, cls = n <= 4 ? 0 : n <= 8 ? 1 : 2;
+  const int ns = (n + A.seg_cap - 1) / A.seg_cap;
+  const unsigned long long own = (unsigned long long)(n | (ns << 10)) << (20 * cls);
+  unsigned long long sum = own;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, ps, o), b = __shfl_up_sync(0xffffffffu, ss, o);
-        if (lane >= o) {
-          ps += a;
-          ss += b;
-        }
-      }
-      const int at = place + ps - np, sg = seg + ss - ns;
-      if (e <= E) P.first[e] = (uint16_t)at;
-      for (int i = 0; i < ns; i++) {
-        P.seg_exp[sg + i] = (uint16_t)e;
-        P.seg_at[sg + i] = (uint16_t)(at + i * A.seg_cap);
-        P.seg_n[sg + i] = (uint16_t)min(A.seg_cap, n - i * A.seg_cap);
-      }
-      if (n & 1) P.asg[at + n] = -1;
-      place += __shfl_sync(0xffffffffu, ps, 31);
-      seg += __shfl_sync(0xffffffffu, ss, 31);
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  if (lane == 31) P.scan[warp] = sum;
+  __syncthreads();
+  unsigned long long total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kFewWarps; w++) {
+    if (w == warp) before = total;
+    total += P.scan[w];
+  }
+  before += sum - own;
+  auto places = [](unsigned long long v, int c) { return (int)(v >> (20 * c)) & 1023; };
+  auto segs = [](unsigned long long v, int c) { return (int)(v >> (20 * c + 10)) & 1023; };
+  int at = places(before, cls), sg = segs(before, cls);
+#pragma unroll
+  for (int c = 0; c < 2; c++)
+    if (c < cls) {
+      at += places(total, c);
+      sg += segs(total, c);
     }
-    if (lane == 0) {
-      P.nseg = seg;
-      P.nplace = place;
-      P.seg_at[seg] = (uint16_t)place;
-    }
+  if (n > 0) P.first[tid] = (uint16_t)at;
+#pragma unroll 1
+  for (int i = 0; i < ns; i++) {
+    P.seg_exp[sg + i] = (uint16_t)tid;
+    P.seg_at[sg + i] = (uint16_t)(at + i * A.seg_cap);
+    P.seg_n[sg + i] = (uint16_t)min(A.seg_cap, n - i * A.seg_cap);
+  }
+  const int n4 = segs(total, 0), n8 = n4 + segs(total, 1), nseg = n8 + segs(total, 2);
+  if (tid == 0) {
+    P.n4 = n4;
+    P.n8 = n8;
+    P.nseg = nseg;
+    P.nplace = T * k + T;
   }
   __syncthreads();
+  if (tid == 0) {
+    P.nplace = P.seg_at[nseg - 1] + P.seg_n[nseg - 1];   // an expert given twice to a token has one place
+    P.seg_at[nseg] = (uint16_t)P.nplace;
+    int c = n8 * few_cost(8);
+#pragma unroll 1
+    for (int s = n8; s < nseg; s++) {
+      P.cost_at[s] = c;
+      c += few_cost(P.seg_n[s]);
+    }
+    P.cost_at[nseg] = c;
+  }
+  if (tid < n8) P.cost_at[tid] = tid * few_cost(8);
+#pragma unroll 1
   for (int i = tid; i < T * (k + 1); i += kFewThreads) {
     const int t = i / (k + 1), j = i % (k + 1);
     const int e = j < k ? P.sel[t * k + j] : E;
-    const int at = P.first[e] + (j < k ? __popcll(P.tok[e] & ((1ull << t) - 1)) : t);
-    P.place[i] = (uint16_t)at;
+    const int to = P.first[e] + (j < k ? __popcll(P.tok[e] & ((1ull << t) - 1)) : t);
+    P.place[i] = (uint16_t)to;
     // an expert given twice to a token (reported above) is computed once
     bool again = false;
+#pragma unroll 1
     for (int q = 0; q < j && j < k; q++) again |= P.sel[t * k + q] == e;
-    if (!again) P.asg[at] = (int16_t)i;
+    if (!again) P.asg[to] = (uint16_t)i;
   }
   __syncthreads();
 }
 
-// Brings the bf16 rows of the assignments at places [p0, p1) into the staging area as matrix
-// operands; src(assignment) is a row of 64 G channels.
-template <class F>
-__device__ __forceinline__ ActDst few_stage(const FewPlan &P, int p0, int p1, int G, uint8_t *area, F src) {
-  const int n = p1 - p0, pitch = act_pitch(G);
-  ActDst D{area, reinterpret_cast<float *>(area + (size_t)n * pitch), pitch, (n + 1) / 2};
-  const int i = threadIdx.x & 7;
-  for (int u0 = 0; u0 < n * G; u0 += kFewThreads / 8) {
-    const int u = u0 + (int)threadIdx.x / 8;
-    const bool in = u < n * G;
-    const int row = in ? u / G : 0, g = in ? u % G : 0, asg = P.asg[p0 + row];
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (in && asg >= 0) w = *reinterpret_cast<const uint4 *>(src(asg) + g * 64 + i * 8);
-    act_group_bf16(w, i, row, g, D, in);
-  }
-  return D;
-}
-
-// One team's tile of phase 2: 8 intermediate indices i0.. (n8 of them) of a segment.
-template <int NT>
-__device__ __forceinline__ void few_gate_up(const FewArgs &A, const FewPlan &P, const ActDst &D, int p0, int seg, int i0,
-                                            int n8, int team, int wk, float *red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % wk;
-  const int G = A.d / 64, e = P.seg_exp[seg], n = P.seg_n[seg], at = P.seg_at[seg] - p0;
-  const uint8_t *blob = e < A.E ? A.experts + (long long)e * A.bl.bytes : A.shared;
-  const int row = i0 + min(lane >> 2, n8 - 1);
-  const Int4Row ra{blob + A.bl.gc + (size_t)row * (A.d / 2) + (lane & 3) * 8,
-                   reinterpret_cast<const uint16_t *>(blob + A.bl.gs) + (size_t)row * G,
-                   reinterpret_cast<const uint16_t *>(blob + A.bl.gm) + (size_t)row * G};
-  const Int4Row rb{blob + A.bl.uc + (size_t)row * (A.d / 2) + (lane & 3) * 8,
-                   reinterpret_cast<const uint16_t *>(blob + A.bl.us) + (size_t)row * G,
-                   reinterpret_cast<const uint16_t *>(blob + A.bl.um) + (size_t)row * G};
-  const uint8_t *col[NT], *sv[NT];
-#pragma unroll
-  for (int q = 0; q < NT; q++) {
-    col[q] = D.op + (size_t)(at + min(8 * q + (lane >> 2), n - 1)) * D.pitch + (lane & 3) * 16;
-    sv[q] = reinterpret_cast<const uint8_t *>(D.sv) + (at / 2 + min(4 * q + (lane & 3), (n - 1) / 2)) * 16;
-  }
-  Int4Acc<NT> acc;
-  acc.clear();
-  int4_rows<NT>(ra, rb, G * sub / wk, G * (sub + 1) / wk, 0, col, sv, D.pairs * 16, acc);
-  float *mine = red + warp * 16 * 32;
-#pragma unroll
-  for (int q = 0; q < NT; q++) {
-    float *p = mine + (lane >> 2) * 32 + 8 * q + 2 * (lane & 3);
-    *reinterpret_cast<unsigned long long *>(p) = acc.a[q];
-    *reinterpret_cast<unsigned long long *>(p + 8 * 32) = acc.b[q];
-  }
-  if (wk > 1) bar_team(1 + team, wk * 32); else __syncwarp();
-  const float *base = red + team * wk * 16 * 32;
-  for (int o = sub * 32 + lane; o < 8 * n; o += wk * 32) {
-    const int q = o & 7, tok = o >> 3;
-    if (q >= n8) continue;
-    float g = 0.f, u = 0.f;
-    for (int w = 0; w < wk; w++) {
-      g += base[w * 16 * 32 + q * 32 + tok];
-      u += base[w * 16 * 32 + (8 + q) * 32 + tok];
-    }
-    g *= kActUnit;
-    u *= kActUnit;
-    const int asg = P.asg[P.seg_at[seg] + tok], i = i0 + q;
-    if (e == A.E && A.Ag) {
-      const float *lt = A.lt + (size_t)(asg / (A.k + 1)) * 2 * A.r;
-      float lg = 0.f, lu = 0.f;
-      for (int j = 0; j < A.r; j++) {
-        lg = fmaf(bf(A.Bg[(size_t)i * A.r + j]), lt[j], lg);
-        lu = fmaf(bf(A.Bu[(size_t)i * A.r + j]), lt[A.r + j], lu);
-      }
-      g = fmaf(A.c, lg, g);
-      u = fmaf(A.c, lu, u);
-    }
-    A.a[(size_t)asg * A.I + i] = f2bf(g / (1.0f + expf(-g)) * u);
-  }
-  if (wk > 1) bar_team(1 + team, wk * 32); else __syncwarp();
-}
-
-// Phase 2: this block's share of all (segment, intermediate index) units.
-__device__ __forceinline__ void few_phase2(const FewArgs &A, const FewPlan &P, uint8_t *area, float *red) {
-  const int warp = threadIdx.x >> 5, I = A.I, G = A.d / 64;
-  const long long units = (long long)P.nseg * I;
-  const int lo = (int)(units * blockIdx.x / gridDim.x), hi = (int)(units * (blockIdx.x + 1) / gridDim.x);
-  for (int s0 = lo / I; s0 * I < hi && lo < hi;) {
-    int s1 = s0 + 1;
-    while (s1 * I < hi && P.seg_at[s1 + 1] - P.seg_at[s0] <= A.gu_rows) s1++;
-    const int p0 = P.seg_at[s0], p1 = P.seg_at[s1];
-    __syncthreads();
-    const uint16_t *xb = A.xb;
-    const int k1 = A.k + 1, d = A.d;
-    const ActDst D = few_stage(P, p0, p1, G, area, [=](int asg) { return xb + (size_t)(asg / k1) * d; });
-    __syncthreads();
-    int tiles = 0;
-    for (int s = s0; s < s1; s++) tiles += (min(hi, (s + 1) * I) - max(lo, s * I) + 7) / 8;
-    // warps to a tile (K split): all of them where there are few tiles
-    const int wk = tiles <= 1 ? 16 : tiles <= 2 ? 8 : tiles <= 4 ? 4 : tiles <= 8 ? 2 : 4;
-    const int team = warp / wk, teams = kFewWarps / wk;
-    int s = s0, base = 0;
-    for (int q = team; q < tiles; q += teams) {
-      int i0, i1;
-      for (;;) {
-        i0 = max(lo, s * I) - s * I;
-        i1 = min(hi, (s + 1) * I) - s * I;
-        const int nq = (i1 - i0 + 7) / 8;
-        if (q < base + nq) break;
-        base += nq;
+// ---------------------------------------------------------------------------------------
+// Streaming
+// ---------------------------------------------------------------------------------------
+// The tiles of a warp (or of a team of wk warps that split K): gate/up, every `step`th of a list
+// of tiles of 8 indices, `per` to a segment; down, every `step`th segment.
+template <bool GU>
+struct FewCursor {
+  int s, i, left;                 // segment, tile of it, tiles left
+  __device__ __forceinline__ void next(int step, int per) {
+    left--;
+    if (GU) {
+      i += step;
+#pragma unroll 1
+      while (i >= per) {
+        i -= per;
         s++;
       }
-      const int i = i0 + (q - base) * 8, n8 = min(8, i1 - i), n = P.seg_n[s];
-      if (n <= 8)
-        few_gate_up<1>(A, P, D, p0, s, i, n8, team, wk, red);
-      else if (n <= 16)
-        few_gate_up<2>(A, P, D, p0, s, i, n8, team, wk, red);
-      else
-        few_gate_up<4>(A, P, D, p0, s, i, n8, team, wk, red);
+    } else {
+      s += step;
     }
+  }
+};
+
+struct FewPart {                  // what a warp does of K, and where its team stands
+  int b0, b1, wk, team, sub, part;
+};
+
+// SwiGLU of one token (a lane's index l / 4 of tile i8 of segment s), with the shared expert's
+// LoRA; a to the workspace in operand order, and the sum of the tile's 8.
+__device__ __noinline__ void few_emit(const FewPlan &P, int s, int i8, int tok, float g, float u) {
+  const FewArgs &A = P.args;
+  const int q = (int)(threadIdx.x & 31) >> 2, n = P.seg_n[s], i = i8 * 8 + q;
+  const int asg = P.asg[P.seg_at[s] + min(tok, n - 1)];
+  if (P.seg_exp[s] == A.E && A.Ag) {
+    const float *lt = A.lt + (size_t)(asg / (A.k + 1)) * 2 * A.r;
+    const uint16_t *bg = A.Bg + (size_t)i * A.r, *bu = A.Bu + (size_t)i * A.r;
+    float lg = 0.f, lu = 0.f;
+#pragma unroll 8
+    for (int j = 0; j < A.r; j++) {
+      lg = fmaf(bf(bg[j]), lt[j], lg);
+      lu = fmaf(bf(bu[j]), lt[A.r + j], lu);
+    }
+    g = fmaf(A.c, lg, g);
+    u = fmaf(A.c, lu, u);
+  }
+  const uint32_t bits = f2bf(g / (1.0f + expf(-g)) * u);
+  float sum = bf(bits);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+  if (tok < n) {
+    A.a[(size_t)asg * A.I + i8 * 8 + ((q & 3) * 2 + (q >> 2))] = (uint16_t)bits;
+    if (q == 0) A.a8[(size_t)asg * (A.I / 8) + i8] = sum;
+  }
+}
+
+// The join of a team's partial sums (red: [warp][16 rows][16 tokens]).
+__device__ __noinline__ void few_join(const FewPlan &P, int s, int i8, int wk, int team, int sub, const float *red) {
+  const int lane = threadIdx.x & 31, n = P.seg_n[s];
+  bar_team(1 + team, wk * 32);
+  // 4 tokens of 8 indices to a warp at a time: lane = token + 4 index
+  const float *base = red + team * wk * 256 + (lane >> 2) * 16;
+#pragma unroll 1
+  for (int t0 = sub * 4; t0 < n; t0 += wk * 4) {
+    const int tok = t0 + (lane & 3), tk = min(tok, n - 1);
+    float g = 0.f, u = 0.f;
+#pragma unroll 2
+    for (int w = 0; w < wk; w++) {
+      g += base[w * 256 + tk];
+      u += base[w * 256 + 128 + tk];
+    }
+    few_emit(P, s, i8, tok, g, u);
+  }
+  bar_team(1 + team, wk * 32);
+}
+
+// Streams a warp's tiles, blocks ahead across the end of a tile too.  Down: rows r0.. (nr of
+// them).  Sums go through few_emit / few_join, or (down) to out[place][16].
+template <bool GU, bool WIDE, int N>
+__device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, const FewOps &O, int p0, FewCursor<GU> C,
+                                           int step, int per, const FewPart &W, int r0, int nr, uint32_t zero, uint32_t ring,
+                                           float *out) {
+  if (C.left <= 0) return;
+  const int lane = threadIdx.x & 31, t = lane & 3, warp = threadIdx.x >> 5;
+  const int K = GU ? A.d : A.I, steps = K / 128;
+  // what this lane copies of a block: chunk l & 7 of rows l / 8 + 4 i, and the scales or mins of
+  // row l / 2
+  const int cr = lane >> 3, cc = lane & 7, sr = lane >> 1;
+  const uint32_t cdst = ring + cr * 128 + ((cc ^ few_swz(cr)) << 4), sdst = ring + 2048 + lane * 8;
+  const bool even = (steps & 1) == 0;
+  FewCursor<GU> L = C;
+  int lb = W.b0, ls = 0;
+  const uint8_t *blob = nullptr;
+  int co[4], so = 0;
+  if (!GU) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) co[i] = (int)A.bl.dc + (r0 + min(cr + 4 * i, nr - 1)) * (K / 2) + cc * 16;
+    so = (int)(lane & 1 ? A.bl.dm : A.bl.ds) + (r0 + min(sr, nr - 1)) * (K / 32);
+  }
+  auto issue = [&]() {
+    if (L.left > 0) {
+      if (lb == W.b0) {
+        const int e = P.seg_exp[L.s];
+        blob = e < A.E ? A.experts + (long long)e * A.bl.bytes : A.shared;
+        if (GU) {
+          co[0] = (int)A.bl.gc + (L.i * 8 + cr) * (K / 2) + cc * 16;
+          co[1] = co[0] + 4 * (K / 2);
+          co[2] = co[0] + (int)(A.bl.uc - A.bl.gc);
+          co[3] = co[2] + 4 * (K / 2);
+          so = (int)(lane & 1 ? A.bl.gm : A.bl.gs) + (sr < 8 ? 0 : (int)(A.bl.uc - A.bl.gc)) + (L.i * 8 + (sr & 7)) * (K / 32);
+        }
+      }
+      const bool whole = 2 * lb + 1 < steps;
+      if (whole || cc < 4)
+#pragma unroll
+        for (int i = 0; i < 4; i++) cp_async16(cdst + ls + i * 512, blob + co[i] + lb * 128);
+      if (even) {
+        cp_async_small<8>(sdst + ls, blob + so + lb * 8);
+      } else {
+        cp_async_small<4>(sdst + ls, blob + so + lb * 8);
+        if (whole) cp_async_small<4>(sdst + ls + 4, blob + so + lb * 8 + 4);
+      }
+      ls = ls == (kFewDepth - 1) * kFewStage ? 0 : ls + kFewStage;
+      if (++lb == W.b1) {
+        lb = W.b0;
+        L.next(step, per);
+      }
+    }
+    cp_async_commit();
+  };
+  __syncwarp();                           // every lane has left the ring's last use
+#pragma unroll
+  for (int u = 0; u < kFewDepth - 1; u++) issue();
+  uint32_t st = ring;
+  Int4Acc<N> acc;
+  FewCol<WIDE, N> X;
+#pragma unroll 1
+  for (; C.left > 0; C.next(step, per)) {
+    const int n = P.seg_n[C.s], at = P.seg_at[C.s];
+    acc.clear();
+    X.set(O, at - p0, n, zero);
+#pragma unroll 1
+    for (int b = W.b0; b < W.b1; b++) {
+      cp_async_wait_but<kFewDepth - 2>();
+      __syncwarp();                       // the block has arrived, and every lane has left the one before
+      issue();
+      few_mul<WIDE, N>(st, b, 2 * b + 1 < steps, X, acc);
+      st = st == ring + (kFewDepth - 1) * kFewStage ? ring : st + kFewStage;
+    }
+    // pair: lanes l and l + 2 hold the same two tokens and take one each; wide: both tokens
+#pragma unroll
+    for (int q = 0; q < N; q++) {
+      if (!WIDE) {
+        acc.a[q] = f2add(acc.a[q], __shfl_xor_sync(0xffffffffu, acc.a[q], 2));
+        acc.b[q] = f2add(acc.b[q], __shfl_xor_sync(0xffffffffu, acc.b[q], 2));
+      }
+#pragma unroll
+      for (int j = 0; j < (WIDE ? 2 : 1); j++) {
+        const int odd = WIDE ? j : t >> 1, tok = WIDE ? 8 * q + 2 * t + j : 4 * q + 2 * (t & 1) + odd;
+        const float va = __uint_as_float((uint32_t)(acc.a[q] >> (32 * odd)));
+        const float vb = __uint_as_float((uint32_t)(acc.b[q] >> (32 * odd)));
+        if (!GU) {
+          if (tok < n) {
+            float *p = out + (size_t)(at + tok) * 16 + (lane >> 2);
+            p[0] = va;
+            p[8] = vb;
+          }
+        } else if (W.wk == 1) {
+          few_emit(P, C.s, C.i, tok, va, vb);
+        } else if (tok < n) {
+          float *p = out + warp * 256 + (lane >> 2) * 16 + tok;
+          p[0] = va;
+          p[128] = vb;
+        }
+      }
+    }
+    if (GU && W.wk > 1) few_join(P, C.s, C.i, W.wk, W.team, W.sub, out);
+  }
+}
+
+// Copies of the activation rows at places [p0, p1) and their sums by group of 64, G groups.
+template <class X, class V>
+__device__ __forceinline__ FewOps few_stage(const FewPlan &P, int p0, int p1, int G, uint8_t *area, X x, V v) {
+  const int n = p1 - p0, pitch = G * 128 + kFewPad, C = G * 8, lane = threadIdx.x & 31;
+  const FewOps O{smem_at(area), smem_at(area + (size_t)n * pitch), pitch, G * 4};
+  float *sums = reinterpret_cast<float *>(area + (size_t)n * pitch);
+#pragma unroll 1
+  for (int r = threadIdx.x >> 5; r < n; r += kFewWarps) {
+    const int asg = P.asg[p0 + r];
+    const uint16_t *src = x(asg);
+#pragma unroll 1
+    for (int c = lane; c < C; c += 32) cp_async16(O.x + r * pitch + c * 16, src + c * 8);
+#pragma unroll 1
+    for (int g = lane; g < G; g += 32) sums[r * G + g] = v(asg, g);
+  }
+  return O;
+}
+
+// ---------------------------------------------------------------------------------------
+// Phase 2
+// ---------------------------------------------------------------------------------------
+// Tile at which block b's share begins: an equal share of the cost of all tiles.
+__device__ __forceinline__ void few_bound(const FewPlan &P, int per, int b, int &s, int &f) {
+  const long long pos = (long long)P.cost_at[P.nseg] * per * b / (int)gridDim.x;
+  int l = 0, h = P.nseg;
+#pragma unroll 1
+  while (l + 1 < h) {
+    const int m = (l + h) >> 1;
+    if ((long long)P.cost_at[m] * per <= pos) l = m; else h = m;
+  }
+  s = l;
+  f = (int)(pos - (long long)P.cost_at[l] * per) / (P.cost_at[l + 1] - P.cost_at[l]);
+  if (f >= per) {
+    s = l + 1;
+    f = 0;
+  }
+}
+
+__device__ __forceinline__ void few_phase2(const FewArgs &A, const FewPlan &P, uint8_t *area, uint32_t zero, uint32_t ring, float *red) {
+  const int per = A.I / 8, G = A.d / 64, NB = A.d / 256, warp = threadIdx.x >> 5;
+  int sl, fl, sh, fh;
+  few_bound(P, per, blockIdx.x, sl, fl);
+  few_bound(P, per, blockIdx.x + 1, sh, fh);
+  const int s_end = fh > 0 ? sh + 1 : sh;             // one past the last segment
+  const int n4 = P.n4, n8 = P.n8;
+#pragma unroll 1
+  for (int s0 = sl; s0 < s_end;) {
+    int s1 = s0 + 1;
+#pragma unroll 1
+    while (s1 < s_end && P.seg_at[s1 + 1] - P.seg_at[s0] <= A.gu_rows) s1++;
+    const int p0 = P.seg_at[s0];
+    __syncthreads();
+    const uint16_t *xb = A.xb;
+    const float *xv = A.xv;
+    const int k1 = A.k + 1, d = A.d;
+    const FewOps O = few_stage(P, p0, P.seg_at[s1], G, area, [=](int asg) { return xb + (size_t)(asg / k1) * d; },
+                               [=](int asg, int g) { return xv[(size_t)(asg / k1) * G + g]; });
+    cp_async_wait();
+    __syncthreads();
+    // the tiles of segments [a, b) of these: warps to a tile by their number, no more than there
+    // are blocks of K
+    auto share = [&](int a, int b, FewCursor<true> &C, FewPart &W) {
+      a = max(a, s0);
+      b = min(b, s1);
+      const int f0 = a == sl ? fl : 0, f1 = b == s_end && fh > 0 ? fh : per;
+      const int tiles = a < b ? (b - a - 1) * per - f0 + f1 : 0;
+      int wk = tiles <= 2 ? 8 : tiles <= 4 ? 4 : tiles <= 8 ? 2 : 1;
+      while (wk > NB) wk >>= 1;
+      const int sub = warp % wk, team = warp / wk, teams = kFewWarps / wk;
+      W = FewPart{NB * sub / wk, NB * (sub + 1) / wk, wk, team, sub, 0};
+      C = FewCursor<true>{a, f0 + team, (tiles - team + teams - 1) / teams};
+      while (C.i >= per) {
+        C.i -= per;
+        C.s++;
+      }
+      return teams;
+    };
+    FewCursor<true> C;
+    FewPart W;
+    int step = share(n8, P.nseg, C, W);
+    few_stream<true, true, 2>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
+    __syncthreads();
+    step = share(n4, n8, C, W);
+    few_stream<true, false, 2>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
+    __syncthreads();
+    step = share(0, n4, C, W);
+    few_stream<true, false, 1>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
     s0 = s1;
   }
 }
 
-// One warp's part of phase 3: 16 output rows (nr of them) of a segment over a part of K.
-template <int NT>
-__device__ __forceinline__ void few_down(const FewArgs &A, const FewPlan &P, const ActDst &D, int p0, int seg, int r0,
-                                         int nr, int g0, int g1, float *out) {
-  const int lane = threadIdx.x & 31;
-  const int G = A.I / 64, e = P.seg_exp[seg], n = P.seg_n[seg], at = P.seg_at[seg] - p0;
-  const uint8_t *blob = e < A.E ? A.experts + (long long)e * A.bl.bytes : A.shared;
-  auto row_at = [&](int q) {
-    const int row = r0 + min(q, nr - 1);
-    return Int4Row{blob + A.bl.dc + (size_t)row * (A.I / 2) + (lane & 3) * 8,
-                   reinterpret_cast<const uint16_t *>(blob + A.bl.ds) + (size_t)row * G,
-                   reinterpret_cast<const uint16_t *>(blob + A.bl.dm) + (size_t)row * G};
-  };
-  const uint8_t *col[NT], *sv[NT];
+// ---------------------------------------------------------------------------------------
+// Phase 3
+// ---------------------------------------------------------------------------------------
+// t_d = A_d a_s of every token: 16 rows by 8 tokens, K split over the warps that are left
+__device__ __forceinline__ int few_td(const FewArgs &A, float *td) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k1 = A.k + 1;
+  const int rt = (A.r + 15) / 16, ntt = (A.T + 7) / 8, nb = A.I / 32;
+  const int split = min(nb, kFewWarps / (rt * ntt)), u = warp;
+  if (u < rt * ntt * split) {
+    const int q = u / split / ntt * 16, t0 = u / split % ntt * 8, part = u % split;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const uint16_t *ra = A.Ad + (size_t)min(q + (lane >> 2), A.r - 1) * A.I + (lane & 3) * 8;
+    const uint16_t *rb = A.Ad + (size_t)min(q + (lane >> 2) + 8, A.r - 1) * A.I + (lane & 3) * 8;
+    const uint16_t *x = A.a + ((size_t)min(t0 + (lane >> 2), A.T - 1) * k1 + A.k) * A.I + (lane & 3) * 8;
+#pragma unroll 4
+    for (int b = nb * part / split; b < nb * (part + 1) / split; b++)
+      bf16_mul(__ldg(reinterpret_cast<const uint4 *>(ra + b * 32)), __ldg(reinterpret_cast<const uint4 *>(rb + b * 32)),
+               natural_order(*reinterpret_cast<const uint4 *>(x + b * 32)), acc);
 #pragma unroll
-  for (int q = 0; q < NT; q++) {
-    col[q] = D.op + (size_t)(at + min(8 * q + (lane >> 2), n - 1)) * D.pitch + (lane & 3) * 16;
-    sv[q] = reinterpret_cast<const uint8_t *>(D.sv) + (at / 2 + min(4 * q + (lane & 3), (n - 1) / 2)) * 16;
-  }
-  Int4Acc<NT> acc;
-  acc.clear();
-  int4_rows<NT>(row_at(lane >> 2), row_at((lane >> 2) + 8), g0, g1, 0, col, sv, D.pairs * 16, acc);
-#pragma unroll
-  for (int q = 0; q < NT; q++)
-#pragma unroll
-    for (int j = 0; j < 2; j++) {
-      const int tok = 8 * q + 2 * (lane & 3) + j;
-      if (tok < n) {
-        float *p = out + (size_t)(P.seg_at[seg] + tok) * 16 + (lane >> 2);
-        p[0] = __uint_as_float((uint32_t)(acc.a[q] >> (32 * j)));
-        p[8] = __uint_as_float((uint32_t)(acc.b[q] >> (32 * j)));
-      }
+    for (int j = 0; j < 4; j++) {
+      const int row = q + (lane >> 2) + 8 * (j >> 1), t = t0 + 2 * (lane & 3) + (j & 1);
+      if (row < A.r && t < A.T) td[(part * A.T + t) * kMaxR + row] = acc[j];
     }
+  }
+  return split;
 }
 
-// Phase 3: this block's share of the output rows.
-__device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, uint8_t *area, float *td) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+__device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, uint8_t *area, uint32_t zero, uint32_t ring, float *td) {
+  const int tid = threadIdx.x, warp = tid >> 5;
   const int lo = (int)((long long)A.d * blockIdx.x / gridDim.x), hi = (int)((long long)A.d * (blockIdx.x + 1) / gridDim.x);
   if (lo >= hi) return;
-  const int G = A.I / 64, k1 = A.k + 1;
+  const int G = A.I / 64, NB = (G + 3) / 4, k1 = A.k + 1, nplace = P.nplace;
   float *out = reinterpret_cast<float *>(area);
-  uint8_t *stage = area + A.parts_bytes;
-  // t_d = A_d a_s of every token, 16 rows by 8 tokens a warp
-  if (A.Ad) {
-    const int rt = (A.r + 15) / 16, ntt = (A.T + 7) / 8;
-    for (int u = warp; u < rt * ntt; u += kFewWarps) {
-      const int q = u / ntt * 16, t0 = u % ntt * 8;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      const uint16_t *ra = A.Ad + (size_t)min(q + (lane >> 2), A.r - 1) * A.I + (lane & 3) * 8;
-      const uint16_t *rb = A.Ad + (size_t)min(q + (lane >> 2) + 8, A.r - 1) * A.I + (lane & 3) * 8;
-      const uint16_t *x = A.a + ((size_t)min(t0 + (lane >> 2), A.T - 1) * k1 + A.k) * A.I + (lane & 3) * 8;
-      bf16_rows(ra, rb, x, 0, A.I, acc);
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const int row = q + (lane >> 2) + 8 * (j >> 1), t = t0 + 2 * (lane & 3) + (j & 1);
-        if (row < A.r && t < A.T) td[t * kMaxR + row] = acc[j];
-      }
-    }
-  }
+  uint8_t *stage = area + A.out_bytes;
+  bool first = true;
+#pragma unroll 1
   for (int r0 = lo; r0 < hi; r0 += 16) {
     const int nr = min(16, hi - r0);
     // parts of K: more where there are few segments to keep the warps busy
     int parts = 1;
-    while (parts < 4 && P.nseg * parts * 2 <= 2 * kFewWarps && 2 * parts <= G &&
-           2 * parts * P.nplace * 64 <= A.parts_bytes)
+    while (parts < 4 && P.nseg * parts * 2 <= kFewWarps && 2 * parts <= NB && 2 * parts * nplace * 64 <= A.out_bytes)
       parts *= 2;
+    // 16 warps are a multiple of the parts, so a warp stays with one part
+    const int part = warp % parts, team = warp / parts, step = kFewWarps / parts;
+    const FewPart W{NB * part / parts, NB * (part + 1) / parts, 1, 0, 0, part};
+    float *o = out + (size_t)part * nplace * 16;
+#pragma unroll 1
     for (int s0 = 0; s0 < P.nseg;) {
       int s1 = s0 + 1;
+#pragma unroll 1
       while (s1 < P.nseg && P.seg_at[s1 + 1] - P.seg_at[s0] <= A.dn_rows) s1++;
-      const int p0 = P.seg_at[s0], p1 = P.seg_at[s1];
+      const int p0 = P.seg_at[s0];
       __syncthreads();
       const uint16_t *a = A.a;
+      const float *a8 = A.a8;
       const int I = A.I;
-      const ActDst D = few_stage(P, p0, p1, G, stage, [=](int asg) { return a + (size_t)asg * I; });
-      __syncthreads();
-      for (int u = warp; u < (s1 - s0) * parts; u += kFewWarps) {
-        const int s = s0 + u / parts, part = u % parts, n = P.seg_n[s];
-        float *o = out + (size_t)part * P.nplace * 16;
-        const int g0 = G * part / parts, g1 = G * (part + 1) / parts;
-        if (n <= 8)
-          few_down<1>(A, P, D, p0, s, r0, nr, g0, g1, o);
-        else if (n <= 16)
-          few_down<2>(A, P, D, p0, s, r0, nr, g0, g1, o);
-        else
-          few_down<4>(A, P, D, p0, s, r0, nr, g0, g1, o);
+      const FewOps O = few_stage(P, p0, P.seg_at[s1], G, stage, [=](int asg) { return a + (size_t)asg * I; },
+                                 [=](int asg, int g) {
+                                   const float4 *p = reinterpret_cast<const float4 *>(a8 + (size_t)asg * (I / 8) + g * 8);
+                                   const float4 u = p[0], w = p[1];
+                                   return ((u.x + u.y) + (u.z + u.w)) + ((w.x + w.y) + (w.z + w.w));
+                                 });
+      if (A.Ad && first) {
+        const int split = few_td(A, td);
+        __syncthreads();
+        float v = 0.f;                    // one (token, rank) a thread and round: T r <= 2048
+#pragma unroll 1
+        for (int u = tid; u < A.T * kMaxR; u += kFewThreads) {
+          v = 0.f;
+#pragma unroll 4
+          for (int w = 0; w < split; w++) v += td[w * A.T * kMaxR + u];
+          td[u] = v;                      // only this thread reads or writes column u
+        }
       }
+      first = false;
+      cp_async_wait();
+      __syncthreads();
+      const int m4 = max(s0, min(s1, P.n4)), m8 = max(m4, min(s1, P.n8));
+      auto cursor = [&](int a, int b) { return FewCursor<false>{a + team, 0, (b - a - team + step - 1) / step}; };
+      few_stream<false, true, 2>(A, P, O, p0, cursor(m8, s1), step, 0, W, r0, nr, zero, ring, o);
+      few_stream<false, false, 2>(A, P, O, p0, cursor(m4, m8), step, 0, W, r0, nr, zero, ring, o);
+      few_stream<false, false, 1>(A, P, O, p0, cursor(s0, m4), step, 0, W, r0, nr, zero, ring, o);
       s0 = s1;
     }
     __syncthreads();
-    for (int o = tid; o < 16 * A.T; o += kFewThreads) {
-      const int t = o / 16, q = o % 16, row = r0 + q;
+#pragma unroll 1
+    for (int u = tid; u < 16 * A.T; u += kFewThreads) {
+      const int t = u / 16, q = u % 16, row = r0 + q;
       if (q >= nr) continue;
       float y = 0.f;
+#pragma unroll 1
       for (int j = 0; j <= A.k; j++) {
         const float *p = out + (size_t)P.place[t * k1 + j] * 16 + q;
         float v = p[0];
-        for (int w = 1; w < parts; w++) v += p[(size_t)w * P.nplace * 16];
-        v *= kActUnit;
+#pragma unroll 1
+        for (int w = 1; w < parts; w++) v += p[(size_t)w * nplace * 16];
         y = j < A.k ? fmaf(P.gate[t * A.k + j], v, y) : y + v;
       }
       if (A.Ad) {
         float b = 0.f;
+#pragma unroll 8
         for (int j = 0; j < A.r; j++) b = fmaf(bf(A.Bd[(size_t)row * A.r + j]), td[t * kMaxR + j], b);
         y = fmaf(A.c, b, y);
       }
@@ -593,19 +975,25 @@ __device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, u
   }
 }
 
-__global__ void __launch_bounds__(kFewThreads, 1) k_moe_few(FewArgs A) {
+__global__ void __launch_bounds__(kFewThreads, 1) k_moe_few(const __grid_constant__ FewArgs A) {
   extern __shared__ __align__(128) uint8_t smem[];
   FewPlan &P = *reinterpret_cast<FewPlan *>(smem);
-  uint8_t *red_area = smem + few_plan_bytes(), *area = red_area + kFewRedBytes;
+  uint8_t *zero = smem + few_plan_bytes(), *red_area = zero + kFewZeroBytes, *rings = red_area + kFewRedBytes;
+  uint8_t *area = rings + kFewRingBytes;          // phase 1, which streams nothing, takes the rings too
   float *red = reinterpret_cast<float *>(red_area);
+  const uint32_t ring = smem_at(rings) + (threadIdx.x >> 5) * kFewDepth * kFewStage;
+  if (threadIdx.x < kFewZeroBytes / 4) reinterpret_cast<uint32_t *>(zero)[threadIdx.x] = 0;
+  static_assert(sizeof(FewArgs) % 4 == 0 && sizeof(FewArgs) / 4 <= kFewThreads, "one word of the arguments a thread");
+  if (threadIdx.x < sizeof(FewArgs) / 4)
+    reinterpret_cast<uint32_t *>(&P.args)[threadIdx.x] = reinterpret_cast<const uint32_t *>(&A)[threadIdx.x];
   cooperative_groups::grid_group grid = cooperative_groups::this_grid();
-  few_phase1(A, P, area, red);
+  few_phase1(A, P, rings, red);
   grid.sync();
-  if (A.h_out) few_residual(A);
+  if (A.h_out) few_residual(A, rings);
   few_plan(A, P);
-  few_phase2(A, P, area, red);
+  few_phase2(A, P, area, smem_at(zero), ring, red);
   grid.sync();
-  few_phase3(A, P, area, red);
+  few_phase3(A, P, area, smem_at(zero), ring, red);
 }
 
 }  // namespace e0

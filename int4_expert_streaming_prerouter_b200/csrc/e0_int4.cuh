@@ -195,6 +195,157 @@ __device__ __forceinline__ void int4_rows(const Int4Row &ra, const Int4Row &rb, 
 }
 
 // ---------------------------------------------------------------------------------------
+// 16 weight rows by up to 8 tokens: two groups to a matrix instruction
+// ---------------------------------------------------------------------------------------
+// With few tokens the 8 columns of a matrix instruction hold 4 tokens twice: columns 0..3 the
+// tokens restricted to a group of 64, columns 4..7 restricted to the next one (zero elsewhere).
+// A lane then takes 16 consecutive bytes of a row, its four lanes cover two groups, the sums of
+// the two come out in different columns, and there is one fold for both.  The lane (row l / 4,
+// t = l & 3) holds tokens 2 (t & 1), 2 (t & 1) + 1 of group t / 2 in its accumulators; lanes t
+// and t + 2 are added at the end.
+//
+// A block is 256 channels of 16 rows: 4 loads of codes and 4 of scales and mins a lane.
+
+struct PairBlk {
+  uint4 a[2], b[2];
+  uint2 sa, ma, sb, mb;
+};
+
+__device__ __forceinline__ uint4 ldg_stream(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// Block b of rows whose codes start at the lane's 16 bytes of the row.  G128: scales per 128
+// (two a block) instead of per 64 (four).
+template <bool G128>
+__device__ __forceinline__ void pair_load(PairBlk &B, const Int4Row &ra, const Int4Row &rb, int b) {
+  B.a[0] = ldg_stream(ra.c + (size_t)b * 128);
+  B.a[1] = ldg_stream(ra.c + (size_t)b * 128 + 64);
+  B.b[0] = ldg_stream(rb.c + (size_t)b * 128);
+  B.b[1] = ldg_stream(rb.c + (size_t)b * 128 + 64);
+  if (G128) {
+    B.sa.x = __ldg(reinterpret_cast<const uint32_t *>(ra.s + b * 2));
+    B.ma.x = __ldg(reinterpret_cast<const uint32_t *>(ra.m + b * 2));
+    B.sb.x = __ldg(reinterpret_cast<const uint32_t *>(rb.s + b * 2));
+    B.mb.x = __ldg(reinterpret_cast<const uint32_t *>(rb.m + b * 2));
+  } else {
+    B.sa = __ldg(reinterpret_cast<const uint2 *>(ra.s + b * 4));
+    B.ma = __ldg(reinterpret_cast<const uint2 *>(ra.m + b * 4));
+    B.sb = __ldg(reinterpret_cast<const uint2 *>(rb.s + b * 4));
+    B.mb = __ldg(reinterpret_cast<const uint2 *>(rb.m + b * 4));
+  }
+}
+
+// The lane's view of the activations of NP times 4 tokens (n of them, at rows `at`.. of D;
+// `at` even).  zero: 128 bytes of zeros in shared memory, 16-byte aligned.
+template <int NP>
+struct PairCol {
+  const uint8_t *col[NP], *sv[NP];
+  int step, svs;
+  uint32_t sel;
+  __device__ __forceinline__ PairCol(const ActDst &D, int at, int n, const uint8_t *zero) {
+    const int lane = threadIdx.x & 31, t = lane & 3, c = lane >> 2;
+    const bool mine = (t >> 1) == (c >> 2);
+    step = mine ? 256 : 0;
+    svs = D.pairs * 16;
+    sel = t >> 1 ? 0x3244u : 0x1044u;
+#pragma unroll
+    for (int q = 0; q < NP; q++) {
+      col[q] = mine ? D.op + (size_t)(at + min(4 * q + (c & 3), n - 1)) * D.pitch + (t >> 1) * 128 + (t & 1) * 32 : zero;
+      sv[q] = reinterpret_cast<const uint8_t *>(D.sv) + (at / 2 + min(2 * q + (t & 1), (n - 1) / 2)) * 16 + (t >> 1) * svs;
+    }
+  }
+};
+
+template <int NP, bool G128>
+__device__ __forceinline__ void pair_mul(const PairBlk &B, int b, const PairCol<NP> &X, Int4Acc<NP> &acc) {
+  constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
+#pragma unroll
+  for (int j = 0; j < 2; j++) {
+    const uint32_t wa[4] = {B.a[j].x, B.a[j].y, B.a[j].z, B.a[j].w}, wb[4] = {B.b[j].x, B.b[j].y, B.b[j].z, B.b[j].w};
+    float p[NP][4];
+#pragma unroll
+    for (int q = 0; q < NP; q++) p[q][0] = p[q][1] = p[q][2] = p[q][3] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; w++) {
+      const uint32_t xa = wa[w], xb = wb[w], ya = xa >> 8, yb = xb >> 8;
+#pragma unroll
+      for (int q = 0; q < NP; q++) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(X.col[q] + (2 * b + j) * X.step + (w & 1) * 64 + (w >> 1) * 16);
+        mma_f16_acc(p[q], xa & LO, xb & LO, xa & HI, xb & HI, x.x, x.y);
+        mma_f16_acc(p[q], ya & LO, yb & LO, ya & HI, yb & HI, x.z, x.w);
+      }
+    }
+    const uint32_t sel = G128 ? (j ? 0x3244u : 0x1044u) : X.sel;
+    auto pick = [&](const uint2 &v) {
+      const float f = __uint_as_float(__byte_perm(G128 || j == 0 ? v.x : v.y, 0u, sel));
+      return pk2(f, f);
+    };
+    const unsigned long long sa = pick(B.sa), ma = pick(B.ma), sb = pick(B.sb), mb = pick(B.mb);
+#pragma unroll
+    for (int q = 0; q < NP; q++) {
+      const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(X.sv[q] + (4 * b + 2 * j) * X.svs);
+      acc.a[q] = f2fma(sa, f2mul(pk2(p[q][0], p[q][1]), f.x), f2fma(ma, f.y, acc.a[q]));
+      acc.b[q] = f2fma(sb, f2mul(pk2(p[q][2], p[q][3]), f.x), f2fma(mb, f.y, acc.b[q]));
+    }
+  }
+}
+
+// Adds lanes t and t + 2: every lane then holds the sums of tokens 2 (t & 1), 2 (t & 1) + 1.
+template <int NP>
+__device__ __forceinline__ void pair_join(Int4Acc<NP> &acc) {
+#pragma unroll
+  for (int q = 0; q < NP; q++) {
+    acc.a[q] = f2add(acc.a[q], __shfl_xor_sync(0xffffffffu, acc.a[q], 2));
+    acc.b[q] = f2add(acc.b[q], __shfl_xor_sync(0xffffffffu, acc.b[q], 2));
+  }
+}
+
+// A warp's jobs one after another, each blocks [b0, b1) of 16 rows, with the loads of the next
+// blocks in flight, across the end of a job too.  rows(j, ra, rb) gives job j's rows,
+// cols(j) its activations, done(j, acc) takes its sums.
+template <int NP, bool G128, class Rows, class Cols, class Done>
+__device__ __forceinline__ void pair_stream(int jobs, int b0, int b1, Rows rows, Cols cols, Done done) {
+  if (jobs <= 0 || b0 >= b1) return;
+  constexpr int D = NP == 1 ? 3 : 2;      // two tiles of tokens leave registers for one less
+  PairBlk buf[D];
+  Int4Row ra, rb;
+  int lj = 0, lb = b0;                    // the next block to load
+  auto load = [&](PairBlk &B) {
+    if (lj >= jobs) return;
+    if (lb == b0) rows(lj, ra, rb);
+    pair_load<G128>(B, ra, rb, lb);
+    if (++lb == b1) {
+      lb = b0;
+      lj++;
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < D - 1; u++) load(buf[u]);
+  Int4Acc<NP> acc;
+  acc.clear();
+  PairCol<NP> X = cols(0);
+  for (int j = 0, b = b0;;) {
+#pragma unroll
+    for (int u = 0; u < D; u++) {
+      load(buf[(u + D - 1) % D]);
+      pair_mul<NP, G128>(buf[u], b, X, acc);
+      if (++b == b1) {
+        pair_join(acc);
+        done(j, acc);
+        if (++j == jobs) return;
+        acc.clear();
+        X = cols(j);
+        b = b0;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------
 // e0_int4_linear
 // ---------------------------------------------------------------------------------------
 enum { ACT_BF16 = 0, ACT_INT8 = 1, ACT_E4M3 = 2 };
