@@ -2210,15 +2210,23 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
   CK(cudaDeviceGetAttribute(&coop, cudaDevAttrCooperativeLaunch, dev));
   CK(cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev));
   if (!coop || nsm < (kFewMaxT + 7) / 8) return fail(E0_ERR_CUDA, "moe_layer_few: the device has no cooperative launch");
-  const int smem = most, area = smem - (int)few_plan_bytes() - kFewZeroBytes - kFewRedBytes - kFewRingBytes;
-  // activation rows that fit the staging area, and so the tokens of a segment
-  A.out_bytes = std::max(16384, T * (A.k + 1) * 64);
-  A.gu_rows = area / few_row_bytes(A.d);
-  A.dn_rows = (area - A.out_bytes) / few_row_bytes(A.I);
-  const int rows = std::min(A.gu_rows, A.dn_rows);
-  A.seg_cap = rows >= 16 ? 16 : 8;
+  // shared memory: phase 2 holds the rings and as many activation rows as the rest takes; phase 3
+  // t_d, the results of every (token, slot), the sums of their activations and the rings, at least
+  // two stages each.  Tokens of a segment: 16 where both phases have room for them, else 8.
+  const int smem = most, rest = smem - (int)few_plan_bytes() - kFewZeroBytes - kFewRedBytes;
+  A.gu_rows = (rest - kFewRingBytes) / few_row_bytes(A.d);
+  const int places = T * (A.k + 1), sum_bytes = A.I / 64 * 4;
+  A.out_bytes = std::max(16384, places * 64);
+  const int least8 = kFewWarps * 2 * few_dn_stage(8), least16 = kFewWarps * 2 * few_dn_stage(16);
+  const int wish = std::min(places, 16) * sum_bytes + 16;
+  A.seg_cap = A.gu_rows >= 16 && rest - A.out_bytes - wish >= least16 ? 16 : 8;
+  const int most_sums = rest - A.out_bytes - 16 - (A.seg_cap == 16 ? least16 : least8);
+  A.dn_rows = std::min(places, most_sums / sum_bytes);
+  A.dn_ring = (rest - A.out_bytes - (A.dn_rows * sum_bytes + 15) / 16 * 16) / kFewWarps / 16 * 16;
+  if (A.gu_rows < 8 || A.dn_rows < std::min(places, A.seg_cap))
+    return fail(E0_ERR_INVALID_ARG, "moe_layer_few: dims too large for the shared memory");
   A.tpb = T <= 8 ? 1 : T <= 16 ? 2 : T <= 32 ? 4 : 8;
-  if (rows < 8) return fail(E0_ERR_INVALID_ARG, "moe_layer_few: dims too large for the staging area");
+  A.lora16 = !misaligned(Y.lora_Bg, 16) && !misaligned(Y.lora_Bu, 16) && !misaligned(Y.lora_Bd, 16);
   CK(cudaFuncSetAttribute(k_moe_few, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   void *args[] = {&A};
   CK(cudaLaunchCooperativeKernel((const void *)k_moe_few, dim3(nsm), dim3(kFewThreads), args, (size_t)smem, (cudaStream_t)stream));

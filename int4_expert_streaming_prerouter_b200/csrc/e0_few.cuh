@@ -65,9 +65,10 @@ struct FewArgs {
   float *a8;                  // [T][k + 1][I / 8] sums of a
   int *err;
   int seg_cap;                // tokens to a segment: 8 or 16
+  int lora16;                 // rows of LoRA B begin at 16 bytes
   int tpb;                    // tokens that a block of phase 1 norms
-  int gu_rows, dn_rows;       // activation rows that fit the staging area in phases 2 and 3
-  int out_bytes;              // bytes of the down-projection results in phase 3
+  int gu_rows;                // activation rows that fit the staging area of phase 2
+  int out_bytes, dn_rows, dn_ring;   // phase 3: bytes of the results; rows whose sums fit; bytes of a warp's ring
 };
 
 struct FewPlan {
@@ -82,7 +83,6 @@ struct FewPlan {
   uint16_t seg_exp[kFewMaxSeg];
   uint16_t seg_at[kFewMaxSeg + 1];
   uint16_t seg_n[kFewMaxSeg];
-  int cost_at[kFewMaxSeg + 1];    // cost of the segments before one, per tile column
   int nseg, nplace, n4, n8;       // segments of experts with at most 4 and at most 8 tokens come first
   double part[kFewWarps];
 };
@@ -90,6 +90,7 @@ struct FewPlan {
 __host__ __device__ inline size_t few_plan_bytes() { return (sizeof(FewPlan) + 127) & ~(size_t)127; }
 constexpr int kFewZeroBytes = 128;
 constexpr int kFewRedBytes = kFewWarps * 16 * 16 * 4;            // partial sums of 16 warps: 16 rows x 16 tokens
+// bytes of an activation row of phase 2 with its sums
 __host__ __device__ inline int few_row_bytes(int channels) { return channels * 2 + kFewPad + channels / 64 * 4; }
 
 __device__ __forceinline__ void bar_team(int id, int threads) {
@@ -102,6 +103,15 @@ __device__ __forceinline__ void mma_bf16_acc(float (&d)[4], uint32_t a0, uint32_
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// the same without a sum to add to
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -147,11 +157,16 @@ __device__ __forceinline__ void bf16_mul(uint4 a, uint4 b, uint4 x, float (&acc)
 // tokens 2 (l & 3), + 1 of a tile (pair: tokens 2 (l & 1), + 1, after adding lanes l and l + 2).
 //
 // Each warp streams its weights through a ring of its own in shared memory, a block to a stage, by
-// cp.async: 16 rows of 128 bytes of codes (their 16-byte chunks permuted by row, so that either
-// form reads without bank conflicts), then per row the scales and the mins of 4 groups.
+// cp.async.  Phase 2: 256 channels, 16 rows of 128 bytes of codes (their 16-byte chunks permuted by
+// row, so that either form reads without bank conflicts), then per row the scales and the mins of 4
+// groups; the activations, which every tile needs again, are staged apart.  Phase 3: 128 channels, 64
+// bytes of codes a row, the scales and mins of 2 groups, and the activations of the segment's
+// tokens, which are used once.
 constexpr int kFewStage = 16 * 128 + 16 * 16;
 constexpr int kFewDepth = 3;
 constexpr int kFewRingBytes = kFewWarps * kFewDepth * kFewStage;
+constexpr int kFewDnHead = 16 * 64 + 16 * 8, kFewDnRow = 256 + 16;
+constexpr int few_dn_stage(int tokens) { return kFewDnHead + tokens * kFewDnRow; }
 
 template <int N>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src) {
@@ -160,12 +175,18 @@ __device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src) {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// all but the newest n (0..2) groups
+__device__ __forceinline__ void cp_async_wait_upto(int n) {
+  if (n <= 0) cp_async_wait_but<0>();
+  else if (n == 1) cp_async_wait_but<1>();
+  else cp_async_wait_but<2>();
+}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
-// chunk c of row r is at chunk c ^ few_swz(r)
+// chunk c of row r is at chunk c ^ few_swz(r) (phase 3, four chunks a row: ^ (r & 2))
 __device__ __forceinline__ int few_swz(int r) { return ((r & 1) << 2) ^ (r & 2); }
 
 // Activation rows in shared memory: bf16 rows `pitch` bytes apart, and their sums by group.
@@ -174,12 +195,13 @@ struct FewOps {
   int pitch, vp;              // bytes between rows of x and of v
 };
 
-// A lane's columns: N tiles of tokens (wide: 8 each, pair: 4), n tokens in all, at row `at`.
+// A lane's columns: N tiles of tokens (wide: 8 each, pair: 4), n tokens in all, at row `at` of x
+// and `vat` of the sums.  step: bytes from 128 channels to the next.
 template <bool WIDE, int N>
 struct FewCol {
   uint32_t x[N], v0[N], v1[N];
   int step;
-  __device__ __forceinline__ void set(const FewOps &O, int at, int n, uint32_t zero) {
+  __device__ __forceinline__ void set(const FewOps &O, int at, int vat, int n, uint32_t zero) {
     const int lane = threadIdx.x & 31, t = lane & 3, c = lane >> 2;
     const bool mine = WIDE || (t >> 1) == (c >> 2);
     step = mine ? 256 : 0;
@@ -187,8 +209,8 @@ struct FewCol {
     for (int q = 0; q < N; q++) {
       const int tok = WIDE ? 8 * q + c : 4 * q + (c & 3), pair = WIDE ? 8 * q + 2 * t : 4 * q + 2 * (t & 1);
       x[q] = mine ? O.x + (at + min(tok, n - 1)) * O.pitch + (WIDE ? t * 32 : t * 64) : zero;
-      v0[q] = O.v + (at + min(pair, n - 1)) * O.vp + (WIDE ? 0 : (t >> 1) * 4);
-      v1[q] = O.v + (at + min(pair + 1, n - 1)) * O.vp + (WIDE ? 0 : (t >> 1) * 4);
+      v0[q] = O.v + (vat + min(pair, n - 1)) * O.vp + (WIDE ? 0 : (t >> 1) * 4);
+      v1[q] = O.v + (vat + min(pair + 1, n - 1)) * O.vp + (WIDE ? 0 : (t >> 1) * 4);
     }
   }
 };
@@ -196,38 +218,37 @@ struct FewCol {
 // 8 codes of a word as four pairs 128 + q, in operand order
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u; }
 
-// One fold: the sums p of a group (or, pair, of a lane's group of two) with its scale and min.
-// The scale is the low (0x1044) or high (0x3244) half of a word.
+// One fold: the sums p of a group (pair: of a lane's group of two) with its scales and mins, the
+// low (sel 0x1044) or high (0x3244) halves of the words.  at: byte offset of the group's sums.
 template <int N>
 __device__ __forceinline__ void few_fold(const float (&p)[N][4], uint32_t wsa, uint32_t wma, uint32_t wsb, uint32_t wmb,
                                          uint32_t sel, const uint32_t (&v0)[N], const uint32_t (&v1)[N], int at,
-                                         Int4Acc<N> &acc) {
+                                         float (&acc)[N][4]) {
   auto pick = [&](uint32_t w) { return __uint_as_float(__byte_perm(w, 0u, sel)); };
   const float sa = pick(wsa), sb = pick(wsb), ma = fmaf(-128.f, sa, pick(wma)), mb = fmaf(-128.f, sb, pick(wmb));
-  const unsigned long long sa2 = pk2(sa, sa), ma2 = pk2(ma, ma), sb2 = pk2(sb, sb), mb2 = pk2(mb, mb);
 #pragma unroll
   for (int q = 0; q < N; q++) {
-    const unsigned long long v = pk2(lds32(v0[q] + at), lds32(v1[q] + at));
-    acc.a[q] = f2fma(sa2, pk2(p[q][0], p[q][1]), f2fma(ma2, v, acc.a[q]));
-    acc.b[q] = f2fma(sb2, pk2(p[q][2], p[q][3]), f2fma(mb2, v, acc.b[q]));
+    const float x0 = lds32(v0[q] + at), x1 = lds32(v1[q] + at);
+    acc[q][0] = fmaf(sa, p[q][0], fmaf(ma, x0, acc[q][0]));
+    acc[q][1] = fmaf(sa, p[q][1], fmaf(ma, x1, acc[q][1]));
+    acc[q][2] = fmaf(sb, p[q][2], fmaf(mb, x0, acc[q][2]));
+    acc[q][3] = fmaf(sb, p[q][3], fmaf(mb, x1, acc[q][3]));
   }
 }
 
-// Block b, at stage address st, times the columns.  whole: 256 channels, else 128.
+// 128 channels: codes of the lane's rows at `row` (the row's address) and `row` + half (8 rows on),
+// chunks permuted by swz, the first at chunk c0; scale words (s, m of rows l / 4, l / 4 + 8) of the
+// two groups; columns at byte offset xo (pair: times step / 256), sums at vo.
 template <bool WIDE, int N>
-__device__ __forceinline__ void few_mul(uint32_t st, int b, bool whole, const FewCol<WIDE, N> &X, Int4Acc<N> &acc) {
-  const int lane = threadIdx.x & 31, t = lane & 3, r = lane >> 2;
-  const uint4 ca = lds128(st + 2048 + r * 16), cb = lds128(st + 2048 + r * 16 + 128);
-  const uint32_t row = st + r * 128, swz = few_swz(r);
+__device__ __forceinline__ void few_mul128(uint32_t row, int half, int c0, int swz, uint32_t wsa, uint32_t wma, uint32_t wsb,
+                                           uint32_t wmb, const FewCol<WIDE, N> &X, int xs, int vo, float (&acc)[N][4]) {
+  const int t = threadIdx.x & 3;
   if (WIDE) {
 #pragma unroll
-    for (int g = 0; g < 4; g++) {
-      if (g == 2 && !whole) break;
-      const uint32_t at = row + (((2 * g + (t >> 1)) ^ swz) << 4) + (t & 1) * 8;
-      const uint2 wa = lds64(at), wb = lds64(at + 1024);
+    for (int g = 0; g < 2; g++) {
+      const uint32_t at = row + (((c0 + 2 * g + (t >> 1)) ^ swz) << 4) + (t & 1) * 8;
+      const uint2 wa = lds64(at), wb = lds64(at + half);
       float p[N][4];
-#pragma unroll
-      for (int q = 0; q < N; q++) p[q][0] = p[q][1] = p[q][2] = p[q][3] = 0.f;
 #pragma unroll
       for (int w = 0; w < 2; w++) {
         const uint32_t xa = w ? wa.y : wa.x, xb = w ? wb.y : wb.x;
@@ -235,85 +256,62 @@ __device__ __forceinline__ void few_mul(uint32_t st, int b, bool whole, const Fe
         const uint32_t b0 = code_pair(xb, 0), b1 = code_pair(xb, 1), b2 = code_pair(xb, 2), b3 = code_pair(xb, 3);
 #pragma unroll
         for (int q = 0; q < N; q++) {
-          const uint4 x = lds128(X.x[q] + b * 512 + g * 128 + w * 16);
-          mma_bf16_acc(p[q], a0, b0, a1, b1, x.x, x.y);
+          const uint4 x = lds128(X.x[q] + xs * 256 + g * 128 + w * 16);
+          if (w == 0) mma_bf16_first(p[q], a0, b0, a1, b1, x.x, x.y);
+          else mma_bf16_acc(p[q], a0, b0, a1, b1, x.x, x.y);
           mma_bf16_acc(p[q], a2, b2, a3, b3, x.z, x.w);
         }
       }
-      few_fold<N>(p, g < 2 ? ca.x : ca.y, g < 2 ? ca.z : ca.w, g < 2 ? cb.x : cb.y, g < 2 ? cb.z : cb.w,
-                  g & 1 ? 0x3244u : 0x1044u, X.v0, X.v1, (4 * b + g) * 4, acc);
+      few_fold<N>(p, wsa, wma, wsb, wmb, g ? 0x3244u : 0x1044u, X.v0, X.v1, vo + g * 4, acc);
     }
   } else {
-    const uint32_t sel = t >> 1 ? 0x3244u : 0x1044u;
+    const uint32_t at = row + (((c0 + t) ^ swz) << 4);
+    const uint4 wa = lds128(at), wb = lds128(at + half);
+    float p[N][4];
 #pragma unroll
-    for (int j = 0; j < 2; j++) {
-      if (j == 1 && !whole) break;
-      const uint32_t at = row + (((4 * j + t) ^ swz) << 4);
-      const uint4 wa = lds128(at), wb = lds128(at + 1024);
-      // two chains of matrix instructions, joined at the fold
-      float p[N][4], p2[N][4];
+    for (int w = 0; w < 4; w++) {
+      const uint32_t xa = w == 0 ? wa.x : w == 1 ? wa.y : w == 2 ? wa.z : wa.w;
+      const uint32_t xb = w == 0 ? wb.x : w == 1 ? wb.y : w == 2 ? wb.z : wb.w;
+      const uint32_t a0 = code_pair(xa, 0), a1 = code_pair(xa, 1), a2 = code_pair(xa, 2), a3 = code_pair(xa, 3);
+      const uint32_t b0 = code_pair(xb, 0), b1 = code_pair(xb, 1), b2 = code_pair(xb, 2), b3 = code_pair(xb, 3);
 #pragma unroll
-      for (int q = 0; q < N; q++) p[q][0] = p[q][1] = p[q][2] = p[q][3] = p2[q][0] = p2[q][1] = p2[q][2] = p2[q][3] = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; w++) {
-        const uint32_t xa = w == 0 ? wa.x : w == 1 ? wa.y : w == 2 ? wa.z : wa.w;
-        const uint32_t xb = w == 0 ? wb.x : w == 1 ? wb.y : w == 2 ? wb.z : wb.w;
-        const uint32_t a0 = code_pair(xa, 0), a1 = code_pair(xa, 1), a2 = code_pair(xa, 2), a3 = code_pair(xa, 3);
-        const uint32_t b0 = code_pair(xb, 0), b1 = code_pair(xb, 1), b2 = code_pair(xb, 2), b3 = code_pair(xb, 3);
-#pragma unroll
-        for (int q = 0; q < N; q++) {
-          const uint4 x = lds128(X.x[q] + (2 * b + j) * X.step + w * 16);
-          mma_bf16_acc(p[q], a0, b0, a1, b1, x.x, x.y);
-          mma_bf16_acc(p2[q], a2, b2, a3, b3, x.z, x.w);
-        }
+      for (int q = 0; q < N; q++) {
+        const uint4 x = lds128(X.x[q] + xs * X.step + w * 16);
+        if (w == 0) mma_bf16_first(p[q], a0, b0, a1, b1, x.x, x.y);
+        else mma_bf16_acc(p[q], a0, b0, a1, b1, x.x, x.y);
+        mma_bf16_acc(p[q], a2, b2, a3, b3, x.z, x.w);
       }
-#pragma unroll
-      for (int q = 0; q < N; q++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) p[q][i] += p2[q][i];
-      few_fold<N>(p, j ? ca.y : ca.x, j ? ca.w : ca.z, j ? cb.y : cb.x, j ? cb.w : cb.z, sel, X.v0, X.v1, (4 * b + 2 * j) * 4,
-                  acc);
     }
+    few_fold<N>(p, wsa, wma, wsb, wmb, t >> 1 ? 0x3244u : 0x1044u, X.v0, X.v1, vo, acc);
   }
 }
 
-// Top-k of E <= 256 logits over a warp, descending, equal values by lower index; a NaN counts
-// as the lowest value, so every index is valid.  Lane j < k gets the j-th.
-__device__ __forceinline__ int few_topk(const float *v, int E, int k, int lane) {
-  float vals[kMaxE / 32];
-  unsigned left = 0;
-#pragma unroll
-  for (int i = 0; i < kMaxE / 32; i++) {
-    const int e = lane + 32 * i;
-    vals[i] = -INFINITY;
-    if (e < E) {
-      const float f = v[e];
-      vals[i] = f == f ? f : -INFINITY;
-      left |= 1u << i;
-    }
-  }
+// A number whose order as an unsigned integer is the order of the floats; a NaN is the lowest
+// but one (0 is what has been taken).
+__device__ __forceinline__ uint32_t few_key(float f) {
+  const uint32_t u = __float_as_uint(f == f ? (f == 0.f ? 0.f : f) : -INFINITY);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Top-k of E <= 256 keys (lane l holds those of l, l + 32, ...; 0 past the end) over a warp,
+// descending, equal values by lower index.  Lane j < k gets the j-th index.
+__device__ __forceinline__ int few_topk(uint32_t (&key)[kMaxE / 32], int k, int lane) {
   int mine = 0;
 #pragma unroll 1
   for (int s = 0; s < k; s++) {
-    float bv = -INFINITY;
-    int be = 0x7fffffff;
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < kMaxE / 32; i++) m = max(m, key[i]);
+    m = __reduce_max_sync(0xffffffffu, m);
+    uint32_t at = 0x7fffffffu;
+#pragma unroll
+    for (int i = kMaxE / 32 - 1; i >= 0; i--)
+      if (key[i] == m) at = lane + 32 * i;
+    at = __reduce_min_sync(0xffffffffu, at);
+    if (lane == s) mine = (int)at;
 #pragma unroll
     for (int i = 0; i < kMaxE / 32; i++)
-      if (((left >> i) & 1u) && (be == 0x7fffffff || vals[i] > bv)) {
-        bv = vals[i];
-        be = lane + 32 * i;
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, bv, o);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-      if (ov > bv || (ov == bv && oe < be)) {
-        bv = ov;
-        be = oe;
-      }
-    }
-    if (lane == s) mine = be;
-    if ((be & 31) == lane) left &= ~(1u << (be >> 5));
+      if ((uint32_t)(lane + 32 * i) == at) key[i] = 0;
   }
   return mine;
 }
@@ -477,21 +475,35 @@ __device__ __forceinline__ void few_residual(const FewArgs &A, const uint8_t *ar
 // ---------------------------------------------------------------------------------------
 // Routing of every token and the segments of (token, slot) assignments by expert
 // ---------------------------------------------------------------------------------------
-// Relative cost of a tile of a segment with n tokens in phase 2 (the weights bound the first).
-__device__ __forceinline__ int few_cost(int n) { return n <= 8 ? 4 : 6; }
+// Relative cost of a tile in phase 2 (measured; the weights bound the first): segments of experts
+// of at most 4 tokens, of at most 8, of more.
+constexpr int kFewCost4 = 4, kFewCost8 = 6, kFewCostMore = 9;
 
 __device__ __forceinline__ void few_plan(const FewArgs &A, FewPlan &P) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int k = A.k, T = A.T, E = A.E;
   if (tid < kMaxE) P.tok[tid] = 0;
+  // a token a warp at a time; the next one's logits come while this one's are sorted
+  uint32_t key[kMaxE / 32];
+  int given = 0;
+  auto fetch = [&](int t) {
+    const float *lg = A.logits + (size_t)t * E;
+#pragma unroll
+    for (int i = 0; i < kMaxE / 32; i++) key[i] = lane + 32 * i < E ? __float_as_uint(lg[lane + 32 * i]) : 0xFFFFFFFFu;
+    if (A.route != nullptr && lane < k) given = A.route[(size_t)t * k + lane];
+  };
+  if (warp < T) fetch(warp);
 #pragma unroll 1
   for (int t = warp; t < T; t += kFewWarps) {
     const float *lg = A.logits + (size_t)t * E;
+    uint32_t now[kMaxE / 32];
     // lane j < k has the token's j-th expert
-    int e = 0, bad = 0;
-    if (A.route != nullptr && lane < k) e = A.route[(size_t)t * k + lane];
+    int e = given, bad = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxE / 32; i++) now[i] = lane + 32 * i < E ? few_key(__uint_as_float(key[i])) : 0u;
+    if (t + kFewWarps < T) fetch(t + kFewWarps);
     if (A.route == nullptr || __shfl_sync(0xffffffffu, e, 0) < 0) {
-      e = few_topk(lg, E, k, lane);
+      e = few_topk(now, k, lane);
     } else {
       if (e < 0 || e >= E) {
         bad = DERR_INDEX;
@@ -559,26 +571,19 @@ __device__ __forceinline__ void few_plan(const FewArgs &A, FewPlan &P) {
     P.seg_at[sg + i] = (uint16_t)(at + i * A.seg_cap);
     P.seg_n[sg + i] = (uint16_t)min(A.seg_cap, n - i * A.seg_cap);
   }
-  const int n4 = segs(total, 0), n8 = n4 + segs(total, 1), nseg = n8 + segs(total, 2);
+  // (with segments of 8 tokens the third class needs no form of its own)
+  const int n4 = segs(total, 0), nseg = n4 + segs(total, 1) + segs(total, 2);
+  const int n8 = A.seg_cap == 8 ? nseg : n4 + segs(total, 1);
   if (tid == 0) {
     P.n4 = n4;
     P.n8 = n8;
     P.nseg = nseg;
-    P.nplace = T * k + T;
   }
   __syncthreads();
   if (tid == 0) {
     P.nplace = P.seg_at[nseg - 1] + P.seg_n[nseg - 1];   // an expert given twice to a token has one place
     P.seg_at[nseg] = (uint16_t)P.nplace;
-    int c = n8 * few_cost(8);
-#pragma unroll 1
-    for (int s = n8; s < nseg; s++) {
-      P.cost_at[s] = c;
-      c += few_cost(P.seg_n[s]);
-    }
-    P.cost_at[nseg] = c;
   }
-  if (tid < n8) P.cost_at[tid] = tid * few_cost(8);
 #pragma unroll 1
   for (int i = tid; i < T * (k + 1); i += kFewThreads) {
     const int t = i / (k + 1), j = i % (k + 1);
@@ -618,8 +623,15 @@ struct FewCursor {
 };
 
 struct FewPart {                  // what a warp does of K, and where its team stands
-  int b0, b1, wk, team, sub, part;
+  int b0, b1, wk, team, sub;
 };
+
+__device__ __forceinline__ float dot8(uint4 w, float4 x, float4 y, float s) {
+  s = fmaf(__uint_as_float(w.x << 16), x.x, fmaf(__uint_as_float(w.x & 0xFFFF0000u), x.y, s));
+  s = fmaf(__uint_as_float(w.y << 16), x.z, fmaf(__uint_as_float(w.y & 0xFFFF0000u), x.w, s));
+  s = fmaf(__uint_as_float(w.z << 16), y.x, fmaf(__uint_as_float(w.z & 0xFFFF0000u), y.y, s));
+  return fmaf(__uint_as_float(w.w << 16), y.z, fmaf(__uint_as_float(w.w & 0xFFFF0000u), y.w, s));
+}
 
 // SwiGLU of one token (a lane's index l / 4 of tile i8 of segment s), with the shared expert's
 // LoRA; a to the workspace in operand order, and the sum of the tile's 8.
@@ -631,10 +643,20 @@ __device__ __noinline__ void few_emit(const FewPlan &P, int s, int i8, int tok, 
     const float *lt = A.lt + (size_t)(asg / (A.k + 1)) * 2 * A.r;
     const uint16_t *bg = A.Bg + (size_t)i * A.r, *bu = A.Bu + (size_t)i * A.r;
     float lg = 0.f, lu = 0.f;
-#pragma unroll 8
-    for (int j = 0; j < A.r; j++) {
-      lg = fmaf(bf(bg[j]), lt[j], lg);
-      lu = fmaf(bf(bu[j]), lt[A.r + j], lu);
+    if ((A.r & 7) == 0 && A.lora16) {
+#pragma unroll 2
+      for (int j = 0; j < A.r; j += 8) {
+        const uint4 wg = __ldg(reinterpret_cast<const uint4 *>(bg + j)), wu = __ldg(reinterpret_cast<const uint4 *>(bu + j));
+        const float4 *tg = reinterpret_cast<const float4 *>(lt + j), *tu = reinterpret_cast<const float4 *>(lt + A.r + j);
+        lg = dot8(wg, tg[0], tg[1], lg);
+        lu = dot8(wu, tu[0], tu[1], lu);
+      }
+    } else {
+#pragma unroll 2
+      for (int j = 0; j < A.r; j++) {
+        lg = fmaf(bf(bg[j]), lt[j], lg);
+        lu = fmaf(bf(bu[j]), lt[A.r + j], lu);
+      }
     }
     g = fmaf(A.c, lg, g);
     u = fmaf(A.c, lu, u);
@@ -651,9 +673,13 @@ __device__ __noinline__ void few_emit(const FewPlan &P, int s, int i8, int tok, 
 }
 
 // The join of a team's partial sums (red: [warp][16 rows][16 tokens]).
+// Barrier of a team: ids 1, 2 for teams of 8 warps, 3..6 of 4, 7..14 of 2 (two of the streams below
+// may be under way at once, with teams of different sizes).
+__device__ __forceinline__ int few_bar(int wk, int team) { return 16 / wk - 1 + team; }
+
 __device__ __noinline__ void few_join(const FewPlan &P, int s, int i8, int wk, int team, int sub, const float *red) {
   const int lane = threadIdx.x & 31, n = P.seg_n[s];
-  bar_team(1 + team, wk * 32);
+  bar_team(few_bar(wk, team), wk * 32);
   // 4 tokens of 8 indices to a warp at a time: lane = token + 4 index
   const float *base = red + team * wk * 256 + (lane >> 2) * 16;
 #pragma unroll 1
@@ -667,30 +693,34 @@ __device__ __noinline__ void few_join(const FewPlan &P, int s, int i8, int wk, i
     }
     few_emit(P, s, i8, tok, g, u);
   }
-  bar_team(1 + team, wk * 32);
+  bar_team(few_bar(wk, team), wk * 32);
 }
 
 // Streams a warp's tiles, blocks ahead across the end of a tile too.  Down: rows r0.. (nr of
-// them).  Sums go through few_emit / few_join, or (down) to out[place][16].
+// them), `depth` stages (2 to 4).  Sums go through few_emit / few_join, or (down) to
+// out[place][16].
 template <bool GU, bool WIDE, int N>
 __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, const FewOps &O, int p0, FewCursor<GU> C,
-                                           int step, int per, const FewPart &W, int r0, int nr, uint32_t zero, uint32_t ring,
-                                           float *out) {
+                                           int step, int per, const FewPart &W, int r0, int nr, int depth, uint32_t zero,
+                                           uint32_t ring, float *out) {
   if (C.left <= 0) return;
-  const int lane = threadIdx.x & 31, t = lane & 3, warp = threadIdx.x >> 5;
-  const int K = GU ? A.d : A.I, steps = K / 128;
-  // what this lane copies of a block: chunk l & 7 of rows l / 8 + 4 i, and the scales or mins of
-  // row l / 2
-  const int cr = lane >> 3, cc = lane & 7, sr = lane >> 1;
-  const uint32_t cdst = ring + cr * 128 + ((cc ^ few_swz(cr)) << 4), sdst = ring + 2048 + lane * 8;
-  const bool even = (steps & 1) == 0;
+  constexpr int TOK = N * (WIDE ? 8 : 4), STAGE = GU ? kFewStage : few_dn_stage(TOK);
+  const int lane = threadIdx.x & 31, t = lane & 3, r = lane >> 2, warp = threadIdx.x >> 5;
+  const int K = GU ? A.d : A.I, end = ring + (GU ? kFewDepth : depth) * STAGE;
+  // what this lane copies of a block.  Phase 2: chunk l & 7 of rows l / 8 + 4 i, the scales or mins
+  // of row l / 2.  Phase 3: chunk l & 3 of rows l / 4 and l / 4 + 8, the same of row l / 2, and
+  // chunk l & 15 of tokens l / 16 + 2 i.
+  const int cr = GU ? lane >> 3 : r, cc = GU ? lane & 7 : t, sr = lane >> 1;
+  const uint32_t cdst = GU ? cr * 128 + ((cc ^ few_swz(cr)) << 4) : cr * 64 + ((cc ^ (cr & 2)) << 4);
+  const uint32_t sdst = GU ? 2048 + lane * 8 : 1024 + lane * 4;
   FewCursor<GU> L = C;
-  int lb = W.b0, ls = 0;
+  int lb = W.b0;
+  uint32_t lst = ring;
   const uint8_t *blob = nullptr;
-  int co[4], so = 0;
+  int co[GU ? 4 : 2], so = 0;
   if (!GU) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) co[i] = (int)A.bl.dc + (r0 + min(cr + 4 * i, nr - 1)) * (K / 2) + cc * 16;
+    for (int i = 0; i < 2; i++) co[i] = (int)A.bl.dc + (r0 + min(cr + 8 * i, nr - 1)) * (K / 2) + cc * 16;
     so = (int)(lane & 1 ? A.bl.dm : A.bl.ds) + (r0 + min(sr, nr - 1)) * (K / 32);
   }
   auto issue = [&]() {
@@ -701,22 +731,25 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
         if (GU) {
           co[0] = (int)A.bl.gc + (L.i * 8 + cr) * (K / 2) + cc * 16;
           co[1] = co[0] + 4 * (K / 2);
-          co[2] = co[0] + (int)(A.bl.uc - A.bl.gc);
-          co[3] = co[2] + 4 * (K / 2);
+          co[GU ? 2 : 0] = co[0] + (int)(A.bl.uc - A.bl.gc);
+          co[GU ? 3 : 0] = co[GU ? 2 : 0] + 4 * (K / 2);
           so = (int)(lane & 1 ? A.bl.gm : A.bl.gs) + (sr < 8 ? 0 : (int)(A.bl.uc - A.bl.gc)) + (L.i * 8 + (sr & 7)) * (K / 32);
         }
       }
-      const bool whole = 2 * lb + 1 < steps;
-      if (whole || cc < 4)
 #pragma unroll
-        for (int i = 0; i < 4; i++) cp_async16(cdst + ls + i * 512, blob + co[i] + lb * 128);
-      if (even) {
-        cp_async_small<8>(sdst + ls, blob + so + lb * 8);
-      } else {
-        cp_async_small<4>(sdst + ls, blob + so + lb * 8);
-        if (whole) cp_async_small<4>(sdst + ls + 4, blob + so + lb * 8 + 4);
+      for (int i = 0; i < (GU ? 4 : 2); i++) cp_async16(lst + cdst + i * 512, blob + co[i] + lb * (GU ? 128 : 64));
+      cp_async_small<GU ? 8 : 4>(lst + sdst, blob + so + lb * (GU ? 8 : 4));
+      if (!GU) {
+        const int n = P.seg_n[L.s], at = P.seg_at[L.s];
+#pragma unroll
+        for (int i = 0; i < TOK / 2; i++) {
+          const int tok = (lane >> 4) + 2 * i;
+          if (tok < n)
+            cp_async16(lst + kFewDnHead + tok * kFewDnRow + (lane & 15) * 16,
+                       A.a + (size_t)P.asg[at + tok] * A.I + lb * 128 + (lane & 15) * 8);
+        }
       }
-      ls = ls == (kFewDepth - 1) * kFewStage ? 0 : ls + kFewStage;
+      lst = lst + STAGE == end ? ring : lst + STAGE;
       if (++lb == W.b1) {
         lb = W.b0;
         L.next(step, per);
@@ -725,46 +758,55 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
     cp_async_commit();
   };
   __syncwarp();                           // every lane has left the ring's last use
-#pragma unroll
-  for (int u = 0; u < kFewDepth - 1; u++) issue();
+#pragma unroll 1
+  for (int u = 1; u < (GU ? kFewDepth : depth); u++) issue();
   uint32_t st = ring;
-  Int4Acc<N> acc;
   FewCol<WIDE, N> X;
 #pragma unroll 1
   for (; C.left > 0; C.next(step, per)) {
     const int n = P.seg_n[C.s], at = P.seg_at[C.s];
-    acc.clear();
-    X.set(O, at - p0, n, zero);
+    float acc[N][4];
+#pragma unroll
+    for (int q = 0; q < N; q++) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
+    X.set(O, GU ? at - p0 : 0, at - p0, n, zero);
 #pragma unroll 1
     for (int b = W.b0; b < W.b1; b++) {
-      cp_async_wait_but<kFewDepth - 2>();
+      if (GU) cp_async_wait_but<kFewDepth - 2>(); else cp_async_wait_upto(depth - 2);
       __syncwarp();                       // the block has arrived, and every lane has left the one before
       issue();
-      few_mul<WIDE, N>(st, b, 2 * b + 1 < steps, X, acc);
-      st = st == ring + (kFewDepth - 1) * kFewStage ? ring : st + kFewStage;
+      if (GU) {
+        const uint4 ca = lds128(st + 2048 + r * 16), cb = lds128(st + 2048 + r * 16 + 128);
+        few_mul128<WIDE, N>(st + r * 128, 1024, 0, few_swz(r), ca.x, ca.z, cb.x, cb.z, X, 2 * b, b * 16, acc);
+        few_mul128<WIDE, N>(st + r * 128, 1024, 4, few_swz(r), ca.y, ca.w, cb.y, cb.w, X, 2 * b + 1, b * 16 + 8, acc);
+      } else {
+        const uint2 ca = lds64(st + 1024 + r * 8), cb = lds64(st + 1024 + r * 8 + 64);
+        FewCol<WIDE, N> Y = X;            // the stage's own columns
+#pragma unroll
+        for (int q = 0; q < N; q++) Y.x[q] = X.step ? X.x[q] + st : zero;
+        few_mul128<WIDE, N>(st + r * 64, 512, 0, r & 2, ca.x, ca.y, cb.x, cb.y, Y, 0, b * 8, acc);
+      }
+      st = st + STAGE == end ? ring : st + STAGE;
     }
     // pair: lanes l and l + 2 hold the same two tokens and take one each; wide: both tokens
 #pragma unroll
     for (int q = 0; q < N; q++) {
-      if (!WIDE) {
-        acc.a[q] = f2add(acc.a[q], __shfl_xor_sync(0xffffffffu, acc.a[q], 2));
-        acc.b[q] = f2add(acc.b[q], __shfl_xor_sync(0xffffffffu, acc.b[q], 2));
-      }
+      if (!WIDE)
+#pragma unroll
+        for (int i = 0; i < 4; i++) acc[q][i] += __shfl_xor_sync(0xffffffffu, acc[q][i], 2);
 #pragma unroll
       for (int j = 0; j < (WIDE ? 2 : 1); j++) {
         const int odd = WIDE ? j : t >> 1, tok = WIDE ? 8 * q + 2 * t + j : 4 * q + 2 * (t & 1) + odd;
-        const float va = __uint_as_float((uint32_t)(acc.a[q] >> (32 * odd)));
-        const float vb = __uint_as_float((uint32_t)(acc.b[q] >> (32 * odd)));
+        const float va = odd ? acc[q][1] : acc[q][0], vb = odd ? acc[q][3] : acc[q][2];
         if (!GU) {
           if (tok < n) {
-            float *p = out + (size_t)(at + tok) * 16 + (lane >> 2);
+            float *p = out + (size_t)(at + tok) * 16 + r;
             p[0] = va;
             p[8] = vb;
           }
         } else if (W.wk == 1) {
           few_emit(P, C.s, C.i, tok, va, vb);
         } else if (tok < n) {
-          float *p = out + warp * 256 + (lane >> 2) * 16 + tok;
+          float *p = out + warp * 256 + r * 16 + tok;
           p[0] = va;
           p[128] = vb;
         }
@@ -774,46 +816,44 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
   }
 }
 
-// Copies of the activation rows at places [p0, p1) and their sums by group of 64, G groups.
-template <class X, class V>
-__device__ __forceinline__ FewOps few_stage(const FewPlan &P, int p0, int p1, int G, uint8_t *area, X x, V v) {
-  const int n = p1 - p0, pitch = G * 128 + kFewPad, C = G * 8, lane = threadIdx.x & 31;
+// ---------------------------------------------------------------------------------------
+// Phase 2
+// ---------------------------------------------------------------------------------------
+// Copies of the x rows of the assignments at places [p0, p1) and their sums by group of 64.
+__device__ __forceinline__ FewOps few_stage(const FewArgs &A, const FewPlan &P, int p0, int p1, uint8_t *area) {
+  const int n = p1 - p0, G = A.d / 64, pitch = A.d * 2 + kFewPad, lane = threadIdx.x & 31;
   const FewOps O{smem_at(area), smem_at(area + (size_t)n * pitch), pitch, G * 4};
-  float *sums = reinterpret_cast<float *>(area + (size_t)n * pitch);
 #pragma unroll 1
   for (int r = threadIdx.x >> 5; r < n; r += kFewWarps) {
-    const int asg = P.asg[p0 + r];
-    const uint16_t *src = x(asg);
+    const int tok = P.asg[p0 + r] / (A.k + 1);
+    const uint16_t *x = A.xb + (size_t)tok * A.d;
 #pragma unroll 1
-    for (int c = lane; c < C; c += 32) cp_async16(O.x + r * pitch + c * 16, src + c * 8);
-#pragma unroll 1
-    for (int g = lane; g < G; g += 32) sums[r * G + g] = v(asg, g);
+    for (int c = lane; c < A.d / 8; c += 32) cp_async16(O.x + r * pitch + c * 16, x + c * 8);
+    // d is a multiple of 256: G of 4
+    if (lane < G / 4) cp_async16(O.v + r * O.vp + lane * 16, A.xv + (size_t)tok * G + lane * 4);
   }
   return O;
 }
 
-// ---------------------------------------------------------------------------------------
-// Phase 2
-// ---------------------------------------------------------------------------------------
-// Tile at which block b's share begins: an equal share of the cost of all tiles.
+// Tile at which block b's share begins: an equal share of the cost of all tiles.  (At most 329
+// segments of 512 tiles of cost 9, times 148 or so: 32 bits.)
 __device__ __forceinline__ void few_bound(const FewPlan &P, int per, int b, int &s, int &f) {
-  const long long pos = (long long)P.cost_at[P.nseg] * per * b / (int)gridDim.x;
-  int l = 0, h = P.nseg;
-#pragma unroll 1
-  while (l + 1 < h) {
-    const int m = (l + h) >> 1;
-    if ((long long)P.cost_at[m] * per <= pos) l = m; else h = m;
+  const unsigned c1 = (unsigned)(P.n4 * per) * kFewCost4, c2 = (unsigned)((P.n8 - P.n4) * per) * kFewCost8;
+  const unsigned c3 = (unsigned)((P.nseg - P.n8) * per) * kFewCostMore;
+  unsigned pos = (unsigned)((unsigned long long)(c1 + c2 + c3) * b / gridDim.x), tile;
+  if (pos < c1) {
+    tile = pos / kFewCost4;
+  } else if (pos < c1 + c2) {
+    tile = P.n4 * per + (pos - c1) / kFewCost8;
+  } else {
+    tile = P.n8 * per + (pos - c1 - c2) / kFewCostMore;
   }
-  s = l;
-  f = (int)(pos - (long long)P.cost_at[l] * per) / (P.cost_at[l + 1] - P.cost_at[l]);
-  if (f >= per) {
-    s = l + 1;
-    f = 0;
-  }
+  s = tile / per;
+  f = tile % per;
 }
 
 __device__ __forceinline__ void few_phase2(const FewArgs &A, const FewPlan &P, uint8_t *area, uint32_t zero, uint32_t ring, float *red) {
-  const int per = A.I / 8, G = A.d / 64, NB = A.d / 256, warp = threadIdx.x >> 5;
+  const int per = A.I / 8, NB = A.d / 256, warp = threadIdx.x >> 5;
   int sl, fl, sh, fh;
   few_bound(P, per, blockIdx.x, sl, fl);
   few_bound(P, per, blockIdx.x + 1, sh, fh);
@@ -826,11 +866,7 @@ __device__ __forceinline__ void few_phase2(const FewArgs &A, const FewPlan &P, u
     while (s1 < s_end && P.seg_at[s1 + 1] - P.seg_at[s0] <= A.gu_rows) s1++;
     const int p0 = P.seg_at[s0];
     __syncthreads();
-    const uint16_t *xb = A.xb;
-    const float *xv = A.xv;
-    const int k1 = A.k + 1, d = A.d;
-    const FewOps O = few_stage(P, p0, P.seg_at[s1], G, area, [=](int asg) { return xb + (size_t)(asg / k1) * d; },
-                               [=](int asg, int g) { return xv[(size_t)(asg / k1) * G + g]; });
+    const FewOps O = few_stage(A, P, p0, P.seg_at[s1], area);
     cp_async_wait();
     __syncthreads();
     // the tiles of segments [a, b) of these: warps to a tile by their number, no more than there
@@ -840,10 +876,10 @@ __device__ __forceinline__ void few_phase2(const FewArgs &A, const FewPlan &P, u
       b = min(b, s1);
       const int f0 = a == sl ? fl : 0, f1 = b == s_end && fh > 0 ? fh : per;
       const int tiles = a < b ? (b - a - 1) * per - f0 + f1 : 0;
-      int wk = tiles <= 2 ? 8 : tiles <= 4 ? 4 : tiles <= 8 ? 2 : 1;
-      while (wk > NB) wk >>= 1;
-      const int sub = warp % wk, team = warp / wk, teams = kFewWarps / wk;
-      W = FewPart{NB * sub / wk, NB * (sub + 1) / wk, wk, team, sub, 0};
+      int lg = tiles <= 2 ? 3 : tiles <= 4 ? 2 : tiles <= 8 ? 1 : 0;
+      while ((1 << lg) > NB) lg--;
+      const int wk = 1 << lg, sub = warp & (wk - 1), team = warp >> lg, teams = kFewWarps >> lg;
+      W = FewPart{NB * sub >> lg, NB * (sub + 1) >> lg, wk, team, sub};
       C = FewCursor<true>{a, f0 + team, (tiles - team + teams - 1) / teams};
       while (C.i >= per) {
         C.i -= per;
@@ -853,14 +889,18 @@ __device__ __forceinline__ void few_phase2(const FewArgs &A, const FewPlan &P, u
     };
     FewCursor<true> C;
     FewPart W;
-    int step = share(n8, P.nseg, C, W);
-    few_stream<true, true, 2>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
-    __syncthreads();
-    step = share(n4, n8, C, W);
-    few_stream<true, false, 2>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
-    __syncthreads();
-    step = share(0, n4, C, W);
-    few_stream<true, false, 1>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
+    if (n8 < s1) {
+      const int step = share(n8, P.nseg, C, W);
+      few_stream<true, true, 2>(A, P, O, p0, C, step, per, W, 0, 0, 0, zero, ring, red);
+    }
+    if (n4 < s1 && s0 < n8) {
+      const int step = share(n4, n8, C, W);
+      few_stream<true, false, 2>(A, P, O, p0, C, step, per, W, 0, 0, 0, zero, ring, red);
+    }
+    if (s0 < n4) {
+      const int step = share(0, n4, C, W);
+      few_stream<true, false, 1>(A, P, O, p0, C, step, per, W, 0, 0, 0, zero, ring, red);
+    }
     s0 = s1;
   }
 }
@@ -892,61 +932,64 @@ __device__ __forceinline__ int few_td(const FewArgs &A, float *td) {
   return split;
 }
 
-__device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, uint8_t *area, uint32_t zero, uint32_t ring, float *td) {
+// area: t_d, the results, the sums of the activations, the rings
+__device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, uint8_t *area, uint32_t zero) {
   const int tid = threadIdx.x, warp = tid >> 5;
   const int lo = (int)((long long)A.d * blockIdx.x / gridDim.x), hi = (int)((long long)A.d * (blockIdx.x + 1) / gridDim.x);
   if (lo >= hi) return;
-  const int G = A.I / 64, NB = (G + 3) / 4, k1 = A.k + 1, nplace = P.nplace;
-  float *out = reinterpret_cast<float *>(area);
-  uint8_t *stage = area + A.out_bytes;
+  const int G = A.I / 64, NB = A.I / 128, k1 = A.k + 1, nplace = P.nplace;
+  float *td = reinterpret_cast<float *>(area), *out = reinterpret_cast<float *>(area + kFewRedBytes);
+  float *sums = reinterpret_cast<float *>(area + kFewRedBytes + A.out_bytes);
+  const uint32_t ring = smem_at(sums) + ((A.dn_rows * G * 4 + 15) & ~15) + warp * A.dn_ring;
   bool first = true;
 #pragma unroll 1
   for (int r0 = lo; r0 < hi; r0 += 16) {
     const int nr = min(16, hi - r0);
     // parts of K: more where there are few segments to keep the warps busy
-    int parts = 1;
-    while (parts < 4 && P.nseg * parts * 2 <= kFewWarps && 2 * parts <= NB && 2 * parts * nplace * 64 <= A.out_bytes)
-      parts *= 2;
+    int lg = 0;
+    while (lg < 2 && (P.nseg << (lg + 1)) <= kFewWarps && (2 << lg) <= NB && (2 << lg) * nplace * 64 <= A.out_bytes) lg++;
     // 16 warps are a multiple of the parts, so a warp stays with one part
-    const int part = warp % parts, team = warp / parts, step = kFewWarps / parts;
-    const FewPart W{NB * part / parts, NB * (part + 1) / parts, 1, 0, 0, part};
+    const int parts = 1 << lg, part = warp & (parts - 1), team = warp >> lg, step = kFewWarps >> lg;
+    const FewPart W{NB * part >> lg, NB * (part + 1) >> lg, 1, 0, 0};
     float *o = out + (size_t)part * nplace * 16;
 #pragma unroll 1
     for (int s0 = 0; s0 < P.nseg;) {
-      int s1 = s0 + 1;
+      int s1 = P.nseg;
+      if (nplace > A.dn_rows) {
+        s1 = s0 + 1;
 #pragma unroll 1
-      while (s1 < P.nseg && P.seg_at[s1 + 1] - P.seg_at[s0] <= A.dn_rows) s1++;
-      const int p0 = P.seg_at[s0];
+        while (s1 < P.nseg && P.seg_at[s1 + 1] - P.seg_at[s0] <= A.dn_rows) s1++;
+      }
+      const int p0 = P.seg_at[s0], p1 = P.seg_at[s1];
       __syncthreads();
-      const uint16_t *a = A.a;
-      const float *a8 = A.a8;
-      const int I = A.I;
-      const FewOps O = few_stage(P, p0, P.seg_at[s1], G, stage, [=](int asg) { return a + (size_t)asg * I; },
-                                 [=](int asg, int g) {
-                                   const float4 *p = reinterpret_cast<const float4 *>(a8 + (size_t)asg * (I / 8) + g * 8);
-                                   const float4 u = p[0], w = p[1];
-                                   return ((u.x + u.y) + (u.z + u.w)) + ((w.x + w.y) + (w.z + w.w));
-                                 });
-      if (A.Ad && first) {
-        const int split = few_td(A, td);
-        __syncthreads();
-        float v = 0.f;                    // one (token, rank) a thread and round: T r <= 2048
+      const int split = A.Ad && first ? few_td(A, td) : 0;
+      // sums by group of 64 of the tiles' sums
+#pragma unroll 1
+      for (int u = tid; u < (p1 - p0) * G; u += kFewThreads) {
+        const int p = u / G, g = u - p * G;
+        const float4 *q = reinterpret_cast<const float4 *>(A.a8 + (size_t)P.asg[p0 + p] * (A.I / 8) + g * 8);
+        const float4 v = q[0], w = q[1];
+        sums[u] = ((v.x + v.y) + (v.z + v.w)) + ((w.x + w.y) + (w.z + w.w));
+      }
+      __syncthreads();
+      if (split > 1) {
+        // each column is read and written by one thread, and read by others after the barrier below
 #pragma unroll 1
         for (int u = tid; u < A.T * kMaxR; u += kFewThreads) {
-          v = 0.f;
+          float v = td[u];
 #pragma unroll 4
-          for (int w = 0; w < split; w++) v += td[w * A.T * kMaxR + u];
-          td[u] = v;                      // only this thread reads or writes column u
+          for (int w = 1; w < split; w++) v += td[w * A.T * kMaxR + u];
+          td[u] = v;
         }
       }
       first = false;
-      cp_async_wait();
-      __syncthreads();
+      const FewOps O{kFewDnHead, smem_at(sums), kFewDnRow, G * 4};
       const int m4 = max(s0, min(s1, P.n4)), m8 = max(m4, min(s1, P.n8));
-      auto cursor = [&](int a, int b) { return FewCursor<false>{a + team, 0, (b - a - team + step - 1) / step}; };
-      few_stream<false, true, 2>(A, P, O, p0, cursor(m8, s1), step, 0, W, r0, nr, zero, ring, o);
-      few_stream<false, false, 2>(A, P, O, p0, cursor(m4, m8), step, 0, W, r0, nr, zero, ring, o);
-      few_stream<false, false, 1>(A, P, O, p0, cursor(s0, m4), step, 0, W, r0, nr, zero, ring, o);
+      auto cursor = [&](int a, int b) { return FewCursor<false>{a + team, 0, (b - a - team + step - 1) >> (4 - lg)}; };
+      auto depth = [&](int tokens) { return min(4, A.dn_ring / few_dn_stage(tokens)); };
+      if (m8 < s1) few_stream<false, true, 2>(A, P, O, p0, cursor(m8, s1), step, 0, W, r0, nr, depth(16), zero, ring, o);
+      if (m4 < m8) few_stream<false, false, 2>(A, P, O, p0, cursor(m4, m8), step, 0, W, r0, nr, depth(8), zero, ring, o);
+      if (s0 < m4) few_stream<false, false, 1>(A, P, O, p0, cursor(s0, m4), step, 0, W, r0, nr, depth(4), zero, ring, o);
       s0 = s1;
     }
     __syncthreads();
@@ -964,9 +1007,18 @@ __device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, u
         y = j < A.k ? fmaf(P.gate[t * A.k + j], v, y) : y + v;
       }
       if (A.Ad) {
+        const uint16_t *bd = A.Bd + (size_t)row * A.r;
+        const float *tv = td + t * kMaxR;
         float b = 0.f;
-#pragma unroll 8
-        for (int j = 0; j < A.r; j++) b = fmaf(bf(A.Bd[(size_t)row * A.r + j]), td[t * kMaxR + j], b);
+        if ((A.r & 7) == 0 && A.lora16) {
+#pragma unroll 2
+          for (int j = 0; j < A.r; j += 8)
+            b = dot8(__ldg(reinterpret_cast<const uint4 *>(bd + j)), *reinterpret_cast<const float4 *>(tv + j),
+                     *reinterpret_cast<const float4 *>(tv + j + 4), b);
+        } else {
+#pragma unroll 2
+          for (int j = 0; j < A.r; j++) b = fmaf(bf(bd[j]), tv[j], b);
+        }
         y = fmaf(A.c, b, y);
       }
       A.y[(size_t)t * A.d + row] = f2bf(y);
@@ -993,7 +1045,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_moe_few(const __grid_constan
   few_plan(A, P);
   few_phase2(A, P, area, smem_at(zero), ring, red);
   grid.sync();
-  few_phase3(A, P, area, smem_at(zero), ring, red);
+  few_phase3(A, P, red_area, smem_at(zero));
 }
 
 }  // namespace e0
