@@ -2147,7 +2147,7 @@ extern "C" int e0_int4_linear(const e0_int4_mat *w, const void *x, int x_format,
 
 // Workspace regions of e0_moe_layer_few, 256-byte aligned.
 struct FewSpace {
-  size_t xb, xv, logits, lt, a, a8, bytes;
+  size_t xb, xv, logits, lt, rsel, rgate, a, a8, bytes;
 };
 static FewSpace few_space(const e0_dims &D, int T) {
   const size_t d = D.d_model, E = D.n_experts, I = D.d_ff, k = D.top_k, r = D.lora_rank;
@@ -2156,6 +2156,8 @@ static FewSpace few_space(const e0_dims &D, int T) {
   S.xv = S.bytes;     S.bytes += noalloc_align((size_t)T * (d / 64) * 4);
   S.logits = S.bytes; S.bytes += noalloc_align((size_t)T * E * 4);
   S.lt = S.bytes;     S.bytes += noalloc_align((size_t)T * 2 * r * 4);
+  S.rsel = S.bytes;   S.bytes += noalloc_align((size_t)T * k * 4);
+  S.rgate = S.bytes;  S.bytes += noalloc_align((size_t)T * k * 4);
   S.a = S.bytes;      S.bytes += noalloc_align((size_t)T * (k + 1) * I * 2);
   S.a8 = S.bytes;     S.bytes += noalloc_align((size_t)T * (k + 1) * (I / 8) * 4);
   return S;
@@ -2202,6 +2204,7 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
   A.h_out = (uint16_t *)h_out; A.y = (uint16_t *)y_bf16; A.yf = y_f32; A.idx = idx_out; A.gates = gate_out;
   uint8_t *ws = (uint8_t *)workspace;
   A.xb = (uint16_t *)(ws + S.xb); A.logits = (float *)(ws + S.logits); A.lt = (float *)(ws + S.lt);
+  A.rsel = (int32_t *)(ws + S.rsel); A.rgate = (float *)(ws + S.rgate);
   A.a = (uint16_t *)(ws + S.a); A.xv = (float *)(ws + S.xv); A.a8 = (float *)(ws + S.a8);
   A.err = dev_status;
   int dev = 0, nsm = 0, coop = 0, most = 0;
@@ -2209,7 +2212,7 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
   CK(cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev));
   CK(cudaDeviceGetAttribute(&coop, cudaDevAttrCooperativeLaunch, dev));
   CK(cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev));
-  if (!coop || nsm < (kFewMaxT + 7) / 8) return fail(E0_ERR_CUDA, "moe_layer_few: the device has no cooperative launch");
+  if (!coop || nsm < kFewWarps) return fail(E0_ERR_CUDA, "moe_layer_few: the device has no cooperative launch");
   // shared memory: phase 2 holds the rings and as many activation rows as the rest takes; phase 3
   // t_d, the results of every (token, slot), the sums of their activations and the rings, at least
   // two stages each.  Tokens of a segment: 16 where both phases have room for them, else 8.
@@ -2225,7 +2228,7 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
   A.dn_ring = (rest - A.out_bytes - (A.dn_rows * sum_bytes + 15) / 16 * 16) / kFewWarps / 16 * 16;
   if (A.gu_rows < 8 || A.dn_rows < std::min(places, A.seg_cap))
     return fail(E0_ERR_INVALID_ARG, "moe_layer_few: dims too large for the shared memory");
-  A.tpb = T <= 8 ? 1 : T <= 16 ? 2 : T <= 32 ? 4 : 8;
+  A.tpb = T <= 16 ? 1 : T <= 32 ? 2 : 4;
   A.lora16 = !misaligned(Y.lora_Bg, 16) && !misaligned(Y.lora_Bu, 16) && !misaligned(Y.lora_Bd, 16);
   CK(cudaFuncSetAttribute(k_moe_few, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   void *args[] = {&A};

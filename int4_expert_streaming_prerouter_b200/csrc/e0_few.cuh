@@ -61,6 +61,8 @@ struct FewArgs {
   float *xv;                  // [T][d / 64] sums of x
   float *logits;              // [T][E]
   float *lt;                  // [T][2][r]
+  int32_t *rsel;              // [T][k] routing and gates, where one block routes for all
+  float *rgate;
   uint16_t *a;                // [T][k + 1][I], channels in operand order
   float *a8;                  // [T][k + 1][I / 8] sums of a
   int *err;
@@ -196,11 +198,11 @@ struct FewOps {
 };
 
 // A lane's columns: N tiles of tokens (wide: 8 each, pair: 4), n tokens in all, at row `at` of x
-// and `vat` of the sums.  step: bytes from 128 channels to the next.
+// and `vat` of the sums; advanced by 128 channels at a time.
 template <bool WIDE, int N>
 struct FewCol {
   uint32_t x[N], v0[N], v1[N];
-  int step;
+  uint32_t step;              // bytes from 128 channels to the next: 256, or 0 at the zeros
   __device__ __forceinline__ void set(const FewOps &O, int at, int vat, int n, uint32_t zero) {
     const int lane = threadIdx.x & 31, t = lane & 3, c = lane >> 2;
     const bool mine = WIDE || (t >> 1) == (c >> 2);
@@ -211,6 +213,14 @@ struct FewCol {
       x[q] = mine ? O.x + (at + min(tok, n - 1)) * O.pitch + (WIDE ? t * 32 : t * 64) : zero;
       v0[q] = O.v + (vat + min(pair, n - 1)) * O.vp + (WIDE ? 0 : (t >> 1) * 4);
       v1[q] = O.v + (vat + min(pair + 1, n - 1)) * O.vp + (WIDE ? 0 : (t >> 1) * 4);
+    }
+  }
+  __device__ __forceinline__ void advance(uint32_t xs) {
+#pragma unroll
+    for (int q = 0; q < N; q++) {
+      x[q] += xs;
+      v0[q] += 8;
+      v1[q] += 8;
     }
   }
 };
@@ -236,18 +246,17 @@ __device__ __forceinline__ void few_fold(const float (&p)[N][4], uint32_t wsa, u
   }
 }
 
-// 128 channels: codes of the lane's rows at `row` (the row's address) and `row` + half (8 rows on),
-// chunks permuted by swz, the first at chunk c0; scale words (s, m of rows l / 4, l / 4 + 8) of the
-// two groups; columns at byte offset xo (pair: times step / 256), sums at vo.
-template <bool WIDE, int N>
-__device__ __forceinline__ void few_mul128(uint32_t row, int half, int c0, int swz, uint32_t wsa, uint32_t wma, uint32_t wsb,
-                                           uint32_t wmb, const FewCol<WIDE, N> &X, int xs, int vo, float (&acc)[N][4]) {
+// 128 channels: the lane's codes at shared address w0 (pair: 16 bytes; wide: 8 bytes, those of the
+// second group at w1), `HALF` bytes on those of 8 rows further; scale words (s, m of rows l / 4,
+// l / 4 + 8) of the two groups.
+template <bool WIDE, int N, int HALF>
+__device__ __forceinline__ void few_mul128(uint32_t w0, uint32_t w1, uint32_t wsa, uint32_t wma, uint32_t wsb, uint32_t wmb,
+                                           const FewCol<WIDE, N> &X, float (&acc)[N][4]) {
   const int t = threadIdx.x & 3;
   if (WIDE) {
 #pragma unroll
     for (int g = 0; g < 2; g++) {
-      const uint32_t at = row + (((c0 + 2 * g + (t >> 1)) ^ swz) << 4) + (t & 1) * 8;
-      const uint2 wa = lds64(at), wb = lds64(at + half);
+      const uint2 wa = lds64(g ? w1 : w0), wb = lds64((g ? w1 : w0) + HALF);
       float p[N][4];
 #pragma unroll
       for (int w = 0; w < 2; w++) {
@@ -256,17 +265,16 @@ __device__ __forceinline__ void few_mul128(uint32_t row, int half, int c0, int s
         const uint32_t b0 = code_pair(xb, 0), b1 = code_pair(xb, 1), b2 = code_pair(xb, 2), b3 = code_pair(xb, 3);
 #pragma unroll
         for (int q = 0; q < N; q++) {
-          const uint4 x = lds128(X.x[q] + xs * 256 + g * 128 + w * 16);
+          const uint4 x = lds128(X.x[q] + g * 128 + w * 16);
           if (w == 0) mma_bf16_first(p[q], a0, b0, a1, b1, x.x, x.y);
           else mma_bf16_acc(p[q], a0, b0, a1, b1, x.x, x.y);
           mma_bf16_acc(p[q], a2, b2, a3, b3, x.z, x.w);
         }
       }
-      few_fold<N>(p, wsa, wma, wsb, wmb, g ? 0x3244u : 0x1044u, X.v0, X.v1, vo + g * 4, acc);
+      few_fold<N>(p, wsa, wma, wsb, wmb, g ? 0x3244u : 0x1044u, X.v0, X.v1, g * 4, acc);
     }
   } else {
-    const uint32_t at = row + (((c0 + t) ^ swz) << 4);
-    const uint4 wa = lds128(at), wb = lds128(at + half);
+    const uint4 wa = lds128(w0), wb = lds128(w0 + HALF);
     float p[N][4];
 #pragma unroll
     for (int w = 0; w < 4; w++) {
@@ -276,13 +284,13 @@ __device__ __forceinline__ void few_mul128(uint32_t row, int half, int c0, int s
       const uint32_t b0 = code_pair(xb, 0), b1 = code_pair(xb, 1), b2 = code_pair(xb, 2), b3 = code_pair(xb, 3);
 #pragma unroll
       for (int q = 0; q < N; q++) {
-        const uint4 x = lds128(X.x[q] + xs * X.step + w * 16);
+        const uint4 x = lds128(X.x[q] + w * 16);
         if (w == 0) mma_bf16_first(p[q], a0, b0, a1, b1, x.x, x.y);
         else mma_bf16_acc(p[q], a0, b0, a1, b1, x.x, x.y);
         mma_bf16_acc(p[q], a2, b2, a3, b3, x.z, x.w);
       }
     }
-    few_fold<N>(p, wsa, wma, wsb, wmb, t >> 1 ? 0x3244u : 0x1044u, X.v0, X.v1, vo, acc);
+    few_fold<N>(p, wsa, wma, wsb, wmb, t >> 1 ? 0x3244u : 0x1044u, X.v0, X.v1, 0, acc);
   }
 }
 
@@ -319,10 +327,10 @@ __device__ __forceinline__ int few_topk(uint32_t (&key)[kMaxE / 32], int k, int 
 // ---------------------------------------------------------------------------------------
 // Phase 1
 // ---------------------------------------------------------------------------------------
-// The block's tokens (at most 8) normed into rows at `area` (operand order) with their sums, h'
+// The block's tokens (at most 4) normed into rows at `area` (operand order) with their sums, h'
 // behind them, then the block's rows of [router; A_g; A_u].  Every block of the same tokens norms
 // them again, which costs less than a grid-wide barrier; so a block has few tokens, and more rows,
-// as long as there are blocks (`tpb` is T / 8, rounded up to a power of two).
+// as long as there are blocks (`tpb` is T / 16, rounded up to a power of two).
 struct FewTok {
   int ntb, tb, member, members, t0, nt;
   __device__ __forceinline__ explicit FewTok(const FewArgs &A) {
@@ -475,6 +483,53 @@ __device__ __forceinline__ void few_residual(const FewArgs &A, const uint8_t *ar
 // ---------------------------------------------------------------------------------------
 // Routing of every token and the segments of (token, slot) assignments by expert
 // ---------------------------------------------------------------------------------------
+// A warp takes one token: lane j < k gets its j-th expert and gate.  `say`: report bad routing.
+__device__ __forceinline__ void few_route(const FewArgs &A, int t, bool say, int &e, float &gate) {
+  const int lane = threadIdx.x & 31, k = A.k, E = A.E;
+  const float *lg = A.logits + (size_t)t * E;
+  uint32_t key[kMaxE / 32];
+  e = -1;
+  if (A.route != nullptr && lane < k) e = A.route[(size_t)t * k + lane];
+#pragma unroll
+  for (int i = 0; i < kMaxE / 32; i++) key[i] = lane + 32 * i < E ? few_key(lg[lane + 32 * i]) : 0u;
+  if (__shfl_sync(0xffffffffu, e, 0) < 0) {
+    e = few_topk(key, k, lane);
+  } else {
+    int bad = 0;
+    if (e < 0 || e >= E) {
+      bad = DERR_INDEX;
+      e = 0;
+    }
+    const unsigned same = __match_any_sync(0xffffffffu, lane < k ? e : -1 - lane);
+    if (same & (same - 1)) bad |= DERR_DUP;
+    if (say && lane < k && bad && A.err) atomicOr(A.err, bad);
+  }
+  const float l = lane < k ? lg[e] : -INFINITY;
+  float mx = l;
+#pragma unroll
+  for (int o = kMaxK / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float ex = lane < k ? expf(l - mx) : 0.f;
+  gate = ex / group_sum(ex, kMaxK);
+}
+
+// Up to this many tokens, every block routes all of them, a warp a token; beyond, each token is
+// routed by one block and a second grid-wide barrier (1.3 us) hands the result round.
+constexpr int kFewRouteAll = kFewWarps;
+
+__device__ __forceinline__ void few_route_share(const FewArgs &A) {
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x >= 32) return;
+  for (int t = blockIdx.x; t < A.T; t += gridDim.x) {
+    int e;
+    float g;
+    few_route(A, t, true, e, g);
+    if (lane < A.k) {
+      A.rsel[t * A.k + lane] = e;
+      A.rgate[t * A.k + lane] = g;
+    }
+  }
+}
+
 // Relative cost of a tile in phase 2 (measured; the weights bound the first): segments of experts
 // of at most 4 tokens, of at most 8, of more.
 constexpr int kFewCost4 = 4, kFewCost8 = 6, kFewCostMore = 9;
@@ -482,56 +537,30 @@ constexpr int kFewCost4 = 4, kFewCost8 = 6, kFewCostMore = 9;
 __device__ __forceinline__ void few_plan(const FewArgs &A, FewPlan &P) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int k = A.k, T = A.T, E = A.E;
+  static_assert(kFewMaxT * kMaxK <= kFewThreads && kMaxE < kFewThreads, "an assignment, an expert a thread");
   if (tid < kMaxE) P.tok[tid] = 0;
-  // a token a warp at a time; the next one's logits come while this one's are sorted
-  uint32_t key[kMaxE / 32];
-  int given = 0;
-  auto fetch = [&](int t) {
-    const float *lg = A.logits + (size_t)t * E;
-#pragma unroll
-    for (int i = 0; i < kMaxE / 32; i++) key[i] = lane + 32 * i < E ? __float_as_uint(lg[lane + 32 * i]) : 0xFFFFFFFFu;
-    if (A.route != nullptr && lane < k) given = A.route[(size_t)t * k + lane];
-  };
-  if (warp < T) fetch(warp);
-#pragma unroll 1
-  for (int t = warp; t < T; t += kFewWarps) {
-    const float *lg = A.logits + (size_t)t * E;
-    uint32_t now[kMaxE / 32];
-    // lane j < k has the token's j-th expert
-    int e = given, bad = 0;
-#pragma unroll
-    for (int i = 0; i < kMaxE / 32; i++) now[i] = lane + 32 * i < E ? few_key(__uint_as_float(key[i])) : 0u;
-    if (t + kFewWarps < T) fetch(t + kFewWarps);
-    if (A.route == nullptr || __shfl_sync(0xffffffffu, e, 0) < 0) {
-      e = few_topk(now, k, lane);
-    } else {
-      if (e < 0 || e >= E) {
-        bad = DERR_INDEX;
-        e = 0;
-      }
-      const unsigned same = __match_any_sync(0xffffffffu, lane < k ? e : -1 - lane);
-      if (same & (same - 1)) bad |= DERR_DUP;
-    }
-    const float l = lane < k ? lg[e] : -INFINITY;
-    float mx = l;
-#pragma unroll
-    for (int o = kMaxK / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float ex = lane < k ? expf(l - mx) : 0.f, g = ex / group_sum(ex, kMaxK);
-    if (lane < k) {
-      P.sel[t * k + lane] = (uint16_t)e;
-      P.gate[t * k + lane] = g;
-      if (blockIdx.x == 0) {
-        if (A.idx) A.idx[(size_t)t * k + lane] = e;
-        if (A.gates) A.gates[(size_t)t * k + lane] = g;
-        if (bad && A.err) atomicOr(A.err, bad);
+  if (T <= kFewRouteAll) {
+    if (warp < T) {
+      int e;
+      float g;
+      few_route(A, warp, blockIdx.x == 0, e, g);
+      if (lane < k) {
+        P.sel[warp * k + lane] = (uint16_t)e;
+        P.gate[warp * k + lane] = g;
       }
     }
+  } else if (tid < T * k) {
+    P.sel[tid] = (uint16_t)A.rsel[tid];
+    P.gate[tid] = A.rgate[tid];
   }
   __syncthreads();
+  if (blockIdx.x == 0 && tid < T * k) {
+    if (A.idx) A.idx[tid] = P.sel[tid];
+    if (A.gates) A.gates[tid] = P.gate[tid];
+  }
   // The rank of a token among those of its expert is a count of bits, so every block comes to
   // the same segments (an expert with more tokens than a segment holds has several, which
   // different blocks work on).
-  static_assert(kFewMaxT * kMaxK <= kFewThreads && kMaxE < kFewThreads, "an assignment, an expert a thread");
   if (tid < T * k) atomicOr(&P.tok[P.sel[tid]], 1ull << (tid / k));
   __syncthreads();
   // Places and segments by one prefix sum over the experts, a thread each: experts of at most 4
@@ -709,45 +738,65 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
   const int K = GU ? A.d : A.I, end = ring + (GU ? kFewDepth : depth) * STAGE;
   // what this lane copies of a block.  Phase 2: chunk l & 7 of rows l / 8 + 4 i, the scales or mins
   // of row l / 2.  Phase 3: chunk l & 3 of rows l / 4 and l / 4 + 8, the same of row l / 2, and
-  // chunk l & 15 of tokens l / 16 + 2 i.
+  // chunk l & 15 of tokens l / 16 + 2 i.  The pointers run on from block to block.
   const int cr = GU ? lane >> 3 : r, cc = GU ? lane & 7 : t, sr = lane >> 1;
   const uint32_t cdst = GU ? cr * 128 + ((cc ^ few_swz(cr)) << 4) : cr * 64 + ((cc ^ (cr & 2)) << 4);
   const uint32_t sdst = GU ? 2048 + lane * 8 : 1024 + lane * 4;
   FewCursor<GU> L = C;
   int lb = W.b0;
   uint32_t lst = ring;
-  const uint8_t *blob = nullptr;
-  int co[GU ? 4 : 2], so = 0;
-  if (!GU) {
-#pragma unroll
-    for (int i = 0; i < 2; i++) co[i] = (int)A.bl.dc + (r0 + min(cr + 8 * i, nr - 1)) * (K / 2) + cc * 16;
-    so = (int)(lane & 1 ? A.bl.dm : A.bl.ds) + (r0 + min(sr, nr - 1)) * (K / 32);
-  }
+  const uint8_t *cp = nullptr, *sp = nullptr;     // codes of the first row, scales or mins
+  const uint8_t *xp[GU ? 1 : TOK / 2];
+  // phase 2: 4 rows on, and from gate to up; phase 3: 8 rows on (the last row again past the end)
+  const int row4 = 4 * (K / 2), up = (int)(A.bl.uc - A.bl.gc);
+  const int row8 = GU ? 0 : (min(cr + 8, nr - 1) - min(cr, nr - 1)) * (K / 2);
+  // a lane's place in the blob of the first index or row
+  const int c_at = GU ? (int)A.bl.gc + cr * (K / 2) + W.b0 * 128 + cc * 16
+                      : (int)A.bl.dc + (r0 + min(cr, nr - 1)) * (K / 2) + W.b0 * 64 + cc * 16;
+  const int s_at = GU ? (int)(lane & 1 ? A.bl.gm : A.bl.gs) + (sr < 8 ? 0 : up) + (sr & 7) * (K / 32) + W.b0 * 8
+                      : (int)(lane & 1 ? A.bl.dm : A.bl.ds) + (r0 + min(sr, nr - 1)) * (K / 32) + W.b0 * 4;
+  int xn = 0;                                     // tokens of the segment
   auto issue = [&]() {
     if (L.left > 0) {
       if (lb == W.b0) {
         const int e = P.seg_exp[L.s];
-        blob = e < A.E ? A.experts + (long long)e * A.bl.bytes : A.shared;
+        const uint8_t *blob = e < A.E ? A.experts + (long long)e * A.bl.bytes : A.shared;
+        cp = blob + c_at;
+        sp = blob + s_at;
         if (GU) {
-          co[0] = (int)A.bl.gc + (L.i * 8 + cr) * (K / 2) + cc * 16;
-          co[1] = co[0] + 4 * (K / 2);
-          co[GU ? 2 : 0] = co[0] + (int)(A.bl.uc - A.bl.gc);
-          co[GU ? 3 : 0] = co[GU ? 2 : 0] + 4 * (K / 2);
-          so = (int)(lane & 1 ? A.bl.gm : A.bl.gs) + (sr < 8 ? 0 : (int)(A.bl.uc - A.bl.gc)) + (L.i * 8 + (sr & 7)) * (K / 32);
+          cp += L.i * 8 * (K / 2);
+          sp += L.i * 8 * (K / 32);
+        } else {
+          xn = P.seg_n[L.s];
+          const int at = P.seg_at[L.s];
+#pragma unroll
+          for (int i = 0; i < TOK / 2; i++) {
+            const int tok = min((lane >> 4) + 2 * i, xn - 1);
+            xp[GU ? 0 : i] = reinterpret_cast<const uint8_t *>(A.a + (size_t)(P.asg[at + tok] * A.I) + W.b0 * 128) + (lane & 15) * 16;
+          }
         }
       }
+      cp_async16(lst + cdst, cp);
+      if (GU) {
+        cp_async16(lst + cdst + 512, cp + row4);
+        const uint8_t *cu = cp + up;
+        cp_async16(lst + cdst + 1024, cu);
+        cp_async16(lst + cdst + 1536, cu + row4);
+        cp_async_small<8>(lst + sdst, sp);
+        cp += 128;
+        sp += 8;
+      } else {
+        cp_async16(lst + cdst + 512, cp + row8);
+        cp_async_small<4>(lst + sdst, sp);
+        cp += 64;
+        sp += 4;
+        const uint32_t xd = lst + kFewDnHead + (lane >> 4) * kFewDnRow + (lane & 15) * 16;
 #pragma unroll
-      for (int i = 0; i < (GU ? 4 : 2); i++) cp_async16(lst + cdst + i * 512, blob + co[i] + lb * (GU ? 128 : 64));
-      cp_async_small<GU ? 8 : 4>(lst + sdst, blob + so + lb * (GU ? 8 : 4));
-      if (!GU) {
-        const int n = P.seg_n[L.s], at = P.seg_at[L.s];
-#pragma unroll
-        for (int i = 0; i < TOK / 2; i++) {
-          const int tok = (lane >> 4) + 2 * i;
-          if (tok < n)
-            cp_async16(lst + kFewDnHead + tok * kFewDnRow + (lane & 15) * 16,
-                       A.a + (size_t)P.asg[at + tok] * A.I + lb * 128 + (lane & 15) * 8);
-        }
+        for (int i = 0; i < TOK / 2; i++)
+          if (2 * i < xn) {                       // (the whole warp; an odd last token is copied twice)
+            if ((lane >> 4) + 2 * i < xn) cp_async16(xd + 2 * i * kFewDnRow, xp[GU ? 0 : i]);
+            xp[GU ? 0 : i] += 256;
+          }
       }
       lst = lst + STAGE == end ? ring : lst + STAGE;
       if (++lb == W.b1) {
@@ -761,6 +810,11 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
 #pragma unroll 1
   for (int u = 1; u < (GU ? kFewDepth : depth); u++) issue();
   uint32_t st = ring;
+  // the lane's codes in a stage: pair, chunk t (and, phase 2, 4 + t); wide, the 8 bytes of groups
+  // 0 and 1 (and 2 and 3, 64 bytes on before the permutation)
+  const int swz = GU ? few_swz(r) : r & 2, pitch = GU ? 128 : 64;
+  const uint32_t o0 = r * pitch + (((WIDE ? t >> 1 : t) ^ swz) << 4) + (WIDE ? (t & 1) * 8 : 0);
+  const uint32_t o1 = r * pitch + (((2 + (t >> 1)) ^ swz) << 4) + (t & 1) * 8;
   FewCol<WIDE, N> X;
 #pragma unroll 1
   for (; C.left > 0; C.next(step, per)) {
@@ -769,6 +823,12 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
 #pragma unroll
     for (int q = 0; q < N; q++) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
     X.set(O, GU ? at - p0 : 0, at - p0, n, zero);
+#pragma unroll
+    for (int q = 0; q < N; q++) {
+      X.x[q] += GU ? 2 * W.b0 * X.step : 0;
+      X.v0[q] += (GU ? 16 : 8) * W.b0;
+      X.v1[q] += (GU ? 16 : 8) * W.b0;
+    }
 #pragma unroll 1
     for (int b = W.b0; b < W.b1; b++) {
       if (GU) cp_async_wait_but<kFewDepth - 2>(); else cp_async_wait_upto(depth - 2);
@@ -776,14 +836,18 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
       issue();
       if (GU) {
         const uint4 ca = lds128(st + 2048 + r * 16), cb = lds128(st + 2048 + r * 16 + 128);
-        few_mul128<WIDE, N>(st + r * 128, 1024, 0, few_swz(r), ca.x, ca.z, cb.x, cb.z, X, 2 * b, b * 16, acc);
-        few_mul128<WIDE, N>(st + r * 128, 1024, 4, few_swz(r), ca.y, ca.w, cb.y, cb.w, X, 2 * b + 1, b * 16 + 8, acc);
+        few_mul128<WIDE, N, 1024>(st + o0, st + o1, ca.x, ca.z, cb.x, cb.z, X, acc);
+        X.advance(X.step);
+        // chunk c + 4 lies 64 bytes from chunk c, on the side that the permutation leaves
+        few_mul128<WIDE, N, 1024>(st + (o0 ^ 64), st + (o1 ^ 64), ca.y, ca.w, cb.y, cb.w, X, acc);
+        X.advance(X.step);
       } else {
         const uint2 ca = lds64(st + 1024 + r * 8), cb = lds64(st + 1024 + r * 8 + 64);
         FewCol<WIDE, N> Y = X;            // the stage's own columns
 #pragma unroll
         for (int q = 0; q < N; q++) Y.x[q] = X.step ? X.x[q] + st : zero;
-        few_mul128<WIDE, N>(st + r * 64, 512, 0, r & 2, ca.x, ca.y, cb.x, cb.y, Y, 0, b * 8, acc);
+        few_mul128<WIDE, N, 512>(st + o0, st + o1, ca.x, ca.y, cb.x, cb.y, Y, acc);
+        X.advance(0);
       }
       st = st + STAGE == end ? ring : st + STAGE;
     }
@@ -1042,6 +1106,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_moe_few(const __grid_constan
   few_phase1(A, P, rings, red);
   grid.sync();
   if (A.h_out) few_residual(A, rings);
+  if (A.T > kFewRouteAll) {
+    few_route_share(A);
+    grid.sync();
+  }
   few_plan(A, P);
   few_phase2(A, P, area, smem_at(zero), ring, red);
   grid.sync();
