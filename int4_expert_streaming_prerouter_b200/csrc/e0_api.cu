@@ -2228,6 +2228,7 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
   A.dn_ring = (rest - A.out_bytes - (A.dn_rows * sum_bytes + 15) / 16 * 16) / kFewWarps / 16 * 16;
   if (A.gu_rows < 8 || A.dn_rows < std::min(places, A.seg_cap))
     return fail(E0_ERR_INVALID_ARG, "moe_layer_few: dims too large for the shared memory");
+  A.code = FewCode{0x000F000Fu, 0x43004300u};
   A.tpb = T <= 16 ? 1 : T <= 32 ? 2 : 4;
   A.lora16 = !misaligned(Y.lora_Bg, 16) && !misaligned(Y.lora_Bu, 16) && !misaligned(Y.lora_Bd, 16);
   CK(cudaFuncSetAttribute(k_moe_few, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));

@@ -43,6 +43,10 @@ constexpr int kFewMaxA = kFewMaxT * (kMaxK + 1);                // assignments
 constexpr int kFewMaxSeg = kMaxE + 1 + kFewMaxA / 8;            // segments
 constexpr int kFewPad = 16;                                     // bytes between rows: 8 rows in distinct banks
 
+struct FewCode {
+  uint32_t mask, offset;        // 0x000F000F, 0x43004300
+};
+
 struct FewArgs {
   const uint16_t *h, *delta;
   const uint16_t *gamma, *router;
@@ -67,6 +71,7 @@ struct FewArgs {
   float *a8;                  // [T][k + 1][I / 8] sums of a
   int *err;
   int seg_cap;                // tokens to a segment: 8 or 16
+  FewCode code;
   int lora16;                 // rows of LoRA B begin at 16 bytes
   int tpb;                    // tokens that a block of phase 1 norms
   int gu_rows;                // activation rows that fit the staging area of phase 2
@@ -225,8 +230,15 @@ struct FewCol {
   }
 };
 
-// 8 codes of a word as four pairs 128 + q, in operand order
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) { return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u; }
+// Pair i of a word's 8 codes as 128 + q, in operand order: one shift and one three-input operation.
+// Mask and offset come from registers: given as constants, they become two operations, since an
+// instruction holds one (the integer pipe is what bounds the products: 179 instructions and 58 us
+// instead of 147 and 47 in phase 2 at 64 tokens).
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i, const FewCode &K) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * i)), "r"(K.mask), "r"(K.offset));
+  return r;
+}
 
 // One fold: the sums p of a group (pair: of a lane's group of two) with its scales and mins, the
 // low (sel 0x1044) or high (0x3244) halves of the words.  at: byte offset of the group's sums.
@@ -251,7 +263,7 @@ __device__ __forceinline__ void few_fold(const float (&p)[N][4], uint32_t wsa, u
 // l / 4 + 8) of the two groups.
 template <bool WIDE, int N, int HALF>
 __device__ __forceinline__ void few_mul128(uint32_t w0, uint32_t w1, uint32_t wsa, uint32_t wma, uint32_t wsb, uint32_t wmb,
-                                           const FewCol<WIDE, N> &X, float (&acc)[N][4]) {
+                                           const FewCol<WIDE, N> &X, const FewCode &K, float (&acc)[N][4]) {
   const int t = threadIdx.x & 3;
   if (WIDE) {
 #pragma unroll
@@ -261,8 +273,8 @@ __device__ __forceinline__ void few_mul128(uint32_t w0, uint32_t w1, uint32_t ws
 #pragma unroll
       for (int w = 0; w < 2; w++) {
         const uint32_t xa = w ? wa.y : wa.x, xb = w ? wb.y : wb.x;
-        const uint32_t a0 = code_pair(xa, 0), a1 = code_pair(xa, 1), a2 = code_pair(xa, 2), a3 = code_pair(xa, 3);
-        const uint32_t b0 = code_pair(xb, 0), b1 = code_pair(xb, 1), b2 = code_pair(xb, 2), b3 = code_pair(xb, 3);
+        const uint32_t a0 = code_pair(xa, 0, K), a1 = code_pair(xa, 1, K), a2 = code_pair(xa, 2, K), a3 = code_pair(xa, 3, K);
+        const uint32_t b0 = code_pair(xb, 0, K), b1 = code_pair(xb, 1, K), b2 = code_pair(xb, 2, K), b3 = code_pair(xb, 3, K);
 #pragma unroll
         for (int q = 0; q < N; q++) {
           const uint4 x = lds128(X.x[q] + g * 128 + w * 16);
@@ -280,8 +292,8 @@ __device__ __forceinline__ void few_mul128(uint32_t w0, uint32_t w1, uint32_t ws
     for (int w = 0; w < 4; w++) {
       const uint32_t xa = w == 0 ? wa.x : w == 1 ? wa.y : w == 2 ? wa.z : wa.w;
       const uint32_t xb = w == 0 ? wb.x : w == 1 ? wb.y : w == 2 ? wb.z : wb.w;
-      const uint32_t a0 = code_pair(xa, 0), a1 = code_pair(xa, 1), a2 = code_pair(xa, 2), a3 = code_pair(xa, 3);
-      const uint32_t b0 = code_pair(xb, 0), b1 = code_pair(xb, 1), b2 = code_pair(xb, 2), b3 = code_pair(xb, 3);
+      const uint32_t a0 = code_pair(xa, 0, K), a1 = code_pair(xa, 1, K), a2 = code_pair(xa, 2, K), a3 = code_pair(xa, 3, K);
+      const uint32_t b0 = code_pair(xb, 0, K), b1 = code_pair(xb, 1, K), b2 = code_pair(xb, 2, K), b3 = code_pair(xb, 3, K);
 #pragma unroll
       for (int q = 0; q < N; q++) {
         const uint4 x = lds128(X.x[q] + w * 16);
@@ -810,6 +822,7 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
 #pragma unroll 1
   for (int u = 1; u < (GU ? kFewDepth : depth); u++) issue();
   uint32_t st = ring;
+  const FewCode code = A.code;
   // the lane's codes in a stage: pair, chunk t (and, phase 2, 4 + t); wide, the 8 bytes of groups
   // 0 and 1 (and 2 and 3, 64 bytes on before the permutation)
   const int swz = GU ? few_swz(r) : r & 2, pitch = GU ? 128 : 64;
@@ -836,17 +849,17 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
       issue();
       if (GU) {
         const uint4 ca = lds128(st + 2048 + r * 16), cb = lds128(st + 2048 + r * 16 + 128);
-        few_mul128<WIDE, N, 1024>(st + o0, st + o1, ca.x, ca.z, cb.x, cb.z, X, acc);
+        few_mul128<WIDE, N, 1024>(st + o0, st + o1, ca.x, ca.z, cb.x, cb.z, X, code, acc);
         X.advance(X.step);
         // chunk c + 4 lies 64 bytes from chunk c, on the side that the permutation leaves
-        few_mul128<WIDE, N, 1024>(st + (o0 ^ 64), st + (o1 ^ 64), ca.y, ca.w, cb.y, cb.w, X, acc);
+        few_mul128<WIDE, N, 1024>(st + (o0 ^ 64), st + (o1 ^ 64), ca.y, ca.w, cb.y, cb.w, X, code, acc);
         X.advance(X.step);
       } else {
         const uint2 ca = lds64(st + 1024 + r * 8), cb = lds64(st + 1024 + r * 8 + 64);
         FewCol<WIDE, N> Y = X;            // the stage's own columns
 #pragma unroll
         for (int q = 0; q < N; q++) Y.x[q] = X.step ? X.x[q] + st : zero;
-        few_mul128<WIDE, N, 512>(st + o0, st + o1, ca.x, ca.y, cb.x, cb.y, Y, acc);
+        few_mul128<WIDE, N, 512>(st + o0, st + o1, ca.x, ca.y, cb.x, cb.y, Y, code, acc);
         X.advance(0);
       }
       st = st + STAGE == end ? ring : st + STAGE;
