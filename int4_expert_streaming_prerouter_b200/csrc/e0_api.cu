@@ -2220,7 +2220,7 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
   A.gu_rows = (rest - kFewRingBytes) / few_row_bytes(A.d);
   const int places = T * (A.k + 1), sum_bytes = A.I / 64 * 4;
   A.out_bytes = std::max(16384, places * 64);
-  const int least8 = kFewWarps * 2 * few_dn_stage(8), least16 = kFewWarps * 2 * few_dn_stage(16);
+  const int least8 = kFewWarps * 2 * (few_dn_stage(8) + kFewSlot), least16 = kFewWarps * 2 * (few_dn_stage(16) + kFewSlot);
   const int wish = std::min(places, 16) * sum_bytes + 16;
   A.seg_cap = A.gu_rows >= 16 && rest - A.out_bytes - wish >= least16 ? 16 : 8;
   const int most_sums = rest - A.out_bytes - 16 - (A.seg_cap == 16 ? least16 : least8);

@@ -131,6 +131,7 @@ __device__ __forceinline__ float lds32(uint32_t a) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
   return v;
 }
+__device__ __forceinline__ uint32_t lds32u(uint32_t a) { return __float_as_uint(lds32(a)); }
 __device__ __forceinline__ uint32_t smem_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -163,16 +164,18 @@ __device__ __forceinline__ void bf16_mul(uint4 a, uint4 b, uint4 x, float (&acc)
 // of a row a lane, a fold per group.  The accumulators of a lane are rows l / 4 and l / 4 + 8,
 // tokens 2 (l & 3), + 1 of a tile (pair: tokens 2 (l & 1), + 1, after adding lanes l and l + 2).
 //
-// Each warp streams its weights through a ring of its own in shared memory, a block to a stage, by
-// cp.async.  Phase 2: 256 channels, 16 rows of 128 bytes of codes (their 16-byte chunks permuted by
-// row, so that either form reads without bank conflicts), then per row the scales and the mins of 4
-// groups; the activations, which every tile needs again, are staged apart.  Phase 3: 128 channels, 64
-// bytes of codes a row, the scales and mins of 2 groups, and the activations of the segment's
-// tokens, which are used once.
-constexpr int kFewStage = 16 * 128 + 16 * 16;
+// Each warp streams its weights through a ring of its own in shared memory by cp.async, a block to
+// a stage.  Phase 2: 256 channels, 16 rows of 128 bytes of codes (their 16-byte chunks permuted by
+// row, so that either form reads without bank conflicts); the activations, which every tile needs
+// again, are staged apart.  Phase 3: 128 channels, 64 bytes of codes a row and the activations of
+// the segment's tokens, which are used once.  The scales and mins of 512 channels (256, 128 where a
+// row is no multiple of that), 16 bytes each a row, have slots of their own: fetched block by block,
+// each would be 4 or 8 bytes of a 32-byte sector.
+constexpr int kFewStage = 16 * 128;
 constexpr int kFewDepth = 3;
-constexpr int kFewRingBytes = kFewWarps * kFewDepth * kFewStage;
-constexpr int kFewDnHead = 16 * 64 + 16 * 8, kFewDnRow = 256 + 16;
+constexpr int kFewSlot = 16 * 32;
+constexpr int kFewRing = kFewDepth * (kFewStage + kFewSlot), kFewRingBytes = kFewWarps * kFewRing;
+constexpr int kFewDnHead = 16 * 64, kFewDnRow = 256 + 16;
 constexpr int few_dn_stage(int tokens) { return kFewDnHead + tokens * kFewDnRow; }
 
 template <int N>
@@ -287,7 +290,8 @@ __device__ __forceinline__ void few_mul128(uint32_t w0, uint32_t w1, uint32_t ws
     }
   } else {
     const uint4 wa = lds128(w0), wb = lds128(w0 + HALF);
-    float p[N][4];
+    // (one tile of tokens: two chains of dependent instructions, joined at the fold)
+    float p[N][4], p2[4];
 #pragma unroll
     for (int w = 0; w < 4; w++) {
       const uint32_t xa = w == 0 ? wa.x : w == 1 ? wa.y : w == 2 ? wa.z : wa.w;
@@ -299,9 +303,14 @@ __device__ __forceinline__ void few_mul128(uint32_t w0, uint32_t w1, uint32_t ws
         const uint4 x = lds128(X.x[q] + w * 16);
         if (w == 0) mma_bf16_first(p[q], a0, b0, a1, b1, x.x, x.y);
         else mma_bf16_acc(p[q], a0, b0, a1, b1, x.x, x.y);
-        mma_bf16_acc(p[q], a2, b2, a3, b3, x.z, x.w);
+        if (N > 1) mma_bf16_acc(p[q], a2, b2, a3, b3, x.z, x.w);
+        else if (w == 0) mma_bf16_first(p2, a2, b2, a3, b3, x.z, x.w);
+        else mma_bf16_acc(p2, a2, b2, a3, b3, x.z, x.w);
       }
     }
+    if (N == 1)
+#pragma unroll
+      for (int i = 0; i < 4; i++) p[0][i] += p2[i];
     few_fold<N>(p, wsa, wma, wsb, wmb, t >> 1 ? 0x3244u : 0x1044u, X.v0, X.v1, 0, acc);
   }
 }
@@ -544,7 +553,7 @@ __device__ __forceinline__ void few_route_share(const FewArgs &A) {
 
 // Relative cost of a tile in phase 2 (measured; the weights bound the first): segments of experts
 // of at most 4 tokens, of at most 8, of more.
-constexpr int kFewCost4 = 4, kFewCost8 = 6, kFewCostMore = 9;
+constexpr int kFewCost4 = 4, kFewCost8 = 6, kFewCostMore = 11;
 
 __device__ __forceinline__ void few_plan(const FewArgs &A, FewPlan &P) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -747,16 +756,19 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
   if (C.left <= 0) return;
   constexpr int TOK = N * (WIDE ? 8 : 4), STAGE = GU ? kFewStage : few_dn_stage(TOK);
   const int lane = threadIdx.x & 31, t = lane & 3, r = lane >> 2, warp = threadIdx.x >> 5;
-  const int K = GU ? A.d : A.I, end = ring + (GU ? kFewDepth : depth) * STAGE;
+  const int K = GU ? A.d : A.I, stages = GU ? kFewDepth : depth;
+  const uint32_t slots = ring, slots_end = slots + stages * kFewSlot;     // of scales, then the stages
+  const uint32_t stages_at = slots_end, end = stages_at + stages * STAGE;
+  const int cs = K % 512 == 0 ? 4 : K % 256 == 0 ? 2 : 1;                 // 128 channels to a slot
   // what this lane copies of a block.  Phase 2: chunk l & 7 of rows l / 8 + 4 i, the scales or mins
   // of row l / 2.  Phase 3: chunk l & 3 of rows l / 4 and l / 4 + 8, the same of row l / 2, and
   // chunk l & 15 of tokens l / 16 + 2 i.  The pointers run on from block to block.
   const int cr = GU ? lane >> 3 : r, cc = GU ? lane & 7 : t, sr = lane >> 1;
   const uint32_t cdst = GU ? cr * 128 + ((cc ^ few_swz(cr)) << 4) : cr * 64 + ((cc ^ (cr & 2)) << 4);
-  const uint32_t sdst = GU ? 2048 + lane * 8 : 1024 + lane * 4;
+  const uint32_t sdst = sr * 32 + (lane & 1) * 16;
   FewCursor<GU> L = C;
   int lb = W.b0;
-  uint32_t lst = ring;
+  uint32_t lst = stages_at, lsl = slots;
   const uint8_t *cp = nullptr, *sp = nullptr;     // codes of the first row, scales or mins
   const uint8_t *xp[GU ? 1 : TOK / 2];
   // phase 2: 4 rows on, and from gate to up; phase 3: 8 rows on (the last row again past the end)
@@ -765,8 +777,8 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
   // a lane's place in the blob of the first index or row
   const int c_at = GU ? (int)A.bl.gc + cr * (K / 2) + W.b0 * 128 + cc * 16
                       : (int)A.bl.dc + (r0 + min(cr, nr - 1)) * (K / 2) + W.b0 * 64 + cc * 16;
-  const int s_at = GU ? (int)(lane & 1 ? A.bl.gm : A.bl.gs) + (sr < 8 ? 0 : up) + (sr & 7) * (K / 32) + W.b0 * 8
-                      : (int)(lane & 1 ? A.bl.dm : A.bl.ds) + (r0 + min(sr, nr - 1)) * (K / 32) + W.b0 * 4;
+  const int s_at = GU ? (int)(lane & 1 ? A.bl.gm : A.bl.gs) + (sr < 8 ? 0 : up) + (sr & 7) * (K / 32) + ((2 * W.b0) & -cs) * 4
+                      : (int)(lane & 1 ? A.bl.dm : A.bl.ds) + (r0 + min(sr, nr - 1)) * (K / 32) + (W.b0 & -cs) * 4;
   int xn = 0;                                     // tokens of the segment
   auto issue = [&]() {
     if (L.left > 0) {
@@ -788,20 +800,23 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
           }
         }
       }
+      if (lb == W.b0 || ((GU ? 2 * lb : lb) & (cs - 1)) == 0) {
+        if (cs == 4) cp_async16(lsl + sdst, sp);
+        else if (cs == 2) cp_async_small<8>(lsl + sdst, sp);
+        else cp_async_small<4>(lsl + sdst, sp);
+        sp += cs * 4;
+        lsl = lsl + kFewSlot == slots_end ? slots : lsl + kFewSlot;
+      }
       cp_async16(lst + cdst, cp);
       if (GU) {
         cp_async16(lst + cdst + 512, cp + row4);
         const uint8_t *cu = cp + up;
         cp_async16(lst + cdst + 1024, cu);
         cp_async16(lst + cdst + 1536, cu + row4);
-        cp_async_small<8>(lst + sdst, sp);
         cp += 128;
-        sp += 8;
       } else {
         cp_async16(lst + cdst + 512, cp + row8);
-        cp_async_small<4>(lst + sdst, sp);
         cp += 64;
-        sp += 4;
         const uint32_t xd = lst + kFewDnHead + (lane >> 4) * kFewDnRow + (lane & 15) * 16;
 #pragma unroll
         for (int i = 0; i < TOK / 2; i++)
@@ -810,7 +825,7 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
             xp[GU ? 0 : i] += 256;
           }
       }
-      lst = lst + STAGE == end ? ring : lst + STAGE;
+      lst = lst + STAGE == end ? stages_at : lst + STAGE;
       if (++lb == W.b1) {
         lb = W.b0;
         L.next(step, per);
@@ -820,8 +835,8 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
   };
   __syncwarp();                           // every lane has left the ring's last use
 #pragma unroll 1
-  for (int u = 1; u < (GU ? kFewDepth : depth); u++) issue();
-  uint32_t st = ring;
+  for (int u = 1; u < stages; u++) issue();
+  uint32_t st = stages_at, sl = slots_end - kFewSlot;
   const FewCode code = A.code;
   // the lane's codes in a stage: pair, chunk t (and, phase 2, 4 + t); wide, the 8 bytes of groups
   // 0 and 1 (and 2 and 3, 64 bytes on before the permutation)
@@ -847,22 +862,24 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
       if (GU) cp_async_wait_but<kFewDepth - 2>(); else cp_async_wait_upto(depth - 2);
       __syncwarp();                       // the block has arrived, and every lane has left the one before
       issue();
+      const int at128 = (GU ? 2 * b : b) & (cs - 1);
+      if (b == W.b0 || at128 == 0) sl = sl + kFewSlot == slots_end ? slots : sl + kFewSlot;
+      const uint32_t sc = sl + r * 32 + at128 * 4;
       if (GU) {
-        const uint4 ca = lds128(st + 2048 + r * 16), cb = lds128(st + 2048 + r * 16 + 128);
-        few_mul128<WIDE, N, 1024>(st + o0, st + o1, ca.x, ca.z, cb.x, cb.z, X, code, acc);
+        const uint2 s0 = lds64(sc), m0 = lds64(sc + 16), s8 = lds64(sc + 256), m8 = lds64(sc + 272);
+        few_mul128<WIDE, N, 1024>(st + o0, st + o1, s0.x, m0.x, s8.x, m8.x, X, code, acc);
         X.advance(X.step);
         // chunk c + 4 lies 64 bytes from chunk c, on the side that the permutation leaves
-        few_mul128<WIDE, N, 1024>(st + (o0 ^ 64), st + (o1 ^ 64), ca.y, ca.w, cb.y, cb.w, X, code, acc);
+        few_mul128<WIDE, N, 1024>(st + (o0 ^ 64), st + (o1 ^ 64), s0.y, m0.y, s8.y, m8.y, X, code, acc);
         X.advance(X.step);
       } else {
-        const uint2 ca = lds64(st + 1024 + r * 8), cb = lds64(st + 1024 + r * 8 + 64);
         FewCol<WIDE, N> Y = X;            // the stage's own columns
 #pragma unroll
         for (int q = 0; q < N; q++) Y.x[q] = X.step ? X.x[q] + st : zero;
-        few_mul128<WIDE, N, 512>(st + o0, st + o1, ca.x, ca.y, cb.x, cb.y, Y, code, acc);
+        few_mul128<WIDE, N, 512>(st + o0, st + o1, lds32u(sc), lds32u(sc + 16), lds32u(sc + 256), lds32u(sc + 272), Y, code, acc);
         X.advance(0);
       }
-      st = st + STAGE == end ? ring : st + STAGE;
+      st = st + STAGE == end ? stages_at : st + STAGE;
     }
     // pair: lanes l and l + 2 hold the same two tokens and take one each; wide: both tokens
 #pragma unroll
@@ -1063,7 +1080,7 @@ __device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, u
       const FewOps O{kFewDnHead, smem_at(sums), kFewDnRow, G * 4};
       const int m4 = max(s0, min(s1, P.n4)), m8 = max(m4, min(s1, P.n8));
       auto cursor = [&](int a, int b) { return FewCursor<false>{a + team, 0, (b - a - team + step - 1) >> (4 - lg)}; };
-      auto depth = [&](int tokens) { return min(4, A.dn_ring / few_dn_stage(tokens)); };
+      auto depth = [&](int tokens) { return min(4, A.dn_ring / (few_dn_stage(tokens) + kFewSlot)); };
       if (m8 < s1) few_stream<false, true, 2>(A, P, O, p0, cursor(m8, s1), step, 0, W, r0, nr, depth(16), zero, ring, o);
       if (m4 < m8) few_stream<false, false, 2>(A, P, O, p0, cursor(m4, m8), step, 0, W, r0, nr, depth(8), zero, ring, o);
       if (s0 < m4) few_stream<false, false, 1>(A, P, O, p0, cursor(s0, m4), step, 0, W, r0, nr, depth(4), zero, ring, o);
@@ -1110,7 +1127,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_moe_few(const __grid_constan
   uint8_t *zero = smem + few_plan_bytes(), *red_area = zero + kFewZeroBytes, *rings = red_area + kFewRedBytes;
   uint8_t *area = rings + kFewRingBytes;          // phase 1, which streams nothing, takes the rings too
   float *red = reinterpret_cast<float *>(red_area);
-  const uint32_t ring = smem_at(rings) + (threadIdx.x >> 5) * kFewDepth * kFewStage;
+  const uint32_t ring = smem_at(rings) + (threadIdx.x >> 5) * kFewRing;
   if (threadIdx.x < kFewZeroBytes / 4) reinterpret_cast<uint32_t *>(zero)[threadIdx.x] = 0;
   static_assert(sizeof(FewArgs) % 4 == 0 && sizeof(FewArgs) / 4 <= kFewThreads, "one word of the arguments a thread");
   if (threadIdx.x < sizeof(FewArgs) / 4)
