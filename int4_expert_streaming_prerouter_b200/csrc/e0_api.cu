@@ -13,6 +13,8 @@
 
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -2093,19 +2095,88 @@ extern "C" int e0_add_rmsnorm(const void *h, long long h_stride, const void *del
   return E0_OK;
 }
 
-template <int NT>
-static int launch_linear(LinearArgs &L, cudaStream_t s) {
-  constexpr int TT = 8 * NT;
-  const int G = L.K / 64;
-  // activations of as many groups as 96 KB hold; an even number, so that scales per 128 start
-  // with a chunk
-  L.kc = std::min(G, ((96 * 1024 - TT * kActPad) / (TT * 136)) & ~1);
-  const size_t smem = std::max((size_t)TT * act_pitch(L.kc) + act_sv_bytes(L.kc, TT), (size_t)(kLinThreads / 32) * 16 * TT * 4);
-  CK(cudaFuncSetAttribute(k_int4_linear<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
-  const dim3 grid((L.N + kLinRows - 1) / kLinRows, (L.T + TT - 1) / TT);
-  k_int4_linear<NT><<<grid, kLinThreads, smem, s>>>(L);
-  CK(cudaGetLastError());
+// Blocks of clusters of S that the device holds at once, one block an SM (looked up once for each
+// kernel, device and S; a race between first calls finds the same number twice).
+static int lin_clusters(const void *kernel, int variant, int dev, int nsm, int S, size_t smem, int *out) {
+  if (S == 1) {
+    *out = nsm;
+    return E0_OK;
+  }
+  static std::atomic<int> known[64][16][4];
+  const int s = S == 2 ? 0 : S == 4 ? 1 : 2;
+  std::atomic<int> *slot = dev < 64 ? &known[dev][variant][s] : nullptr;
+  if (slot && slot->load() > 0) {
+    *out = slot->load();
+    return E0_OK;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(S);
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = S;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  int n = 0;
+  CK(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg));
+  if (n < 1) return fail(E0_ERR_CUDA, "int4_linear: no cluster of %d blocks fits the device", S);
+  if (slot) slot->store(n);
+  *out = n;
   return E0_OK;
+}
+
+template <bool WIDE, int N, bool G128>
+static int launch_linear(LinearArgs &L, cudaStream_t s) {
+  constexpr int TOK = N * (WIDE ? 8 : 4);
+  int dev = 0, nsm = 0, most = 0;
+  CK(cudaGetDevice(&dev));
+  CK(cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev));
+  CK(cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev));
+  const size_t room = (size_t)most - lin_fixed(WIDE, N);
+  // as few blocks to a cluster as the activations need; where even 8 do not hold them, fewer tokens
+  // a block
+  L.tok = std::min(TOK, L.T);
+  for (L.S = 1, L.kc = L.K;;) {
+    if (lin_acts(L.tok, L.kc) <= room) break;
+    if (L.S < 8) {
+      L.S *= 2;
+    } else if (L.tok > 1) {
+      L.tok = (L.tok + 1) / 2;
+      L.S = 1;
+    } else {
+      return fail(E0_ERR_INVALID_ARG, "int4_linear: k = %d is too long", L.K);
+    }
+    L.kc = L.S == 1 ? L.K : ((L.K + L.S - 1) / L.S + 1023) / 1024 * 1024;
+  }
+  if (L.S > 1) L.S = (L.K + L.kc - 1) / L.kc > 4 ? 8 : (L.K + L.kc - 1) / L.kc > 2 ? 4 : 2;
+  const int tiles = (L.T + L.tok - 1) / L.tok;
+  if (tiles > 65535) return fail(E0_ERR_INVALID_ARG, "int4_linear: T = %d is too large for k = %d", L.T, L.K);
+  const size_t smem = lin_fixed(WIDE, N) + lin_acts(L.tok, L.kc);
+  const void *kernel = (const void *)k_int4_linear<WIDE, N, G128>;
+  CK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+  int clusters = 0;
+  if (int rc = lin_clusters(kernel, (WIDE ? 8 : 0) + N + (G128 ? 4 : 0) - 1, dev, nsm, L.S, (size_t)most, &clusters)) return rc;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(std::min(clusters, L.N) * L.S, tiles);
+  cfg.blockDim = dim3(kLinThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = L.S;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = L.S > 1 ? 1 : 0;
+  CK(cudaLaunchKernelEx(&cfg, k_int4_linear<WIDE, N, G128>, L));
+  return E0_OK;
+}
+
+template <bool G128>
+static int launch_linear_tokens(LinearArgs &L, cudaStream_t s) {
+  return L.T <= 4 ? launch_linear<false, 1, G128>(L, s) : L.T <= 8 ? launch_linear<false, 2, G128>(L, s)
+         : L.T <= 16 ? launch_linear<true, 2, G128>(L, s) : launch_linear<true, 4, G128>(L, s);
 }
 
 extern "C" int e0_int4_linear(const e0_int4_mat *w, const void *x, int x_format, long long x_stride,
@@ -2117,8 +2188,8 @@ extern "C" int e0_int4_linear(const e0_int4_mat *w, const void *x, int x_format,
   if (!w->codes || !w->scale || !w->min || w->n < 1 || w->k < 1)
     return fail(E0_ERR_INVALID_ARG, "int4_linear: codes, scale, min, n and k are required");
   if (w->group != 64 && w->group != 128) return fail(E0_ERR_INVALID_ARG, "int4_linear: group must be 64 or 128");
-  if (w->k % w->group || w->k > (1 << 20))
-    return fail(E0_ERR_INVALID_ARG, "int4_linear: k = %d must be a multiple of the group and at most 2^20", w->k);
+  if (w->k % w->group || w->k > (1 << 18))
+    return fail(E0_ERR_INVALID_ARG, "int4_linear: k = %d must be a multiple of the group and at most 2^18", w->k);
   if (w->n > (1 << 26)) return fail(E0_ERR_INVALID_ARG, "int4_linear: n = %d, at most 2^26", w->n);
   if (T > 65535 * 8) return fail(E0_ERR_INVALID_ARG, "int4_linear: T = %d, at most %d", T, 65535 * 8);
   const bool lora = w->lora_A || w->lora_B;
@@ -2136,13 +2207,21 @@ extern "C" int e0_int4_linear(const e0_int4_mat *w, const void *x, int x_format,
   if (misaligned(w->codes, 16) || misaligned(x, bf16x ? 16 : 8) || x_stride % 8 || misaligned(w->lora_A, 16))
     return fail(E0_ERR_INVALID_ARG, "int4_linear: codes, lora_A and bf16 x are 16-byte aligned, 8-bit x 8-byte, x_stride a multiple of 8");
   LinearArgs L{};
-  L.codes = (const uint8_t *)w->codes; L.scale = (const uint16_t *)w->scale; L.min = (const uint16_t *)w->min;
-  L.N = w->n; L.K = w->k; L.gs = w->group == 128;
+  L.codes = (const uint8_t *)w->codes; L.scale = (const uint8_t *)w->scale; L.min = (const uint8_t *)w->min;
+  L.N = w->n; L.K = w->k;
   L.A = (const uint16_t *)w->lora_A; L.B = (const uint16_t *)w->lora_B; L.r = w->lora_rank; L.c = w->lora_scale;
   L.x = x; L.x_type = x_format; L.x_stride = x_stride; L.x_scale = x_scale; L.x_group = x_group ? x_group : w->k;
   L.T = T; L.y = y; L.y_f32 = y_f32; L.y_stride = y_stride;
   cudaStream_t s = (cudaStream_t)stream;
-  return T <= 8 ? launch_linear<1>(L, s) : T <= 16 ? launch_linear<2>(L, s) : launch_linear<4>(L, s);
+  L.b16 = w->lora_rank % 8 == 0 && !misaligned(w->lora_B, 16);
+  // scales of as many channels at a time as 16 bytes hold, where every row of scales begins at that
+  // alignment; 8 or 4 bytes at 256 channels; else one by one
+  const int per = w->group == 128 ? 2 : 4;          // bytes to 128 channels
+  const uintptr_t row = (uintptr_t)(w->k / w->group * 2) | (uintptr_t)w->scale | (uintptr_t)w->min;
+  L.cs = 16 / per;
+  while (L.cs > 2 && row % (L.cs * per)) L.cs /= 2;
+  if (row % (L.cs * per)) L.cs = 0;
+  return w->group == 128 ? launch_linear_tokens<true>(L, s) : launch_linear_tokens<false>(L, s);
 }
 
 // Workspace regions of e0_moe_layer_few, 256-byte aligned.

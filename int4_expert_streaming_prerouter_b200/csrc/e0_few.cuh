@@ -100,19 +100,7 @@ constexpr int kFewRedBytes = kFewWarps * 16 * 16 * 4;            // partial sums
 // bytes of an activation row of phase 2 with its sums
 __host__ __device__ inline int few_row_bytes(int channels) { return channels * 2 + kFewPad + channels / 64 * 4; }
 
-__device__ __forceinline__ void bar_team(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
-__device__ __forceinline__ void mma_bf16_acc(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                             uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// the same without a sum to add to
+// mma_bf16_acc without a sum to add to
 __device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -120,23 +108,6 @@ __device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint3
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ float lds32(uint32_t a) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds32u(uint32_t a) { return __float_as_uint(lds32(a)); }
-__device__ __forceinline__ uint32_t smem_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // 8 channels 0..7 -> 0 4 1 5 2 6 3 7 and back (pairs of a 16-byte chunk)
 __device__ __forceinline__ uint4 operand_order(uint4 v) {
@@ -146,13 +117,6 @@ __device__ __forceinline__ uint4 operand_order(uint4 v) {
 __device__ __forceinline__ uint4 natural_order(uint4 v) {
   return make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.x, v.y, 0x7632),
                     __byte_perm(v.z, v.w, 0x7632));
-}
-
-// 16 bf16 rows times 8 bf16 columns, 32 channels: a, b the lane's rows l / 4 and l / 4 + 8 at
-// channel 8 (l & 3), x its column there.
-__device__ __forceinline__ void bf16_mul(uint4 a, uint4 b, uint4 x, float (&acc)[4]) {
-  mma_bf16_acc(acc, a.x, b.x, a.y, b.y, x.x, x.y);
-  mma_bf16_acc(acc, a.z, b.z, a.w, b.w, x.z, x.w);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -178,27 +142,12 @@ constexpr int kFewRing = kFewDepth * (kFewStage + kFewSlot), kFewRingBytes = kFe
 constexpr int kFewDnHead = 16 * 64, kFewDnRow = 256 + 16;
 constexpr int few_dn_stage(int tokens) { return kFewDnHead + tokens * kFewDnRow; }
 
-template <int N>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 // all but the newest n (0..2) groups
 __device__ __forceinline__ void cp_async_wait_upto(int n) {
   if (n <= 0) cp_async_wait_but<0>();
   else if (n == 1) cp_async_wait_but<1>();
   else cp_async_wait_but<2>();
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-// chunk c of row r is at chunk c ^ few_swz(r) (phase 3, four chunks a row: ^ (r & 2))
-__device__ __forceinline__ int few_swz(int r) { return ((r & 1) << 2) ^ (r & 2); }
-
 // Activation rows in shared memory: bf16 rows `pitch` bytes apart, and their sums by group.
 struct FewOps {
   uint32_t x, v;              // shared addresses
@@ -676,13 +625,6 @@ struct FewPart {                  // what a warp does of K, and where its team s
   int b0, b1, wk, team, sub;
 };
 
-__device__ __forceinline__ float dot8(uint4 w, float4 x, float4 y, float s) {
-  s = fmaf(__uint_as_float(w.x << 16), x.x, fmaf(__uint_as_float(w.x & 0xFFFF0000u), x.y, s));
-  s = fmaf(__uint_as_float(w.y << 16), x.z, fmaf(__uint_as_float(w.y & 0xFFFF0000u), x.w, s));
-  s = fmaf(__uint_as_float(w.z << 16), y.x, fmaf(__uint_as_float(w.z & 0xFFFF0000u), y.y, s));
-  return fmaf(__uint_as_float(w.w << 16), y.z, fmaf(__uint_as_float(w.w & 0xFFFF0000u), y.w, s));
-}
-
 // SwiGLU of one token (a lane's index l / 4 of tile i8 of segment s), with the shared expert's
 // LoRA; a to the workspace in operand order, and the sum of the tile's 8.
 __device__ __noinline__ void few_emit(const FewPlan &P, int s, int i8, int tok, float g, float u) {
@@ -723,13 +665,9 @@ __device__ __noinline__ void few_emit(const FewPlan &P, int s, int i8, int tok, 
 }
 
 // The join of a team's partial sums (red: [warp][16 rows][16 tokens]).
-// Barrier of a team: ids 1, 2 for teams of 8 warps, 3..6 of 4, 7..14 of 2 (two of the streams below
-// may be under way at once, with teams of different sizes).
-__device__ __forceinline__ int few_bar(int wk, int team) { return 16 / wk - 1 + team; }
-
 __device__ __noinline__ void few_join(const FewPlan &P, int s, int i8, int wk, int team, int sub, const float *red) {
   const int lane = threadIdx.x & 31, n = P.seg_n[s];
-  bar_team(few_bar(wk, team), wk * 32);
+  bar_team(wk, team);
   // 4 tokens of 8 indices to a warp at a time: lane = token + 4 index
   const float *base = red + team * wk * 256 + (lane >> 2) * 16;
 #pragma unroll 1
@@ -743,7 +681,7 @@ __device__ __noinline__ void few_join(const FewPlan &P, int s, int i8, int wk, i
     }
     few_emit(P, s, i8, tok, g, u);
   }
-  bar_team(few_bar(wk, team), wk * 32);
+  bar_team(wk, team);
 }
 
 // Streams a warp's tiles, blocks ahead across the end of a tile too.  Down: rows r0.. (nr of
@@ -764,7 +702,7 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
   // of row l / 2.  Phase 3: chunk l & 3 of rows l / 4 and l / 4 + 8, the same of row l / 2, and
   // chunk l & 15 of tokens l / 16 + 2 i.  The pointers run on from block to block.
   const int cr = GU ? lane >> 3 : r, cc = GU ? lane & 7 : t, sr = lane >> 1;
-  const uint32_t cdst = GU ? cr * 128 + ((cc ^ few_swz(cr)) << 4) : cr * 64 + ((cc ^ (cr & 2)) << 4);
+  const uint32_t cdst = GU ? cr * 128 + ((cc ^ row_swz(cr)) << 4) : cr * 64 + ((cc ^ (cr & 2)) << 4);
   const uint32_t sdst = sr * 32 + (lane & 1) * 16;
   FewCursor<GU> L = C;
   int lb = W.b0;
@@ -840,7 +778,7 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
   const FewCode code = A.code;
   // the lane's codes in a stage: pair, chunk t (and, phase 2, 4 + t); wide, the 8 bytes of groups
   // 0 and 1 (and 2 and 3, 64 bytes on before the permutation)
-  const int swz = GU ? few_swz(r) : r & 2, pitch = GU ? 128 : 64;
+  const int swz = GU ? row_swz(r) : r & 2, pitch = GU ? 128 : 64;
   const uint32_t o0 = r * pitch + (((WIDE ? t >> 1 : t) ^ swz) << 4) + (WIDE ? (t & 1) * 8 : 0);
   const uint32_t o1 = r * pitch + (((2 + (t >> 1)) ^ swz) << 4) + (t & 1) * 8;
   FewCol<WIDE, N> X;

@@ -1,5 +1,4 @@
-// Products of a few tokens with a matrix in the int4 affine group format (e0_int4_linear),
-// and the pieces it shares with the few-token MoE layer.
+// Products of a few tokens with a matrix in the int4 affine group format (e0_int4_linear).
 //
 //   W[n, k] = s[n, k / g] q[n, k] + m[n, k / g],  g = 64 or 128
 //   y[t, n] = sum_k W[n, k] x[t, k]
@@ -17,9 +16,81 @@
 // group's largest, and off by at most 2^-36 of the largest below that.  8-bit activations are
 // exact.
 #pragma once
+#include <cooperative_groups.h>
 #include "e0_device.cuh"
 
 namespace e0 {
+
+// ---------------------------------------------------------------------------------------
+// Shared-memory and copy instructions
+// ---------------------------------------------------------------------------------------
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float lds32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds32u(uint32_t a) { return __float_as_uint(lds32(a)); }
+__device__ __forceinline__ uint32_t smem_at(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
+// the first `bytes` (0..N) from src, zeros behind
+template <int N>
+__device__ __forceinline__ void cp_async_part(uint32_t dst, const void *src, int bytes) {
+  if (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Barrier of a team of wk warps (a power of two below 16): ids 1, 2 for teams of 8, 3..6 of 4, 7..14 of 2, so that
+// teams of different sizes may be under way at once.
+__device__ __forceinline__ void bar_team(int wk, int team) {
+  asm volatile("bar.sync %0, %1;" ::"r"(16 / wk - 1 + team), "r"(wk * 32) : "memory");
+}
+
+// chunk c (of 16 bytes) of row r of 128 bytes lies at chunk c ^ row_swz(r): the lanes of a load, whether 16 or 8
+// bytes each, fall into distinct banks
+__device__ __forceinline__ int row_swz(int r) { return ((r & 1) << 2) ^ (r & 2); }
+
+__device__ __forceinline__ float dot8(uint4 w, float4 x, float4 y, float s) {
+  s = fmaf(__uint_as_float(w.x << 16), x.x, fmaf(__uint_as_float(w.x & 0xFFFF0000u), x.y, s));
+  s = fmaf(__uint_as_float(w.y << 16), x.z, fmaf(__uint_as_float(w.y & 0xFFFF0000u), x.w, s));
+  s = fmaf(__uint_as_float(w.z << 16), y.x, fmaf(__uint_as_float(w.z & 0xFFFF0000u), y.y, s));
+  return fmaf(__uint_as_float(w.w << 16), y.z, fmaf(__uint_as_float(w.w & 0xFFFF0000u), y.w, s));
+}
+
+__device__ __forceinline__ void mma_bf16_acc(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 16 bf16 rows times 8 bf16 columns, 32 channels: a, b the lane's rows l / 4 and l / 4 + 8 at
+// channel 8 (l & 3), x its column there.
+__device__ __forceinline__ void bf16_mul(uint4 a, uint4 b, uint4 x, float (&acc)[4]) {
+  mma_bf16_acc(acc, a.x, b.x, a.y, b.y, x.x, x.y);
+  mma_bf16_acc(acc, a.z, b.z, a.w, b.w, x.z, x.w);
+}
 
 // ---------------------------------------------------------------------------------------
 // Activations as matrix operands
@@ -31,10 +102,7 @@ namespace e0 {
 // first, of the second, sum of the first, of the second}.  factor and sum carry 2^-9, which
 // the end result is multiplied with once, so that no factor overflows.
 constexpr float kActUnit = 512.0f;
-constexpr int kActPad = 64;               // per token, so that 8 tokens fall into distinct banks
-
-__host__ __device__ inline int act_pitch(int groups) { return groups * 128 + kActPad; }
-__host__ __device__ inline int act_sv_bytes(int groups, int tokens) { return groups * ((tokens + 1) / 2) * 16; }
+constexpr int kActPad = 64;               // per token, so that the tokens of a load fall into distinct banks
 
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {
   uint32_t r;
@@ -93,10 +161,8 @@ __device__ __forceinline__ void act_group_bf16(uint4 w, int i, int tok, int grp,
   if (put) D.put(tok, grp, i, act_pack(v), factor, s);
 }
 
-// The same for 8-bit channels (int8, or e4m3) with a scale: 8 bytes a lane.
-__device__ __forceinline__ void act_group_q8(uint2 w, bool e4m3, float scale, int i, int tok, int grp,
-                                             const ActDst &D, bool put) {
-  float v[8];
+// The values of 8 int8 or e4m3 codes.
+__device__ __forceinline__ void q8_values(uint2 w, bool e4m3, float (&v)[8]) {
   const uint32_t ws[2] = {w.x, w.y};
 #pragma unroll
   for (int j = 0; j < 4; j++) {
@@ -104,15 +170,19 @@ __device__ __forceinline__ void act_group_q8(uint2 w, bool e4m3, float scale, in
     if (e4m3) {
       uint32_t h2;
       asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)two));
-      float lo, hi;
-      asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(lo), "=f"(hi) : "r"(h2));
-      v[2 * j] = lo;
-      v[2 * j + 1] = hi;
+      asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(v[2 * j]), "=f"(v[2 * j + 1]) : "r"(h2));
     } else {
       v[2 * j] = (float)(int8_t)(two & 0xFFu);
       v[2 * j + 1] = (float)(int8_t)(two >> 8);
     }
   }
+}
+
+// The same for 8-bit channels (int8, or e4m3) with a scale: 8 bytes a lane.
+__device__ __forceinline__ void act_group_q8(uint2 w, bool e4m3, float scale, int i, int tok, int grp,
+                                             const ActDst &D, bool put) {
+  float v[8];
+  q8_values(w, e4m3, v);
   float s = group_sum(sum8(v), 8) * (scale * (1.0f / kActUnit));
 #pragma unroll
   for (int j = 0; j < 8; j++) v[j] *= 64.0f;            // q 2^6: the factor is scale 2^24 / 2^6 / 2^9
@@ -120,8 +190,56 @@ __device__ __forceinline__ void act_group_q8(uint2 w, bool e4m3, float scale, in
 }
 
 // ---------------------------------------------------------------------------------------
-// 16 weight rows by 8 NT tokens
+// e0_int4_linear
 // ---------------------------------------------------------------------------------------
+// A block (one an SM, 16 warps) holds the activations of its tokens in shared memory and takes a
+// contiguous share of the rows in tiles of 16; each warp (or a team of wk warps that splits K, where
+// there are few tiles) streams its tiles through a ring of its own by cp.async, a stage of 256
+// channels.  Where the activations do not fit (many tokens times a long K), the blocks of a cluster
+// split K, and each adds up a part of the rows over the cluster's shared memory.
+//
+// Two forms.  Pair (up to 8 tokens, N tiles of 4): the 8 columns of a matrix instruction are 4 tokens
+// restricted to one group of 64 and the same 4 restricted to the next (zeros elsewhere), so a lane
+// takes 16 consecutive bytes of a row and one fold serves both groups.  Wide (N tiles of 8 tokens): 8
+// bytes of a row a lane, a fold per group.  The accumulators of a lane are rows l / 4 and l / 4 + 8,
+// tokens 2 (l & 3), + 1 of a tile (pair: tokens 2 (l & 1), + 1, after adding lanes l and l + 2).
+enum { ACT_BF16 = 0, ACT_INT8 = 1, ACT_E4M3 = 2 };
+
+struct LinearArgs {
+  const uint8_t *codes;          // [N, K / 2]
+  const uint8_t *scale, *min;    // [N, K / g] bf16
+  int N, K;
+  const uint16_t *A, *B;         // LoRA [r, K], [N, r], or nullptr
+  int r, b16;                    // b16: rows of B begin at 16 bytes and r is a multiple of 8
+  float c;
+  const void *x;                 // [T, K]
+  int x_type;
+  long long x_stride;            // elements
+  const float *x_scale;          // [T, K / x_group], or nullptr
+  int x_group;                   // channels to a scale
+  int T;
+  void *y;                       // [T, N]
+  int y_f32;
+  long long y_stride;
+  int S, kc;                     // blocks of a cluster, channels a block (a multiple of 1024 where S > 1)
+  int cs;                        // 128-channel steps to a slot of scales: 8, 4, 2; 0: 2, fetched one by one
+  int tok;                       // tokens of a block
+};
+
+constexpr int kLinThreads = 512, kLinWarps = kLinThreads / 32;
+constexpr int kLinStage = 16 * 128, kLinSlot = 16 * 32;
+constexpr int kLinPass = 128;    // rows between two exchanges of a cluster
+constexpr int lin_depth(bool wide) { return wide ? 2 : 3; }
+constexpr int lin_ring(bool wide) { return lin_depth(wide) * (kLinStage + kLinSlot); }
+__host__ __device__ inline int lin_blocks(int kc) { return (kc + 255) / 256; }
+// shared memory: zeros | t | partial sums | rings | activations of nt tokens
+__host__ __device__ inline size_t lin_fixed(bool wide, int N) {
+  return 128 + 32 * (size_t)(wide ? 8 : 4) * N * 4 + (size_t)kLinWarps * 16 * (wide ? 8 : 4) * N * 4 + (size_t)kLinWarps * lin_ring(wide);
+}
+__host__ __device__ inline size_t lin_acts(int nt, int kc) {
+  return (size_t)nt * (lin_blocks(kc) * 512 + kActPad) + (size_t)lin_blocks(kc) * 4 * ((nt + 1) / 2) * 16;
+}
+
 __device__ __forceinline__ void mma_f16_acc(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -129,348 +247,455 @@ __device__ __forceinline__ void mma_f16_acc(float (&d)[4], uint32_t a0, uint32_t
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-// One weight row as a lane sees it: its codes (already at the lane's 8 bytes of a group of 64),
-// scales and mins.
-struct Int4Row {
-  const uint8_t *c;
-  const uint16_t *s, *m;
-};
-
-__device__ __forceinline__ unsigned long long f2mul(unsigned long long a, unsigned long long b) {
-  unsigned long long d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
+// the same without a sum to add to
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Sums over the tokens of a lane's two rows: accumulator columns 2 t, 2 t + 1 of each n-tile.
-template <int NT>
-struct Int4Acc {
-  unsigned long long a[NT], b[NT];
-  __device__ __forceinline__ void clear() {
+// One fold: the sums p of a group (pair: of a lane's group of two) with its scales and mins, the
+// low (sel 0x1044) or high (0x3244) halves of the words.  sv: {factors, sums} of a lane's two tokens.
+template <int N>
+__device__ __forceinline__ void lin_fold(const float (&p)[N][4], uint32_t wsa, uint32_t wma, uint32_t wsb, uint32_t wmb,
+                                         uint32_t sel, const uint32_t (&sv)[N], float (&acc)[N][4]) {
+  auto pick = [&](uint32_t w) { return __uint_as_float(__byte_perm(w, 0u, sel)); };
+  const float sa = pick(wsa), sb = pick(wsb), ma = pick(wma), mb = pick(wmb);
 #pragma unroll
-    for (int n = 0; n < NT; n++) a[n] = b[n] = 0ull;
+  for (int q = 0; q < N; q++) {
+    const uint4 f = lds128(sv[q]);
+    const float f0 = __uint_as_float(f.x), f1 = __uint_as_float(f.y), v0 = __uint_as_float(f.z), v1 = __uint_as_float(f.w);
+    acc[q][0] = fmaf(sa, p[q][0] * f0, fmaf(ma, v0, acc[q][0]));
+    acc[q][1] = fmaf(sa, p[q][1] * f1, fmaf(ma, v1, acc[q][1]));
+    acc[q][2] = fmaf(sb, p[q][2] * f0, fmaf(mb, v0, acc[q][2]));
+    acc[q][3] = fmaf(sb, p[q][3] * f1, fmaf(mb, v1, acc[q][3]));
+  }
+}
+
+// A lane's columns: operands x, and {factors, sums} sv, advanced by 128 channels at a time.
+template <int N>
+struct LinCol {
+  uint32_t x[N], sv[N], step, svs;
+  __device__ __forceinline__ void advance() {
+#pragma unroll
+    for (int q = 0; q < N; q++) {
+      x[q] += step;
+      sv[q] += 2 * svs;
+    }
   }
 };
 
-// Adds groups [g0, g1) (of 64 channels) of rows `ra` (row l / 4 of the tile) and `rb` (row
-// l / 4 + 8).  gs: 0 when the scales are per 64, 1 when per 128.  col[n]: the lane's token
-// (column l / 4 of n-tile n) at its 16 bytes (16 (l & 3)) of group 0; sv[n]: the pair of
-// tokens 2 (l & 3), 2 (l & 3) + 1 of n-tile n in group 0, `svs` bytes from group to group.
-template <int NT>
-__device__ __forceinline__ void int4_rows(const Int4Row &ra, const Int4Row &rb, int g0, int g1, int gs,
-                                          const uint8_t *const (&col)[NT], const uint8_t *const (&sv)[NT], int svs,
-                                          Int4Acc<NT> &acc) {
+// 128 channels: the lane's codes at shared address w0 (pair: 16 bytes; wide: 8 bytes, those of the
+// second group at w1), those of 8 rows further 1024 bytes on; words of scales and mins.  hi: the
+// scales are the high halves (one scale for both groups); otherwise a half each.
+template <bool WIDE, int N, bool G128>
+__device__ __forceinline__ void lin_mul128(uint32_t w0, uint32_t w1, uint32_t wsa, uint32_t wma, uint32_t wsb, uint32_t wmb,
+                                           bool hi, const LinCol<N> &X, float (&acc)[N][4]) {
   constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
-#pragma unroll 4
-  for (int g = g0; g < g1; g++) {
-    const uint2 wa = __ldg(reinterpret_cast<const uint2 *>(ra.c + (size_t)g * 32));
-    const uint2 wb = __ldg(reinterpret_cast<const uint2 *>(rb.c + (size_t)g * 32));
-    const float sa = bf(__ldg(ra.s + (g >> gs))), ma = bf(__ldg(ra.m + (g >> gs)));
-    const float sb = bf(__ldg(rb.s + (g >> gs))), mb = bf(__ldg(rb.m + (g >> gs)));
-    float p[NT][4];
+  const int t = threadIdx.x & 3;
+  if (WIDE) {
 #pragma unroll
-    for (int n = 0; n < NT; n++)
+    for (int g = 0; g < 2; g++) {
+      const uint2 wa = lds64(g ? w1 : w0), wb = lds64((g ? w1 : w0) + 1024);
+      float p[N][4];
 #pragma unroll
-      for (int j = 0; j < 4; j++) p[n][j] = 0.f;
-    const uint32_t wa2[2] = {wa.x, wa.y}, wb2[2] = {wb.x, wb.y};
+      for (int w = 0; w < 2; w++) {
+        const uint32_t xa = w ? wa.y : wa.x, xb = w ? wb.y : wb.x, ya = xa >> 8, yb = xb >> 8;
 #pragma unroll
-    for (int w = 0; w < 2; w++) {
-      const uint32_t xa = wa2[w], xb = wb2[w], ya = xa >> 8, yb = xb >> 8;
-#pragma unroll
-      for (int n = 0; n < NT; n++) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(col[n] + g * 128 + w * 64);
-        mma_f16_acc(p[n], xa & LO, xb & LO, xa & HI, xb & HI, x.x, x.y);
-        mma_f16_acc(p[n], ya & LO, yb & LO, ya & HI, yb & HI, x.z, x.w);
+        for (int q = 0; q < N; q++) {
+          const uint4 x = lds128(X.x[q] + g * 128 + w * 64);
+          if (w == 0) mma_f16_first(p[q], xa & LO, xb & LO, xa & HI, xb & HI, x.x, x.y);
+          else mma_f16_acc(p[q], xa & LO, xb & LO, xa & HI, xb & HI, x.x, x.y);
+          mma_f16_acc(p[q], ya & LO, yb & LO, ya & HI, yb & HI, x.z, x.w);
+        }
       }
-    }
-    const unsigned long long sa2 = pk2(sa, sa), ma2 = pk2(ma, ma), sb2 = pk2(sb, sb), mb2 = pk2(mb, mb);
+      uint32_t sv[N];
 #pragma unroll
-    for (int n = 0; n < NT; n++) {
-      const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(sv[n] + (size_t)g * svs);
-      acc.a[n] = f2fma(sa2, f2mul(pk2(p[n][0], p[n][1]), f.x), f2fma(ma2, f.y, acc.a[n]));
-      acc.b[n] = f2fma(sb2, f2mul(pk2(p[n][2], p[n][3]), f.x), f2fma(mb2, f.y, acc.b[n]));
+      for (int q = 0; q < N; q++) sv[q] = X.sv[q] + g * X.svs;
+      lin_fold<N>(p, wsa, wma, wsb, wmb, (G128 ? hi : g) ? 0x3244u : 0x1044u, sv, acc);
     }
-  }
-}
-
-// ---------------------------------------------------------------------------------------
-// 16 weight rows by up to 8 tokens: two groups to a matrix instruction
-// ---------------------------------------------------------------------------------------
-// With few tokens the 8 columns of a matrix instruction hold 4 tokens twice: columns 0..3 the
-// tokens restricted to a group of 64, columns 4..7 restricted to the next one (zero elsewhere).
-// A lane then takes 16 consecutive bytes of a row, its four lanes cover two groups, the sums of
-// the two come out in different columns, and there is one fold for both.  The lane (row l / 4,
-// t = l & 3) holds tokens 2 (t & 1), 2 (t & 1) + 1 of group t / 2 in its accumulators; lanes t
-// and t + 2 are added at the end.
-//
-// A block is 256 channels of 16 rows: 4 loads of codes and 4 of scales and mins a lane.
-
-struct PairBlk {
-  uint4 a[2], b[2];
-  uint2 sa, ma, sb, mb;
-};
-
-__device__ __forceinline__ uint4 ldg_stream(const void *p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-
-// Block b of rows whose codes start at the lane's 16 bytes of the row.  G128: scales per 128
-// (two a block) instead of per 64 (four).
-template <bool G128>
-__device__ __forceinline__ void pair_load(PairBlk &B, const Int4Row &ra, const Int4Row &rb, int b) {
-  B.a[0] = ldg_stream(ra.c + (size_t)b * 128);
-  B.a[1] = ldg_stream(ra.c + (size_t)b * 128 + 64);
-  B.b[0] = ldg_stream(rb.c + (size_t)b * 128);
-  B.b[1] = ldg_stream(rb.c + (size_t)b * 128 + 64);
-  if (G128) {
-    B.sa.x = __ldg(reinterpret_cast<const uint32_t *>(ra.s + b * 2));
-    B.ma.x = __ldg(reinterpret_cast<const uint32_t *>(ra.m + b * 2));
-    B.sb.x = __ldg(reinterpret_cast<const uint32_t *>(rb.s + b * 2));
-    B.mb.x = __ldg(reinterpret_cast<const uint32_t *>(rb.m + b * 2));
   } else {
-    B.sa = __ldg(reinterpret_cast<const uint2 *>(ra.s + b * 4));
-    B.ma = __ldg(reinterpret_cast<const uint2 *>(ra.m + b * 4));
-    B.sb = __ldg(reinterpret_cast<const uint2 *>(rb.s + b * 4));
-    B.mb = __ldg(reinterpret_cast<const uint2 *>(rb.m + b * 4));
-  }
-}
-
-// The lane's view of the activations of NP times 4 tokens (n of them, at rows `at`.. of D;
-// `at` even).  zero: 128 bytes of zeros in shared memory, 16-byte aligned.
-template <int NP>
-struct PairCol {
-  const uint8_t *col[NP], *sv[NP];
-  int step, svs;
-  uint32_t sel;
-  __device__ __forceinline__ PairCol(const ActDst &D, int at, int n, const uint8_t *zero) {
-    const int lane = threadIdx.x & 31, t = lane & 3, c = lane >> 2;
-    const bool mine = (t >> 1) == (c >> 2);
-    step = mine ? 256 : 0;
-    svs = D.pairs * 16;
-    sel = t >> 1 ? 0x3244u : 0x1044u;
-#pragma unroll
-    for (int q = 0; q < NP; q++) {
-      col[q] = mine ? D.op + (size_t)(at + min(4 * q + (c & 3), n - 1)) * D.pitch + (t >> 1) * 128 + (t & 1) * 32 : zero;
-      sv[q] = reinterpret_cast<const uint8_t *>(D.sv) + (at / 2 + min(2 * q + (t & 1), (n - 1) / 2)) * 16 + (t >> 1) * svs;
-    }
-  }
-};
-
-template <int NP, bool G128>
-__device__ __forceinline__ void pair_mul(const PairBlk &B, int b, const PairCol<NP> &X, Int4Acc<NP> &acc) {
-  constexpr uint32_t LO = 0x000F000Fu, HI = 0x00F000F0u;
-#pragma unroll
-  for (int j = 0; j < 2; j++) {
-    const uint32_t wa[4] = {B.a[j].x, B.a[j].y, B.a[j].z, B.a[j].w}, wb[4] = {B.b[j].x, B.b[j].y, B.b[j].z, B.b[j].w};
-    float p[NP][4];
-#pragma unroll
-    for (int q = 0; q < NP; q++) p[q][0] = p[q][1] = p[q][2] = p[q][3] = 0.f;
+    const uint4 wa = lds128(w0), wb = lds128(w0 + 1024);
+    // (one tile of tokens: two chains of dependent instructions, joined at the fold)
+    float p[N][4], p2[4];
 #pragma unroll
     for (int w = 0; w < 4; w++) {
-      const uint32_t xa = wa[w], xb = wb[w], ya = xa >> 8, yb = xb >> 8;
+      const uint32_t xa = w == 0 ? wa.x : w == 1 ? wa.y : w == 2 ? wa.z : wa.w;
+      const uint32_t xb = w == 0 ? wb.x : w == 1 ? wb.y : w == 2 ? wb.z : wb.w, ya = xa >> 8, yb = xb >> 8;
 #pragma unroll
-      for (int q = 0; q < NP; q++) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(X.col[q] + (2 * b + j) * X.step + (w & 1) * 64 + (w >> 1) * 16);
-        mma_f16_acc(p[q], xa & LO, xb & LO, xa & HI, xb & HI, x.x, x.y);
-        mma_f16_acc(p[q], ya & LO, yb & LO, ya & HI, yb & HI, x.z, x.w);
+      for (int q = 0; q < N; q++) {
+        // chunk 4 (t & 1) + w of the group: word w & 1, lane 2 (t & 1) + w / 2 of it
+        const uint4 x = lds128(X.x[q] + (w & 1) * 64 + (w >> 1) * 16);
+        if (w == 0) mma_f16_first(p[q], xa & LO, xb & LO, xa & HI, xb & HI, x.x, x.y);
+        else mma_f16_acc(p[q], xa & LO, xb & LO, xa & HI, xb & HI, x.x, x.y);
+        if (N > 1) mma_f16_acc(p[q], ya & LO, yb & LO, ya & HI, yb & HI, x.z, x.w);
+        else if (w == 0) mma_f16_first(p2, ya & LO, yb & LO, ya & HI, yb & HI, x.z, x.w);
+        else mma_f16_acc(p2, ya & LO, yb & LO, ya & HI, yb & HI, x.z, x.w);
       }
     }
-    const uint32_t sel = G128 ? (j ? 0x3244u : 0x1044u) : X.sel;
-    auto pick = [&](const uint2 &v) {
-      const float f = __uint_as_float(__byte_perm(G128 || j == 0 ? v.x : v.y, 0u, sel));
-      return pk2(f, f);
-    };
-    const unsigned long long sa = pick(B.sa), ma = pick(B.ma), sb = pick(B.sb), mb = pick(B.mb);
+    if (N == 1)
 #pragma unroll
-    for (int q = 0; q < NP; q++) {
-      const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(X.sv[q] + (4 * b + 2 * j) * X.svs);
-      acc.a[q] = f2fma(sa, f2mul(pk2(p[q][0], p[q][1]), f.x), f2fma(ma, f.y, acc.a[q]));
-      acc.b[q] = f2fma(sb, f2mul(pk2(p[q][2], p[q][3]), f.x), f2fma(mb, f.y, acc.b[q]));
-    }
+      for (int i = 0; i < 4; i++) p[0][i] += p2[i];
+    lin_fold<N>(p, wsa, wma, wsb, wmb, (G128 ? hi : t >> 1) ? 0x3244u : 0x1044u, X.sv, acc);
   }
 }
 
-// Adds lanes t and t + 2: every lane then holds the sums of tokens 2 (t & 1), 2 (t & 1) + 1.
-template <int NP>
-__device__ __forceinline__ void pair_join(Int4Acc<NP> &acc) {
-#pragma unroll
-  for (int q = 0; q < NP; q++) {
-    acc.a[q] = f2add(acc.a[q], __shfl_xor_sync(0xffffffffu, acc.a[q], 2));
-    acc.b[q] = f2add(acc.b[q], __shfl_xor_sync(0xffffffffu, acc.b[q], 2));
-  }
+// y[tok][row] from the whole sum, with the LoRA where it has not been added yet
+__device__ __forceinline__ void lin_store(const LinearArgs &L, int tok, int row, float v) {
+  const long long at = (long long)tok * L.y_stride + row;
+  if (L.y_f32)
+    ((float *)L.y)[at] = v;
+  else
+    ((uint16_t *)L.y)[at] = f2bf(v);
 }
 
-// A warp's jobs one after another, each blocks [b0, b1) of 16 rows, with the loads of the next
-// blocks in flight, across the end of a job too.  rows(j, ra, rb) gives job j's rows,
-// cols(j) its activations, done(j, acc) takes its sums.
-template <int NP, bool G128, class Rows, class Cols, class Done>
-__device__ __forceinline__ void pair_stream(int jobs, int b0, int b1, Rows rows, Cols cols, Done done) {
-  if (jobs <= 0 || b0 >= b1) return;
-  constexpr int D = NP == 1 ? 3 : 2;      // two tiles of tokens leave registers for one less
-  PairBlk buf[D];
-  Int4Row ra, rb;
-  int lj = 0, lb = b0;                    // the next block to load
-  auto load = [&](PairBlk &B) {
-    if (lj >= jobs) return;
-    if (lb == b0) rows(lj, ra, rb);
-    pair_load<G128>(B, ra, rb, lb);
-    if (++lb == b1) {
-      lb = b0;
-      lj++;
-    }
-  };
-#pragma unroll
-  for (int u = 0; u < D - 1; u++) load(buf[u]);
-  Int4Acc<NP> acc;
-  acc.clear();
-  PairCol<NP> X = cols(0);
-  for (int j = 0, b = b0;;) {
-#pragma unroll
-    for (int u = 0; u < D; u++) {
-      load(buf[(u + D - 1) % D]);
-      pair_mul<NP, G128>(buf[u], b, X, acc);
-      if (++b == b1) {
-        pair_join(acc);
-        done(j, acc);
-        if (++j == jobs) return;
-        acc.clear();
-        X = cols(j);
-        b = b0;
-      }
-    }
+// c B t of one row and token (t: 32 floats in shared memory)
+__device__ __forceinline__ float lin_lora(const LinearArgs &L, int row, const float *t) {
+  const uint16_t *b = L.B + (long long)row * L.r;
+  float s = 0.f;
+  if (L.b16) {
+#pragma unroll 2
+    for (int j = 0; j < L.r; j += 8)
+      s = dot8(__ldg(reinterpret_cast<const uint4 *>(b + j)), *reinterpret_cast<const float4 *>(t + j),
+               *reinterpret_cast<const float4 *>(t + j + 4), s);
+  } else {
+#pragma unroll 2
+    for (int j = 0; j < L.r; j++) s = fmaf(bf(b[j]), t[j], s);
   }
+  return L.c * s;
 }
 
-// ---------------------------------------------------------------------------------------
-// e0_int4_linear
-// ---------------------------------------------------------------------------------------
-enum { ACT_BF16 = 0, ACT_INT8 = 1, ACT_E4M3 = 2 };
-
-struct LinearArgs {
-  const uint8_t *codes;       // [N, K / 2]
-  const uint16_t *scale, *min;   // [N, K / g]
-  int N, K, gs;               // gs: 0 for g = 64, 1 for g = 128
-  const uint16_t *A, *B;      // LoRA [r, K], [N, r], or nullptr
-  int r;
-  float c;
-  const void *x;              // [T, K]
-  int x_type;
-  long long x_stride;         // elements
-  const float *x_scale;       // [T, K / x_group], or nullptr
-  int x_group;                // channels to a scale
-  int T;
-  void *y;                    // [T, N]
-  int y_f32;
-  long long y_stride;
-  int kc;                     // groups of 64 to a chunk of the activations
-};
-
-constexpr int kLinThreads = 256;
-constexpr int kLinRows = 16;
-
-template <int NT>
-__global__ void __launch_bounds__(kLinThreads) k_int4_linear(LinearArgs L) {
+template <bool WIDE, int N, bool G128>
+__global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_constant__ LinearArgs L) {
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int TT = 8 * NT, NW = kLinThreads / 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t0 = blockIdx.y * TT, nt = min(TT, L.T - t0);
-  const int row0 = blockIdx.x * kLinRows;
-  const int G = L.K / 64, pitch = act_pitch(L.kc);
-  ActDst D{smem, reinterpret_cast<float *>(smem + TT * pitch), pitch, TT / 2};
-  float *red = reinterpret_cast<float *>(smem);        // [NW][16][TT], after the last chunk
-  __shared__ float lt[TT][32];
-  // rows past the end read the last row and are not stored
-  auto row_at = [&](int r) {
-    const long long n = min(row0 + r, L.N - 1);
-    return Int4Row{L.codes + n * (L.K / 2) + (lane & 3) * 8, L.scale + n * (G >> L.gs), L.min + n * (G >> L.gs)};
-  };
-  const Int4Row ra = row_at(lane >> 2), rb = row_at((lane >> 2) + 8);
-  Int4Acc<NT> acc;
-  acc.clear();
-  const uint8_t *col[NT], *sv[NT];
+  constexpr int TOK = N * (WIDE ? 8 : 4), DEPTH = lin_depth(WIDE);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, t = lane & 3;
+  const int rank = blockIdx.x % L.S, part = blockIdx.x / L.S, parts = gridDim.x / L.S;
+  const int t0 = blockIdx.y * L.tok, nt = min(L.tok, L.T - t0);
+  // (the last blocks of a cluster may have fewer channels, or none)
+  const int k0 = min(rank * L.kc, L.K), kc = min(L.kc, L.K - k0), NB = lin_blocks(kc), NBmost = lin_blocks(L.kc);
+  const int row_lo = (int)((long long)L.N * part / parts), row_hi = (int)((long long)L.N * (part + 1) / parts);
+  // shared memory
+  float *lt = reinterpret_cast<float *>(smem + 128);                 // [TOK][32]
+  float *red = lt + TOK * 32;                                        // [16 warps][16 rows][TOK], or [pass rows][TOK]
+  const uint32_t ring = smem_at(red + kLinWarps * 16 * TOK) + warp * lin_ring(WIDE);
+  uint8_t *ops = reinterpret_cast<uint8_t *>(red + kLinWarps * 16 * TOK) + kLinWarps * lin_ring(WIDE);
+  const int pitch = NB * 512 + kActPad, pairs = (nt + 1) / 2;
+  const ActDst D{ops, reinterpret_cast<float *>(ops + (size_t)nt * pitch), pitch, pairs};
+  const uint32_t zero = smem_at(smem);
+  if (tid < 32) reinterpret_cast<uint32_t *>(smem)[tid] = 0;
+
+  // ---- the ring: slots of scales, then the stages
+  const uint32_t slots = ring, slots_end = slots + DEPTH * kLinSlot, end = slots_end + DEPTH * kLinStage;
+  const int cr = lane >> 3, cc = lane & 7, sr = lane >> 1, cs = L.cs ? L.cs : 2;
+  const uint32_t cdst = cr * 128 + ((cc ^ row_swz(cr)) << 4), sdst = sr * 32 + (lane & 1) * 16;
+  const int Gn = L.K / (G128 ? 128 : 64);                            // scales of a row
+  int lj = 0, jobs = 0, lb = 0, b0 = 0, b1 = 0, step = 1, tile0 = 0, tiles = 0, base = 0, top = 0;
+  const uint8_t *cp = nullptr, *sp = nullptr;
+  int o[4] = {};
+  uint32_t lst = slots_end, lsl = slots;
+  // tile q of the pass: rows base + 16 q .., at most to top
+  auto issue = [&]() {
+    if (lj < jobs) {
+      if (lb == b0) {
+        const int row = base + (tile0 + lj * step) * 16, nr = min(16, top - row);
+        cp = L.codes + (long long)row * (L.K / 2) + k0 / 2 + b0 * 128 + cc * 16;
 #pragma unroll
-  for (int n = 0; n < NT; n++) {
-    col[n] = D.op + min(8 * n + (lane >> 2), nt - 1) * pitch + (lane & 3) * 16;
-    sv[n] = reinterpret_cast<const uint8_t *>(D.sv) + (4 * n + (lane & 3)) * 16;
-  }
-  for (int c0 = 0; c0 < G; c0 += L.kc) {
-    const int gc = min(L.kc, G - c0);
-    __syncthreads();
-    // activations of the chunk: 8 lanes to a token's group
-    for (int u0 = 0; u0 < nt * gc; u0 += kLinThreads / 8) {
-      const int u = u0 + tid / 8, i = tid & 7;
-      const bool in = u < nt * gc;
-      const int tok = in ? u / gc : 0, grp = in ? u % gc : 0;
-      const long long k = (long long)(c0 + grp) * 64 + i * 8, base = (long long)(t0 + tok) * L.x_stride;
-      if (L.x_type == ACT_BF16) {
-        act_group_bf16(*reinterpret_cast<const uint4 *>((const uint16_t *)L.x + base + k), i, tok, grp, D, in);
-      } else {
-        const float s = L.x_scale[(long long)(t0 + tok) * (L.K / L.x_group) + k / L.x_group];
-        act_group_q8(*reinterpret_cast<const uint2 *>((const uint8_t *)L.x + base + k), L.x_type == ACT_E4M3, s, i, tok,
-                     grp, D, in);
+        for (int i = 0; i < 4; i++) o[i] = min(cr + 4 * i, nr - 1) * (L.K / 2);
+        sp = (lane & 1 ? L.min : L.scale) + ((long long)(row + min(sr, nr - 1)) * Gn + (k0 + (2 * b0 & -cs) * 128) / (G128 ? 128 : 64)) * 2;
       }
-    }
-    __syncthreads();
-    const int per = (gc + NW - 1) / NW, g0 = min(warp * per, gc), g1 = min(g0 + per, gc);
-    const Int4Row pa{ra.c + (size_t)c0 * 32, ra.s + (c0 >> L.gs), ra.m + (c0 >> L.gs)};
-    const Int4Row pb{rb.c + (size_t)c0 * 32, rb.s + (c0 >> L.gs), rb.m + (c0 >> L.gs)};
-    int4_rows<NT>(pa, pb, g0, g1, L.gs, col, sv, TT / 2 * 16, acc);
-  }
-  // LoRA: t = A x, one warp to a (token, rank) pair at a time
-  if (L.A) {
-    for (int u = warp; u < nt * L.r; u += NW) {
-      const int tok = u / L.r, rr = u % L.r;
-      const long long base = (long long)(t0 + tok) * L.x_stride;
-      float s = 0.f;
-      for (int k = lane; k < L.K; k += 32) {
-        float xv;
-        if (L.x_type == ACT_BF16) {
-          xv = bf(((const uint16_t *)L.x)[base + k]);
+      if (lb == b0 || (2 * lb & (cs - 1)) == 0) {
+        const int ch = (2 * lb & -cs) * 128, bytes = min(cs * 128, kc - ch) / (G128 ? 128 : 64) * 2;
+        if (L.cs == 0) {
+          // rows of an odd number of groups, or no aligned base: one by one
+          const uint16_t *p = reinterpret_cast<const uint16_t *>(sp);
+          uint32_t w[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            if (2 * i < bytes) w[i >> 1] |= (uint32_t)__ldg(p + i) << (16 * (i & 1));
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(lsl + sdst), "r"(w[0]), "r"(w[1]) : "memory");
+        } else if (cs * (G128 ? 2 : 4) == 16) {
+          cp_async_part<16>(lsl + sdst, sp, bytes);
+        } else if (cs * (G128 ? 2 : 4) == 8) {
+          cp_async_part<8>(lsl + sdst, sp, bytes);
         } else {
-          const uint8_t b = ((const uint8_t *)L.x)[base + k];
-          if (L.x_type == ACT_INT8) {
-            xv = (float)(int8_t)b;
-          } else {
-            uint32_t h2;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)b));
-            asm("{.reg .f16 a, b; mov.b32 {a, b}, %1; cvt.f32.f16 %0, a;}" : "=f"(xv) : "r"(h2));
-          }
-          xv *= L.x_scale[(long long)(t0 + tok) * (L.K / L.x_group) + k / L.x_group];
+          cp_async_part<4>(lsl + sdst, sp, bytes);
         }
-        s = fmaf(bf(L.A[(long long)rr * L.K + k]), xv, s);
+        sp += cs * (G128 ? 2 : 4);
+        lsl = lsl + kLinSlot == slots_end ? slots : lsl + kLinSlot;
       }
-      s = warp_sum(s);
-      if (lane == 0) lt[tok][rr] = s;
-    }
-  }
-  __syncthreads();
+      if ((lb + 1) * 256 <= kc) {
 #pragma unroll
-  for (int n = 0; n < NT; n++) {
-    float *p = red + (size_t)warp * 16 * TT + (lane >> 2) * TT + 8 * n + 2 * (lane & 3);
-    *reinterpret_cast<unsigned long long *>(p) = acc.a[n];
-    *reinterpret_cast<unsigned long long *>(p + 8 * TT) = acc.b[n];
+        for (int i = 0; i < 4; i++) cp_async16(lst + cdst + i * 512, cp + o[i]);
+      } else {
+        const int bytes = lb * 256 + cc * 32 < kc ? 16 : 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++) cp_async_part<16>(lst + cdst + i * 512, bytes ? cp + o[i] : L.codes, bytes);
+      }
+      cp += 128;
+      lst = lst + kLinStage == end ? slots_end : lst + kLinStage;
+      if (++lb == b1) {
+        lb = b0;
+        lj++;
+      }
+    }
+    cp_async_commit();
+  };
+  int wk = 1, team = 0, sub = 0;
+  // the tiles of rows [lo, hi): warps to a tile so that the last round is full, no more than there
+  // are blocks of K (the same in every block of a cluster); a warp without a block adds nothing
+  auto begin = [&](int lo, int hi) {
+    base = lo;
+    top = hi;
+    tiles = (hi - lo + 15) / 16;
+    int best = 1 << 30, lg = 0;
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      const int cost = (((tiles << g) + 15) >> 4 << (4 - g)) + g;
+      if ((1 << g) <= NBmost && cost < best) {
+        best = cost;
+        lg = g;
+      }
+    }
+    wk = 1 << lg;
+    team = warp >> lg;
+    sub = warp & (wk - 1);
+    step = kLinWarps >> lg;
+    tile0 = team;
+    jobs = (tiles - team + step - 1) >> (4 - lg);
+    b0 = lb = NB * sub >> lg;
+    b1 = NB * (sub + 1) >> lg;
+    lj = b0 < b1 ? 0 : jobs;
+    __syncwarp();
+#pragma unroll 1
+    for (int u = 1; u < DEPTH; u++) issue();
+  };
+  const int pass = L.S > 1 ? kLinPass : row_hi - row_lo;
+  begin(row_lo, min(row_lo + pass, row_hi));
+
+  // ---- the activations of this block's channels: 8 lanes to a token's group, zeros behind the last
+  {
+    const int G = NB * 4, units = nt * G, i = tid & 7;
+    auto load = [&](int u, uint4 &w, float &s) {
+      w = make_uint4(0, 0, 0, 0);
+      s = 0.f;
+      const int tok = u / G, k = (u - tok * G) * 64;
+      if (u < units && k < kc) {
+        const long long at = (long long)(t0 + tok) * L.x_stride + k0 + k + i * 8;
+        if (L.x_type == ACT_BF16) {
+          w = __ldg(reinterpret_cast<const uint4 *>((const uint16_t *)L.x + at));
+        } else {
+          const uint2 v = __ldg(reinterpret_cast<const uint2 *>((const uint8_t *)L.x + at));
+          w.x = v.x;
+          w.y = v.y;
+          s = __ldg(L.x_scale + (long long)(t0 + tok) * (L.K / L.x_group) + (k0 + k) / L.x_group);
+        }
+      }
+    };
+#pragma unroll 1
+    for (int u0 = tid >> 3; u0 - (tid >> 3) < units; u0 += 4 * (kLinThreads / 8)) {
+      uint4 w[4];
+      float s[4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) load(u0 + j * (kLinThreads / 8), w[j], s[j]);
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int u = u0 + j * (kLinThreads / 8), tok = u / G, g = u - tok * G;
+        if (L.x_type == ACT_BF16)
+          act_group_bf16(w[j], i, tok, g, D, u < units);
+        else
+          act_group_q8(make_uint2(w[j].x, w[j].y), L.x_type == ACT_E4M3, s[j], i, tok, g, D, u < units);
+      }
+    }
+  }
+  // ---- t = A x of this block's channels, K split over the warps: 16 ranks by 8 tokens at a time
+  if (L.A) {
+    const int G = kc / 64;
+#pragma unroll 1
+    for (int u = 0; u < (L.r + 15) / 16 * ((nt + 7) / 8); u++) {
+      const int q = u / ((nt + 7) / 8) * 16, tt = u % ((nt + 7) / 8) * 8;
+      const uint16_t *ra = L.A + (long long)min(q + r, L.r - 1) * L.K + k0 + t * 8;
+      const uint16_t *rb = L.A + (long long)min(q + r + 8, L.r - 1) * L.K + k0 + t * 8;
+      const int tok = min(tt + r, nt - 1);
+      const long long xa = (long long)(t0 + tok) * L.x_stride + k0 + t * 8;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+      for (int g = G * warp / kLinWarps; g < G * (warp + 1) / kLinWarps; g++) {
+        float p[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+          const int k = g * 64 + h * 32;
+          uint4 x;
+          if (L.x_type == ACT_BF16) {
+            x = __ldg(reinterpret_cast<const uint4 *>((const uint16_t *)L.x + xa + k));
+          } else {
+            float v[8];
+            q8_values(__ldg(reinterpret_cast<const uint2 *>((const uint8_t *)L.x + xa + k)), L.x_type == ACT_E4M3, v);
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) w[j] = (__float_as_uint(v[2 * j]) >> 16) | (__float_as_uint(v[2 * j + 1]) & 0xFFFF0000u);
+            x = make_uint4(w[0], w[1], w[2], w[3]);            // codes are exact in bf16
+          }
+          bf16_mul(__ldg(reinterpret_cast<const uint4 *>(ra + k)), __ldg(reinterpret_cast<const uint4 *>(rb + k)), x, p);
+        }
+        // columns 2 t, 2 t + 1 are tokens of their own scales
+        float s0 = 1.f, s1 = 1.f;
+        if (L.x_type != ACT_BF16) {
+          const int gs = (k0 + g * 64) / L.x_group, ng = L.K / L.x_group;
+          s0 = __ldg(L.x_scale + (long long)(t0 + min(tt + 2 * t, nt - 1)) * ng + gs);
+          s1 = __ldg(L.x_scale + (long long)(t0 + min(tt + 2 * t + 1, nt - 1)) * ng + gs);
+        }
+        acc[0] = fmaf(s0, p[0], acc[0]);
+        acc[1] = fmaf(s1, p[1], acc[1]);
+        acc[2] = fmaf(s0, p[2], acc[2]);
+        acc[3] = fmaf(s1, p[3], acc[3]);
+      }
+      float *p = red + warp * 128 + r * 8 + 2 * t;               // TOK >= 4: 16 warps of 64 floats or more
+      if (TOK >= 8) {
+        p[0] = acc[0];
+        p[1] = acc[1];
+        p[64] = acc[2];
+        p[65] = acc[3];
+      } else if (t < 2) {                                        // 4 tokens: columns 0..3
+        p = red + warp * 64 + r * 4 + 2 * t;
+        p[0] = acc[0];
+        p[1] = acc[1];
+        p[32] = acc[2];
+        p[33] = acc[3];
+      }
+      __syncthreads();
+      constexpr int W = TOK >= 8 ? 8 : 4;
+      if (tid < 16 * W) {
+        const int row = q + tid / W, tk = tt + tid % W;
+        if (row < L.r && tk < nt) {
+          float s = 0.f;
+#pragma unroll
+          for (int w = 0; w < kLinWarps; w++) s += red[w * 16 * W + tid];
+          lt[tk * 32 + row] = s;
+        }
+      }
+      __syncthreads();
+    }
   }
   __syncthreads();
-  for (int o = tid; o < 16 * nt; o += kLinThreads) {
-    const int tok = o / 16, r = o % 16, n = row0 + r;
-    if (n >= L.N) continue;
-    float s = 0.f;
-    for (int w = 0; w < NW; w++) s += red[(size_t)w * 16 * TT + r * TT + tok];
-    s *= kActUnit;
-    if (L.A) {
-      float b = 0.f;
-      for (int j = 0; j < L.r; j++) b = fmaf(bf(L.B[(long long)n * L.r + j]), lt[tok][j], b);
-      s = fmaf(L.c, b, s);
+
+  // ---- the tiles
+  const int swz = row_swz(r);
+  const uint32_t w_at = r * 128 + (((WIDE ? t >> 1 : t) ^ swz) << 4) + (WIDE ? (t & 1) * 8 : 0);
+  const uint32_t w_at1 = r * 128 + (((2 + (t >> 1)) ^ swz) << 4) + (t & 1) * 8;
+  const bool mine = WIDE || (t >> 1) == (r >> 2);
+  LinCol<N> X0;
+  X0.step = mine ? 256 : 0;
+  X0.svs = pairs * 16;
+#pragma unroll
+  for (int q = 0; q < N; q++) {
+    const int tok = min(WIDE ? 8 * q + r : 4 * q + (r & 3), nt - 1), pair = min(WIDE ? 4 * q + t : 2 * q + (t & 1), pairs - 1);
+    X0.x[q] = mine ? smem_at(D.op) + tok * pitch + (WIDE ? t * 16 : (t >> 1) * 128 + (t & 1) * 32) : zero;
+    X0.sv[q] = smem_at(D.sv) + pair * 16 + (WIDE ? 0 : (t >> 1) * X0.svs);
+  }
+  uint32_t st = slots_end, sl = slots_end - kLinSlot;
+  for (int lo = row_lo; lo < row_hi; lo += pass) {
+    const int hi = min(lo + pass, row_hi);
+    if (lo != row_lo) begin(lo, hi);
+    // begin() starts where the ring stands
+#pragma unroll 1
+    for (int j = 0; j < jobs; j++) {
+      const int row = lo + (tile0 + j * step) * 16;
+      float acc[N][4];
+#pragma unroll
+      for (int q = 0; q < N; q++) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
+      LinCol<N> X = X0;
+#pragma unroll
+      for (int q = 0; q < N; q++) {
+        X.x[q] += 2 * b0 * X.step;
+        X.sv[q] += 4 * b0 * X.svs;
+      }
+#pragma unroll 1
+      for (int b = b0; b < b1; b++) {
+        cp_async_wait_but<DEPTH - 2>();
+        __syncwarp();                     // the block has arrived, and every lane has left the one before
+        issue();
+        const int at = 2 * b & (cs - 1);
+        if (b == b0 || at == 0) sl = sl + kLinSlot == slots_end ? slots : sl + kLinSlot;
+        const uint32_t sc = sl + r * 32 + at * (G128 ? 2 : 4);
+        uint2 sa, ma, sb, mb;
+        if (G128) {
+          sa.x = sa.y = lds32u(sc);
+          ma.x = ma.y = lds32u(sc + 16);
+          sb.x = sb.y = lds32u(sc + 256);
+          mb.x = mb.y = lds32u(sc + 272);
+        } else {
+          sa = lds64(sc);
+          ma = lds64(sc + 16);
+          sb = lds64(sc + 256);
+          mb = lds64(sc + 272);
+        }
+        lin_mul128<WIDE, N, G128>(st + w_at, st + w_at1, sa.x, ma.x, sb.x, mb.x, false, X, acc);
+        X.advance();
+        // chunk c + 4 lies 64 bytes from chunk c, on the side that the permutation leaves
+        lin_mul128<WIDE, N, G128>(st + (w_at ^ 64), st + (w_at1 ^ 64), sa.y, ma.y, sb.y, mb.y, true, X, acc);
+        X.advance();
+        st = st + kLinStage == end ? slots_end : st + kLinStage;
+      }
+      // pair: lanes l and l + 2 hold the same two tokens and take one each; wide: both tokens
+#pragma unroll
+      for (int q = 0; q < N; q++) {
+        if (!WIDE)
+#pragma unroll
+          for (int i = 0; i < 4; i++) acc[q][i] += __shfl_xor_sync(0xffffffffu, acc[q][i], 2);
+#pragma unroll
+        for (int h = 0; h < (WIDE ? 2 : 1); h++) {
+          const int odd = WIDE ? h : t >> 1, tok = WIDE ? 8 * q + 2 * t + h : 4 * q + 2 * (t & 1) + odd;
+          if (tok >= nt) continue;
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const float v = (e ? (odd ? acc[q][3] : acc[q][2]) : (odd ? acc[q][1] : acc[q][0])) * kActUnit;
+            const int rr = r + 8 * e;
+            if (wk > 1)
+              red[(warp * 16 + rr) * TOK + tok] = v;
+            else if (L.S > 1)
+              red[(row - lo + rr) * TOK + tok] = L.A && row + rr < hi ? v + lin_lora(L, row + rr, lt + tok * 32) : v;
+            else if (row + rr < hi)
+              lin_store(L, t0 + tok, row + rr, L.A ? v + lin_lora(L, row + rr, lt + tok * 32) : v);
+          }
+        }
+      }
+      if (wk > 1) {
+        bar_team(wk, team);
+        float *p = red + team * wk * 16 * TOK;
+#pragma unroll 1
+        for (int u = sub * 32 + lane; u < 16 * TOK; u += wk * 32) {
+          const int rr = u / TOK, tok = u % TOK;
+          if (tok >= nt || row + rr >= hi) continue;
+          float v = p[u];
+#pragma unroll 1
+          for (int w = 1; w < wk; w++) v += p[w * 16 * TOK + u];
+          if (L.A) v += lin_lora(L, row + rr, lt + tok * 32);
+          if (L.S > 1)
+            p[u] = v;                     // the team's first warp's sums, at the tile's place (below)
+          else
+            lin_store(L, t0 + tok, row + rr, v);
+        }
+        bar_team(wk, team);
+      }
     }
-    const long long at = (long long)(t0 + tok) * L.y_stride + n;
-    if (L.y_f32)
-      ((float *)L.y)[at] = s;
-    else
-      ((uint16_t *)L.y)[at] = f2bf(s);
+    if (L.S > 1) {
+      // rows of a tile: with a team of wk warps a pass has at most 16 / wk tiles, tile q at wk 16 q
+      // rows; else at 16 q rows
+      cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
+      cluster.sync();
+      for (int u = rank * kLinThreads + tid; u < (hi - lo) * TOK; u += L.S * kLinThreads) {
+        const int rr = u / TOK, tok = u % TOK;
+        if (tok >= nt) continue;
+        const int at = ((rr >> 4) * wk * 16 + (rr & 15)) * TOK + tok;
+        float v = 0.f;
+        for (int w = 0; w < L.S; w++) v += cluster.map_shared_rank(red, w)[at];
+        lin_store(L, t0 + tok, lo + rr, v);
+      }
+      cluster.sync();
+    }
   }
 }
 
