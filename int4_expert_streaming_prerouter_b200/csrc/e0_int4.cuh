@@ -101,6 +101,7 @@ __device__ __forceinline__ void bf16_mul(uint4 a, uint4 b, uint4 x, float (&acc)
 // word in one 16-byte access.  `sv` holds, for each group and pair of tokens, {factor of the
 // first, of the second, sum of the first, of the second}.  factor and sum carry 2^-9, which
 // the end result is multiplied with once, so that no factor overflows.
+enum { ACT_BF16 = 0, ACT_INT8 = 1, ACT_E4M3 = 2 };
 constexpr float kActUnit = 512.0f;
 constexpr int kActPad = 64;               // per token, so that the tokens of a load fall into distinct banks
 
@@ -135,32 +136,6 @@ struct ActDst {
   }
 };
 
-// Eight lanes (i = 0..7) bring one token's group of 64 bf16 channels, 8 each, into place.
-// All 32 lanes of the warp call it together.
-__device__ __forceinline__ void act_group_bf16(uint4 w, int i, int tok, int grp, const ActDst &D, bool put) {
-  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-  float v[8];
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < 4; j++) {
-    m = max(m, max(ws[j] & 0x7FFFu, (ws[j] >> 16) & 0x7FFFu));
-    v[2 * j] = __uint_as_float(ws[j] << 16);
-    v[2 * j + 1] = __uint_as_float(ws[j] & 0xFFFF0000u);
-  }
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
-  // largest in [2^(eb-127), 2^(eb-126)) -> [2^15, 2^16); a group with a NaN or an infinity
-  // keeps it (eb = 255 makes the factor infinite), so its outputs are not finite
-  const uint32_t eb = max(m >> 7, 15u);
-  const float up = __uint_as_float((269u - eb) << 23), factor = __uint_as_float(eb << 23);
-  float s = sum8(v) * (1.0f / kActUnit);
-  s = group_sum(s, 8);
-#pragma unroll
-  for (int j = 0; j < 8; j++) v[j] *= up;
-  if (put) D.put(tok, grp, i, act_pack(v), factor, s);
-}
-
 // The values of 8 int8 or e4m3 codes.
 __device__ __forceinline__ void q8_values(uint2 w, bool e4m3, float (&v)[8]) {
   const uint32_t ws[2] = {w.x, w.y};
@@ -178,15 +153,37 @@ __device__ __forceinline__ void q8_values(uint2 w, bool e4m3, float (&v)[8]) {
   }
 }
 
-// The same for 8-bit channels (int8, or e4m3) with a scale: 8 bytes a lane.
-__device__ __forceinline__ void act_group_q8(uint2 w, bool e4m3, float scale, int i, int tok, int grp,
-                                             const ActDst &D, bool put) {
-  float v[8];
-  q8_values(w, e4m3, v);
-  float s = group_sum(sum8(v), 8) * (scale * (1.0f / kActUnit));
+// The values of 8 channels, which bf16 holds exactly: of bf16 (w) or of 8-bit codes (its first half).
+__device__ __forceinline__ void act_values(uint4 w, int type, float (&v)[8]) {
+  if (type != ACT_BF16) {
+    q8_values(make_uint2(w.x, w.y), type == ACT_E4M3, v);
+    return;
+  }
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-  for (int j = 0; j < 8; j++) v[j] *= 64.0f;            // q 2^6: the factor is scale 2^24 / 2^6 / 2^9
-  if (put) D.put(tok, grp, i, act_pack(v), scale * 512.0f, s);
+  for (int j = 0; j < 4; j++) {
+    v[2 * j] = __uint_as_float(ws[j] << 16);
+    v[2 * j + 1] = __uint_as_float(ws[j] & 0xFFFF0000u);
+  }
+}
+
+// Eight lanes (i = 0..7) bring one token's group of 64 channels, 8 each, into place; scale: of 8-bit
+// codes, else 1.  All 32 lanes of the warp call it together.
+__device__ __forceinline__ void act_group(float (&v)[8], float scale, int i, int tok, int grp, const ActDst &D, bool put) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; j++) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
+  // largest in [2^(eb-127), 2^(eb-126)) -> [2^15, 2^16); a group with a NaN or an infinity keeps
+  // it (eb = 255 makes the factor infinite), so its outputs are not finite
+  const uint32_t eb = max(m >> 23, 15u);
+  const float up = __uint_as_float((269u - eb) << 23), factor = __uint_as_float(eb << 23);
+  const float s = group_sum(sum8(v) * (1.0f / kActUnit), 8);
+#pragma unroll
+  for (int j = 0; j < 8; j++) v[j] *= up;
+  if (put) D.put(tok, grp, i, act_pack(v), factor * scale, s * scale);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -203,8 +200,6 @@ __device__ __forceinline__ void act_group_q8(uint2 w, bool e4m3, float scale, in
 // takes 16 consecutive bytes of a row and one fold serves both groups.  Wide (N tiles of 8 tokens): 8
 // bytes of a row a lane, a fold per group.  The accumulators of a lane are rows l / 4 and l / 4 + 8,
 // tokens 2 (l & 3), + 1 of a tile (pair: tokens 2 (l & 1), + 1, after adding lanes l and l + 2).
-enum { ACT_BF16 = 0, ACT_INT8 = 1, ACT_E4M3 = 2 };
-
 struct LinearArgs {
   const uint8_t *codes;          // [N, K / 2]
   const uint8_t *scale, *min;    // [N, K / g] bf16
@@ -379,7 +374,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
   const int row_lo = (int)((long long)L.N * part / parts), row_hi = (int)((long long)L.N * (part + 1) / parts);
   // shared memory
   float *lt = reinterpret_cast<float *>(smem + 128);                 // [TOK][32]
-  float *red = lt + TOK * 32;                                        // [16 warps][16 rows][TOK], or [pass rows][TOK]
+  float *red = lt + TOK * 32;                                        // [16 warps][TOK][16 rows]
   const uint32_t ring = smem_at(red + kLinWarps * 16 * TOK) + warp * lin_ring(WIDE);
   uint8_t *ops = reinterpret_cast<uint8_t *>(red + kLinWarps * 16 * TOK) + kLinWarps * lin_ring(WIDE);
   const int pitch = NB * 512 + kActPad, pairs = (nt + 1) / 2;
@@ -453,7 +448,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
     int best = 1 << 30, lg = 0;
 #pragma unroll
     for (int g = 0; g < 4; g++) {
-      const int cost = (((tiles << g) + 15) >> 4 << (4 - g)) + g;
+      const int cost = (((tiles << g) + 15) >> 4 << (4 - g)) + 2 * g;
       if ((1 << g) <= NBmost && cost < best) {
         best = cost;
         lg = g;
@@ -472,115 +467,6 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
 #pragma unroll 1
     for (int u = 1; u < DEPTH; u++) issue();
   };
-  const int pass = L.S > 1 ? kLinPass : row_hi - row_lo;
-  begin(row_lo, min(row_lo + pass, row_hi));
-
-  // ---- the activations of this block's channels: 8 lanes to a token's group, zeros behind the last
-  {
-    const int G = NB * 4, units = nt * G, i = tid & 7;
-    auto load = [&](int u, uint4 &w, float &s) {
-      w = make_uint4(0, 0, 0, 0);
-      s = 0.f;
-      const int tok = u / G, k = (u - tok * G) * 64;
-      if (u < units && k < kc) {
-        const long long at = (long long)(t0 + tok) * L.x_stride + k0 + k + i * 8;
-        if (L.x_type == ACT_BF16) {
-          w = __ldg(reinterpret_cast<const uint4 *>((const uint16_t *)L.x + at));
-        } else {
-          const uint2 v = __ldg(reinterpret_cast<const uint2 *>((const uint8_t *)L.x + at));
-          w.x = v.x;
-          w.y = v.y;
-          s = __ldg(L.x_scale + (long long)(t0 + tok) * (L.K / L.x_group) + (k0 + k) / L.x_group);
-        }
-      }
-    };
-#pragma unroll 1
-    for (int u0 = tid >> 3; u0 - (tid >> 3) < units; u0 += 4 * (kLinThreads / 8)) {
-      uint4 w[4];
-      float s[4];
-#pragma unroll
-      for (int j = 0; j < 4; j++) load(u0 + j * (kLinThreads / 8), w[j], s[j]);
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const int u = u0 + j * (kLinThreads / 8), tok = u / G, g = u - tok * G;
-        if (L.x_type == ACT_BF16)
-          act_group_bf16(w[j], i, tok, g, D, u < units);
-        else
-          act_group_q8(make_uint2(w[j].x, w[j].y), L.x_type == ACT_E4M3, s[j], i, tok, g, D, u < units);
-      }
-    }
-  }
-  // ---- t = A x of this block's channels, K split over the warps: 16 ranks by 8 tokens at a time
-  if (L.A) {
-    const int G = kc / 64;
-#pragma unroll 1
-    for (int u = 0; u < (L.r + 15) / 16 * ((nt + 7) / 8); u++) {
-      const int q = u / ((nt + 7) / 8) * 16, tt = u % ((nt + 7) / 8) * 8;
-      const uint16_t *ra = L.A + (long long)min(q + r, L.r - 1) * L.K + k0 + t * 8;
-      const uint16_t *rb = L.A + (long long)min(q + r + 8, L.r - 1) * L.K + k0 + t * 8;
-      const int tok = min(tt + r, nt - 1);
-      const long long xa = (long long)(t0 + tok) * L.x_stride + k0 + t * 8;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-      for (int g = G * warp / kLinWarps; g < G * (warp + 1) / kLinWarps; g++) {
-        float p[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-          const int k = g * 64 + h * 32;
-          uint4 x;
-          if (L.x_type == ACT_BF16) {
-            x = __ldg(reinterpret_cast<const uint4 *>((const uint16_t *)L.x + xa + k));
-          } else {
-            float v[8];
-            q8_values(__ldg(reinterpret_cast<const uint2 *>((const uint8_t *)L.x + xa + k)), L.x_type == ACT_E4M3, v);
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) w[j] = (__float_as_uint(v[2 * j]) >> 16) | (__float_as_uint(v[2 * j + 1]) & 0xFFFF0000u);
-            x = make_uint4(w[0], w[1], w[2], w[3]);            // codes are exact in bf16
-          }
-          bf16_mul(__ldg(reinterpret_cast<const uint4 *>(ra + k)), __ldg(reinterpret_cast<const uint4 *>(rb + k)), x, p);
-        }
-        // columns 2 t, 2 t + 1 are tokens of their own scales
-        float s0 = 1.f, s1 = 1.f;
-        if (L.x_type != ACT_BF16) {
-          const int gs = (k0 + g * 64) / L.x_group, ng = L.K / L.x_group;
-          s0 = __ldg(L.x_scale + (long long)(t0 + min(tt + 2 * t, nt - 1)) * ng + gs);
-          s1 = __ldg(L.x_scale + (long long)(t0 + min(tt + 2 * t + 1, nt - 1)) * ng + gs);
-        }
-        acc[0] = fmaf(s0, p[0], acc[0]);
-        acc[1] = fmaf(s1, p[1], acc[1]);
-        acc[2] = fmaf(s0, p[2], acc[2]);
-        acc[3] = fmaf(s1, p[3], acc[3]);
-      }
-      float *p = red + warp * 128 + r * 8 + 2 * t;               // TOK >= 4: 16 warps of 64 floats or more
-      if (TOK >= 8) {
-        p[0] = acc[0];
-        p[1] = acc[1];
-        p[64] = acc[2];
-        p[65] = acc[3];
-      } else if (t < 2) {                                        // 4 tokens: columns 0..3
-        p = red + warp * 64 + r * 4 + 2 * t;
-        p[0] = acc[0];
-        p[1] = acc[1];
-        p[32] = acc[2];
-        p[33] = acc[3];
-      }
-      __syncthreads();
-      constexpr int W = TOK >= 8 ? 8 : 4;
-      if (tid < 16 * W) {
-        const int row = q + tid / W, tk = tt + tid % W;
-        if (row < L.r && tk < nt) {
-          float s = 0.f;
-#pragma unroll
-          for (int w = 0; w < kLinWarps; w++) s += red[w * 16 * W + tid];
-          lt[tk * 32 + row] = s;
-        }
-      }
-      __syncthreads();
-    }
-  }
-  __syncthreads();
-
   // ---- the tiles
   const int swz = row_swz(r);
   const uint32_t w_at = r * 128 + (((WIDE ? t >> 1 : t) ^ swz) << 4) + (WIDE ? (t & 1) * 8 : 0);
@@ -596,10 +482,118 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
     X0.sv[q] = smem_at(D.sv) + pair * 16 + (WIDE ? 0 : (t >> 1) * X0.svs);
   }
   uint32_t st = slots_end, sl = slots_end - kLinSlot;
+  const int pass = L.S > 1 ? kLinPass : row_hi - row_lo;
+#pragma unroll 1
   for (int lo = row_lo; lo < row_hi; lo += pass) {
     const int hi = min(lo + pass, row_hi);
-    if (lo != row_lo) begin(lo, hi);
-    // begin() starts where the ring stands
+    begin(lo, hi);                        // the first weights are on their way while the activations come
+    if (lo == row_lo) {
+      // ---- the activations of this block's channels: 8 lanes to a token's group, zeros behind the last
+      {
+        const int G = NB * 4, units = nt * G, i = tid & 7;
+        auto load = [&](int u, uint4 &w, float &s) {
+          w = make_uint4(0, 0, 0, 0);
+          s = 1.f;
+          const int tok = u / G, k = (u - tok * G) * 64;
+          if (u < units && k < kc) {
+            const long long at = (long long)(t0 + tok) * L.x_stride + k0 + k + i * 8;
+            if (L.x_type == ACT_BF16) {
+              w = __ldg(reinterpret_cast<const uint4 *>((const uint16_t *)L.x + at));
+            } else {
+              const uint2 v = __ldg(reinterpret_cast<const uint2 *>((const uint8_t *)L.x + at));
+              w.x = v.x;
+              w.y = v.y;
+              s = __ldg(L.x_scale + (long long)(t0 + tok) * (L.K / L.x_group) + (k0 + k) / L.x_group);
+            }
+          }
+        };
+#pragma unroll 1
+        for (int u0 = tid >> 3; u0 - (tid >> 3) < units; u0 += 4 * (kLinThreads / 8)) {
+          uint4 w[4];
+          float s[4];
+#pragma unroll
+          for (int j = 0; j < 4; j++) load(u0 + j * (kLinThreads / 8), w[j], s[j]);
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const int u = u0 + j * (kLinThreads / 8), tok = u / G, g = u - tok * G;
+            if (u - (tid >> 3) >= units) break;         // (the same for the whole block)
+            float v[8];
+            act_values(w[j], L.x_type, v);
+            act_group(v, s[j], i, tok, g, D, u < units);
+          }
+        }
+      }
+      // ---- t = A x of this block's channels, K split over the warps: 16 ranks by 8 tokens at a time
+      if (L.A) {
+        const int G = kc / 64;
+#pragma unroll 1
+        for (int u = 0; u < (L.r + 15) / 16 * ((nt + 7) / 8); u++) {
+          const int q = u / ((nt + 7) / 8) * 16, tt = u % ((nt + 7) / 8) * 8;
+          const uint16_t *ra = L.A + (long long)min(q + r, L.r - 1) * L.K + k0 + t * 8;
+          const uint16_t *rb = L.A + (long long)min(q + r + 8, L.r - 1) * L.K + k0 + t * 8;
+          const int tok = min(tt + r, nt - 1);
+          const long long xa = (long long)(t0 + tok) * L.x_stride + k0 + t * 8;
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+          for (int g = G * warp / kLinWarps; g < G * (warp + 1) / kLinWarps; g++) {
+            float p[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+              const int k = g * 64 + h * 32;
+              uint4 x;
+              if (L.x_type == ACT_BF16) {
+                x = __ldg(reinterpret_cast<const uint4 *>((const uint16_t *)L.x + xa + k));
+              } else {
+                float v[8];
+                q8_values(__ldg(reinterpret_cast<const uint2 *>((const uint8_t *)L.x + xa + k)), L.x_type == ACT_E4M3, v);
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; j++) w[j] = (__float_as_uint(v[2 * j]) >> 16) | (__float_as_uint(v[2 * j + 1]) & 0xFFFF0000u);
+                x = make_uint4(w[0], w[1], w[2], w[3]);            // codes are exact in bf16
+              }
+              bf16_mul(__ldg(reinterpret_cast<const uint4 *>(ra + k)), __ldg(reinterpret_cast<const uint4 *>(rb + k)), x, p);
+            }
+            // columns 2 t, 2 t + 1 are tokens of their own scales
+            float s0 = 1.f, s1 = 1.f;
+            if (L.x_type != ACT_BF16) {
+              const int gs = (k0 + g * 64) / L.x_group, ng = L.K / L.x_group;
+              s0 = __ldg(L.x_scale + (long long)(t0 + min(tt + 2 * t, nt - 1)) * ng + gs);
+              s1 = __ldg(L.x_scale + (long long)(t0 + min(tt + 2 * t + 1, nt - 1)) * ng + gs);
+            }
+            acc[0] = fmaf(s0, p[0], acc[0]);
+            acc[1] = fmaf(s1, p[1], acc[1]);
+            acc[2] = fmaf(s0, p[2], acc[2]);
+            acc[3] = fmaf(s1, p[3], acc[3]);
+          }
+          float *p = red + warp * 128 + r * 8 + 2 * t;               // TOK >= 4: 16 warps of 64 floats or more
+          if (TOK >= 8) {
+            p[0] = acc[0];
+            p[1] = acc[1];
+            p[64] = acc[2];
+            p[65] = acc[3];
+          } else if (t < 2) {                                        // 4 tokens: columns 0..3
+            p = red + warp * 64 + r * 4 + 2 * t;
+            p[0] = acc[0];
+            p[1] = acc[1];
+            p[32] = acc[2];
+            p[33] = acc[3];
+          }
+          __syncthreads();
+          constexpr int W = TOK >= 8 ? 8 : 4;
+          if (tid < 16 * W) {
+            const int row = q + tid / W, tk = tt + tid % W;
+            if (row < L.r && tk < nt) {
+              float s = 0.f;
+#pragma unroll
+              for (int w = 0; w < kLinWarps; w++) s += red[w * 16 * W + tid];
+              lt[tk * 32 + row] = s;
+            }
+          }
+          __syncthreads();
+        }
+      }
+      __syncthreads();
+    }
 #pragma unroll 1
     for (int j = 0; j < jobs; j++) {
       const int row = lo + (tile0 + j * step) * 16;
@@ -640,6 +634,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
         st = st + kLinStage == end ? slots_end : st + kLinStage;
       }
       // pair: lanes l and l + 2 hold the same two tokens and take one each; wide: both tokens
+      float *mine_at = red + warp * 16 * TOK;
 #pragma unroll
       for (int q = 0; q < N; q++) {
         if (!WIDE)
@@ -648,51 +643,40 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
 #pragma unroll
         for (int h = 0; h < (WIDE ? 2 : 1); h++) {
           const int odd = WIDE ? h : t >> 1, tok = WIDE ? 8 * q + 2 * t + h : 4 * q + 2 * (t & 1) + odd;
-          if (tok >= nt) continue;
-#pragma unroll
-          for (int e = 0; e < 2; e++) {
-            const float v = (e ? (odd ? acc[q][3] : acc[q][2]) : (odd ? acc[q][1] : acc[q][0])) * kActUnit;
-            const int rr = r + 8 * e;
-            if (wk > 1)
-              red[(warp * 16 + rr) * TOK + tok] = v;
-            else if (L.S > 1)
-              red[(row - lo + rr) * TOK + tok] = L.A && row + rr < hi ? v + lin_lora(L, row + rr, lt + tok * 32) : v;
-            else if (row + rr < hi)
-              lin_store(L, t0 + tok, row + rr, L.A ? v + lin_lora(L, row + rr, lt + tok * 32) : v);
-          }
+          mine_at[tok * 16 + r] = odd ? acc[q][1] : acc[q][0];
+          mine_at[tok * 16 + r + 8] = odd ? acc[q][3] : acc[q][2];
         }
       }
-      if (wk > 1) {
-        bar_team(wk, team);
-        float *p = red + team * wk * 16 * TOK;
+      if (wk > 1) bar_team(wk, team); else __syncwarp();
+      float *p = red + team * wk * 16 * TOK;
 #pragma unroll 1
-        for (int u = sub * 32 + lane; u < 16 * TOK; u += wk * 32) {
-          const int rr = u / TOK, tok = u % TOK;
-          if (tok >= nt || row + rr >= hi) continue;
-          float v = p[u];
+      for (int u = sub * 32 + lane; u < 16 * nt; u += wk * 32) {
+        const int tok = u >> 4, n = row + (u & 15);
+        float v = p[u];
 #pragma unroll 1
-          for (int w = 1; w < wk; w++) v += p[w * 16 * TOK + u];
-          if (L.A) v += lin_lora(L, row + rr, lt + tok * 32);
-          if (L.S > 1)
-            p[u] = v;                     // the team's first warp's sums, at the tile's place (below)
-          else
-            lin_store(L, t0 + tok, row + rr, v);
-        }
-        bar_team(wk, team);
+        for (int w = 1; w < wk; w++) v += p[w * 16 * TOK + u];
+        v *= kActUnit;
+        if (n >= hi) continue;
+        if (L.A) v += lin_lora(L, n, lt + tok * 32);
+        if (L.S > 1)
+          p[u] = v;                       // joined below
+        else
+          lin_store(L, t0 + tok, n, v);
       }
+      if (wk > 1) bar_team(wk, team); else __syncwarp();
     }
     if (L.S > 1) {
-      // rows of a tile: with a team of wk warps a pass has at most 16 / wk tiles, tile q at wk 16 q
-      // rows; else at 16 q rows
+      // A pass has at most 8 tiles, so each warp or team has had one: tile q is where team q left it.
       cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
       cluster.sync();
-      for (int u = rank * kLinThreads + tid; u < (hi - lo) * TOK; u += L.S * kLinThreads) {
-        const int rr = u / TOK, tok = u % TOK;
-        if (tok >= nt) continue;
-        const int at = ((rr >> 4) * wk * 16 + (rr & 15)) * TOK + tok;
+#pragma unroll 1
+      for (int u = rank * kLinThreads + tid; u < tiles * 16 * nt; u += L.S * kLinThreads) {
+        const int q = u / (16 * nt), at = u - q * 16 * nt, n = lo + q * 16 + (at & 15);
+        if (n >= hi) continue;
         float v = 0.f;
-        for (int w = 0; w < L.S; w++) v += cluster.map_shared_rank(red, w)[at];
-        lin_store(L, t0 + tok, lo + rr, v);
+#pragma unroll 1
+        for (int w = 0; w < L.S; w++) v += cluster.map_shared_rank(red, w)[q * wk * 16 * TOK + at];
+        lin_store(L, t0 + (at >> 4), n, v);
       }
       cluster.sync();
     }
