@@ -2127,6 +2127,9 @@ static int lin_clusters(const void *kernel, int variant, int dev, int nsm, int S
   return E0_OK;
 }
 
+// Channels times tokens that a block brings to fp16 by itself before K is split over a cluster.
+static constexpr long long kLinActs = 32768;
+
 template <bool WIDE, int N, bool G128>
 static int launch_linear(LinearArgs &L, cudaStream_t s) {
   constexpr int TOK = N * (WIDE ? 8 : 4);
@@ -2135,11 +2138,14 @@ static int launch_linear(LinearArgs &L, cudaStream_t s) {
   CK(cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev));
   CK(cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev));
   const size_t room = (size_t)most - lin_fixed(WIDE, N);
-  // as few blocks to a cluster as the activations need; where even 8 do not hold them, fewer tokens
-  // a block
+  // Blocks of a cluster: a block brings at most kLinActs channels of all its tokens to fp16, and its
+  // activations leave room for the sums of 16 rows or more; where even 8 blocks do not hold them,
+  // fewer tokens a block.
+  const auto space = [&](int S, int tok, int kc) { return lin_acts(tok, kc) + (S > 1 ? (size_t)16 * tok * 4 : 0); };
   L.tok = std::min(TOK, L.T);
-  for (L.S = 1, L.kc = L.K;;) {
-    if (lin_acts(L.tok, L.kc) <= room) break;
+  for (L.S = 1;;) {
+    L.kc = L.S == 1 ? L.K : ((L.K + L.S - 1) / L.S + 255) / 256 * 256;
+    if (space(L.S, L.tok, L.kc) <= room && (L.S == 8 || (long long)L.tok * L.kc <= kLinActs)) break;
     if (L.S < 8) {
       L.S *= 2;
     } else if (L.tok > 1) {
@@ -2148,18 +2154,24 @@ static int launch_linear(LinearArgs &L, cudaStream_t s) {
     } else {
       return fail(E0_ERR_INVALID_ARG, "int4_linear: k = %d is too long", L.K);
     }
-    L.kc = L.S == 1 ? L.K : ((L.K + L.S - 1) / L.S + 1023) / 1024 * 1024;
   }
-  if (L.S > 1) L.S = (L.K + L.kc - 1) / L.kc > 4 ? 8 : (L.K + L.kc - 1) / L.kc > 2 ? 4 : 2;
+  if (L.S > 1)
+    while (L.cs > 2 && L.kc % (128 * L.cs)) L.cs /= 2;   // every block's scales begin with a slot
   const int tiles = (L.T + L.tok - 1) / L.tok;
   if (tiles > 65535) return fail(E0_ERR_INVALID_ARG, "int4_linear: T = %d is too large for k = %d", L.T, L.K);
-  const size_t smem = lin_fixed(WIDE, N) + lin_acts(L.tok, L.kc);
   const void *kernel = (const void *)k_int4_linear<WIDE, N, G128>;
   CK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
   int clusters = 0;
   if (int rc = lin_clusters(kernel, (WIDE ? 8 : 0) + N + (G128 ? 4 : 0) - 1, dev, nsm, L.S, (size_t)most, &clusters)) return rc;
+  const int parts = std::min(clusters, L.N);
+  size_t smem = lin_fixed(WIDE, N) + lin_acts(L.tok, L.kc);
+  if (L.S > 1) {
+    const int most_rows = (int)(((size_t)most - smem) / ((size_t)L.tok * 4)) / 16 * 16;
+    L.pass = std::min(most_rows, ((L.N + parts - 1) / parts + 15) / 16 * 16);
+    smem += (size_t)L.pass * L.tok * 4;
+  }
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(std::min(clusters, L.N) * L.S, tiles);
+  cfg.gridDim = dim3(parts * L.S, tiles);
   cfg.blockDim = dim3(kLinThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -2210,7 +2222,8 @@ extern "C" int e0_int4_linear(const e0_int4_mat *w, const void *x, int x_format,
   L.codes = (const uint8_t *)w->codes; L.scale = (const uint8_t *)w->scale; L.min = (const uint8_t *)w->min;
   L.N = w->n; L.K = w->k;
   L.A = (const uint16_t *)w->lora_A; L.B = (const uint16_t *)w->lora_B; L.r = w->lora_rank; L.c = w->lora_scale;
-  L.x = x; L.x_type = x_format; L.x_stride = x_stride; L.x_scale = x_scale; L.x_group = x_group ? x_group : w->k;
+  L.x = x; L.x_type = x_format; L.x_stride = x_stride; L.x_scale = x_scale;
+  L.x_shift = x_group == 64 ? 6 : x_group == 128 ? 7 : 30; L.x_groups = x_group ? w->k / x_group : 1;
   L.T = T; L.y = y; L.y_f32 = y_f32; L.y_stride = y_stride;
   cudaStream_t s = (cudaStream_t)stream;
   L.b16 = w->lora_rank % 8 == 0 && !misaligned(w->lora_B, 16);

@@ -111,12 +111,6 @@ __device__ __forceinline__ uint32_t half2_of(float a, float b) {
   return r;
 }
 
-__device__ __forceinline__ uint4 act_pack(const float *v) {
-  constexpr float o = 0.0625f;
-  return make_uint4(half2_of(v[0], v[4]), half2_of(v[1] * o, v[5] * o), half2_of(v[2], v[6]),
-                    half2_of(v[3] * o, v[7] * o));
-}
-
 __device__ __forceinline__ float sum8(const float *v) {
   return ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
 }
@@ -153,37 +147,67 @@ __device__ __forceinline__ void q8_values(uint2 w, bool e4m3, float (&v)[8]) {
   }
 }
 
-// The values of 8 channels, which bf16 holds exactly: of bf16 (w) or of 8-bit codes (its first half).
-__device__ __forceinline__ void act_values(uint4 w, int type, float (&v)[8]) {
-  if (type != ACT_BF16) {
-    q8_values(make_uint2(w.x, w.y), type == ACT_E4M3, v);
-    return;
-  }
+// Eight lanes (i = 0..7) bring one token's group of 64 channels, 8 each (16 bytes of bf16, or 8 of
+// codes with their scale), into place.  All 32 lanes of the warp call these together.
+__device__ __forceinline__ void act_group_bf16(uint4 w, int i, int tok, int grp, const ActDst &D, bool put) {
   const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  float v[8], m = 0.f;
 #pragma unroll
   for (int j = 0; j < 4; j++) {
     v[2 * j] = __uint_as_float(ws[j] << 16);
     v[2 * j + 1] = __uint_as_float(ws[j] & 0xFFFF0000u);
+    m = fmaxf(m, fmaxf(fabsf(v[2 * j]), fabsf(v[2 * j + 1])));
   }
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+  // largest in [2^(eb-127), 2^(eb-126)) -> [2^15, 2^16); an infinity (eb = 255) makes the factor
+  // infinite and a NaN the sum, so the token's outputs are not finite
+  const uint32_t eb = max(__float_as_uint(m) >> 23, 15u);
+  const float up = __uint_as_float((269u - eb) << 23), up16 = up * 0.0625f, factor = __uint_as_float(eb << 23);
+  const float s = group_sum(sum8(v) * (1.0f / kActUnit), 8);
+  if (put)
+    D.put(tok, grp, i, make_uint4(half2_of(v[0] * up, v[4] * up), half2_of(v[1] * up16, v[5] * up16),
+                                  half2_of(v[2] * up, v[6] * up), half2_of(v[3] * up16, v[7] * up16)), factor, s);
 }
 
-// Eight lanes (i = 0..7) bring one token's group of 64 channels, 8 each, into place; scale: of 8-bit
-// codes, else 1.  All 32 lanes of the warp call it together.
-__device__ __forceinline__ void act_group(float (&v)[8], float scale, int i, int tok, int grp, const ActDst &D, bool put) {
-  uint32_t m = 0;
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// Codes times 32 (odd channels times 2): exact in fp16; the factor is scale 2^24 / 2^5 / 2^9.
+__device__ __forceinline__ void act_group_int8(uint2 w, float scale, int i, int tok, int grp, const ActDst &D, bool put) {
+  constexpr uint32_t X32 = 0x50005000u, X2 = 0x40004000u;             // 32, 2
+  constexpr uint32_t O32 = 0xF880F880u, O2 = 0xE880E880u;             // -1152 * 32, -1152 * 2
+  // a byte b + 128 under 0x64 is the fp16 number 1024 + 128 + b
+  const uint32_t x = w.x ^ 0x80808080u, y = w.y ^ 0x80808080u;
+  const uint32_t u = __byte_perm(x, y, 0x5140), v = __byte_perm(x, y, 0x7362);   // channels 0 4 1 5, 2 6 3 7
+  const uint4 p = make_uint4(hfma2(__byte_perm(u, 0x64646464u, 0x4140), X32, O32), hfma2(__byte_perm(u, 0x64646464u, 0x4342), X2, O2),
+                             hfma2(__byte_perm(v, 0x64646464u, 0x4140), X32, O32), hfma2(__byte_perm(v, 0x64646464u, 0x4342), X2, O2));
+  int n = __dp4a((int)w.x, 0x01010101, __dp4a((int)w.y, 0x01010101, 0));
+  n += __shfl_xor_sync(0xffffffffu, n, 1);
+  n += __shfl_xor_sync(0xffffffffu, n, 2);
+  n += __shfl_xor_sync(0xffffffffu, n, 4);
+  if (put) D.put(tok, grp, i, p, scale * 1024.0f, (float)n * (scale * (1.0f / kActUnit)));
+}
+
+__device__ __forceinline__ void act_group_e4m3(uint2 w, float scale, int i, int tok, int grp, const ActDst &D, bool put) {
+  constexpr uint32_t X32 = 0x50005000u, X2 = 0x40004000u;
+  uint32_t h[4];
+  float v[8];
 #pragma unroll
-  for (int j = 0; j < 8; j++) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
-  // largest in [2^(eb-127), 2^(eb-126)) -> [2^15, 2^16); a group with a NaN or an infinity keeps
-  // it (eb = 255 makes the factor infinite), so its outputs are not finite
-  const uint32_t eb = max(m >> 23, 15u);
-  const float up = __uint_as_float((269u - eb) << 23), factor = __uint_as_float(eb << 23);
-  const float s = group_sum(sum8(v) * (1.0f / kActUnit), 8);
-#pragma unroll
-  for (int j = 0; j < 8; j++) v[j] *= up;
-  if (put) D.put(tok, grp, i, act_pack(v), factor * scale, s * scale);
+  for (int j = 0; j < 4; j++) {
+    const uint32_t two = ((j < 2 ? w.x : w.y) >> (16 * (j & 1))) & 0xFFFFu;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h[j]) : "h"((uint16_t)two));
+    asm("{.reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b;}" : "=f"(v[2 * j]), "=f"(v[2 * j + 1]) : "r"(h[j]));
+  }
+  const uint32_t none = 0x80008000u;                                   // -0: x y + -0 = x y
+  const uint4 p = make_uint4(hfma2(__byte_perm(h[0], h[2], 0x5410), X32, none), hfma2(__byte_perm(h[0], h[2], 0x7632), X2, none),
+                             hfma2(__byte_perm(h[1], h[3], 0x5410), X32, none), hfma2(__byte_perm(h[1], h[3], 0x7632), X2, none));
+  const float s = group_sum(sum8(v), 8);
+  if (put) D.put(tok, grp, i, p, scale * 1024.0f, s * (scale * (1.0f / kActUnit)));
 }
 
 // ---------------------------------------------------------------------------------------
@@ -192,8 +216,9 @@ __device__ __forceinline__ void act_group(float (&v)[8], float scale, int i, int
 // A block (one an SM, 16 warps) holds the activations of its tokens in shared memory and takes a
 // contiguous share of the rows in tiles of 16; each warp (or a team of wk warps that splits K, where
 // there are few tiles) streams its tiles through a ring of its own by cp.async, a stage of 256
-// channels.  Where the activations do not fit (many tokens times a long K), the blocks of a cluster
-// split K, and each adds up a part of the rows over the cluster's shared memory.
+// channels.  Where the activations are many (tokens times K), so that every block would spend more on
+// bringing them to fp16 than on its weights, or they do not fit, the blocks of a cluster split K, and
+// each adds up a part of the rows over the cluster's shared memory.
 //
 // Two forms.  Pair (up to 8 tokens, N tiles of 4): the 8 columns of a matrix instruction are 4 tokens
 // restricted to one group of 64 and the same 4 restricted to the next (zeros elsewhere), so a lane
@@ -211,23 +236,23 @@ struct LinearArgs {
   int x_type;
   long long x_stride;            // elements
   const float *x_scale;          // [T, K / x_group], or nullptr
-  int x_group;                   // channels to a scale
+  int x_shift, x_groups;         // scale k >> x_shift of x_groups belongs to channel k
   int T;
   void *y;                       // [T, N]
   int y_f32;
   long long y_stride;
-  int S, kc;                     // blocks of a cluster, channels a block (a multiple of 1024 where S > 1)
+  int S, kc;                     // blocks of a cluster, channels a block (a multiple of 256 and 128 cs where S > 1)
+  int pass;                      // rows between two exchanges of a cluster (a multiple of 16)
   int cs;                        // 128-channel steps to a slot of scales: 8, 4, 2; 0: 2, fetched one by one
   int tok;                       // tokens of a block
 };
 
 constexpr int kLinThreads = 512, kLinWarps = kLinThreads / 32;
 constexpr int kLinStage = 16 * 128, kLinSlot = 16 * 32;
-constexpr int kLinPass = 128;    // rows between two exchanges of a cluster
 constexpr int lin_depth(bool wide) { return wide ? 2 : 3; }
 constexpr int lin_ring(bool wide) { return lin_depth(wide) * (kLinStage + kLinSlot); }
 __host__ __device__ inline int lin_blocks(int kc) { return (kc + 255) / 256; }
-// shared memory: zeros | t | partial sums | rings | activations of nt tokens
+// shared memory: zeros | t | partial sums | rings | activations of nt tokens | sums of a pass (S > 1)
 __host__ __device__ inline size_t lin_fixed(bool wide, int N) {
   return 128 + 32 * (size_t)(wide ? 8 : 4) * N * 4 + (size_t)kLinWarps * 16 * (wide ? 8 : 4) * N * 4 + (size_t)kLinWarps * lin_ring(wide);
 }
@@ -370,7 +395,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
   const int rank = blockIdx.x % L.S, part = blockIdx.x / L.S, parts = gridDim.x / L.S;
   const int t0 = blockIdx.y * L.tok, nt = min(L.tok, L.T - t0);
   // (the last blocks of a cluster may have fewer channels, or none)
-  const int k0 = min(rank * L.kc, L.K), kc = min(L.kc, L.K - k0), NB = lin_blocks(kc), NBmost = lin_blocks(L.kc);
+  const int k0 = min(rank * L.kc, L.K), kc = min(L.kc, L.K - k0), NB = lin_blocks(kc), NB1 = max(NB, 1),
+            NBmost = lin_blocks(L.kc);
   const int row_lo = (int)((long long)L.N * part / parts), row_hi = (int)((long long)L.N * (part + 1) / parts);
   // shared memory
   float *lt = reinterpret_cast<float *>(smem + 128);                 // [TOK][32]
@@ -379,6 +405,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
   uint8_t *ops = reinterpret_cast<uint8_t *>(red + kLinWarps * 16 * TOK) + kLinWarps * lin_ring(WIDE);
   const int pitch = NB * 512 + kActPad, pairs = (nt + 1) / 2;
   const ActDst D{ops, reinterpret_cast<float *>(ops + (size_t)nt * pitch), pitch, pairs};
+  float *sums = reinterpret_cast<float *>(ops + lin_acts(min(L.tok, L.T), L.kc));   // S > 1: [pass / 16][nt][16 rows]
   const uint32_t zero = smem_at(smem);
   if (tid < 32) reinterpret_cast<uint32_t *>(smem)[tid] = 0;
 
@@ -482,44 +509,55 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
     X0.sv[q] = smem_at(D.sv) + pair * 16 + (WIDE ? 0 : (t >> 1) * X0.svs);
   }
   uint32_t st = slots_end, sl = slots_end - kLinSlot;
-  const int pass = L.S > 1 ? kLinPass : row_hi - row_lo;
+  const int pass = L.S > 1 ? L.pass : row_hi - row_lo;
 #pragma unroll 1
   for (int lo = row_lo; lo < row_hi; lo += pass) {
     const int hi = min(lo + pass, row_hi);
     begin(lo, hi);                        // the first weights are on their way while the activations come
     if (lo == row_lo) {
-      // ---- the activations of this block's channels: 8 lanes to a token's group, zeros behind the last
+      // ---- the activations of this block's channels, zeros behind the last: a warp takes 256 of a
+      // token, 8 lanes to a group of 64; four of them are under way at once
       {
-        const int G = NB * 4, units = nt * G, i = tid & 7;
-        auto load = [&](int u, uint4 &w, float &s) {
-          w = make_uint4(0, 0, 0, 0);
-          s = 1.f;
-          const int tok = u / G, k = (u - tok * G) * 64;
-          if (u < units && k < kc) {
-            const long long at = (long long)(t0 + tok) * L.x_stride + k0 + k + i * 8;
-            if (L.x_type == ACT_BF16) {
-              w = __ldg(reinterpret_cast<const uint4 *>((const uint16_t *)L.x + at));
-            } else {
-              const uint2 v = __ldg(reinterpret_cast<const uint2 *>((const uint8_t *)L.x + at));
-              w.x = v.x;
-              w.y = v.y;
-              s = __ldg(L.x_scale + (long long)(t0 + tok) * (L.K / L.x_group) + (k0 + k) / L.x_group);
-            }
-          }
-        };
+        const int i = lane & 7;
+        int ct = warp / NB1, cb = warp - ct * NB1;
 #pragma unroll 1
-        for (int u0 = tid >> 3; u0 - (tid >> 3) < units; u0 += 4 * (kLinThreads / 8)) {
+        while (ct < nt && NB > 0) {
           uint4 w[4];
           float s[4];
-#pragma unroll
-          for (int j = 0; j < 4; j++) load(u0 + j * (kLinThreads / 8), w[j], s[j]);
+          int tk[4], gr[4];
 #pragma unroll
           for (int j = 0; j < 4; j++) {
-            const int u = u0 + j * (kLinThreads / 8), tok = u / G, g = u - tok * G;
-            if (u - (tid >> 3) >= units) break;         // (the same for the whole block)
-            float v[8];
-            act_values(w[j], L.x_type, v);
-            act_group(v, s[j], i, tok, g, D, u < units);
+            const int k = cb * 256 + lane * 8;
+            w[j] = make_uint4(0, 0, 0, 0);
+            s[j] = 1.f;
+            tk[j] = ct;
+            gr[j] = cb * 4 + (lane >> 3);
+            if (ct < nt) {
+              if (k < kc) {
+                const long long at = (long long)(t0 + ct) * L.x_stride + k0 + k;
+                if (L.x_type == ACT_BF16) {
+                  w[j] = __ldg(reinterpret_cast<const uint4 *>((const uint16_t *)L.x + at));
+                } else {
+                  const uint2 v = __ldg(reinterpret_cast<const uint2 *>((const uint8_t *)L.x + at));
+                  w[j].x = v.x;
+                  w[j].y = v.y;
+                  s[j] = __ldg(L.x_scale + (long long)(t0 + ct) * L.x_groups + ((k0 + k) >> L.x_shift));
+                }
+              }
+              cb += kLinWarps;
+#pragma unroll 1
+              while (cb >= NB) {
+                cb -= NB;
+                ct++;
+              }
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            if (tk[j] >= nt) break;                     // (the same for the whole warp)
+            if (L.x_type == ACT_BF16) act_group_bf16(w[j], i, tk[j], gr[j], D, true);
+            else if (L.x_type == ACT_INT8) act_group_int8(make_uint2(w[j].x, w[j].y), s[j], i, tk[j], gr[j], D, true);
+            else act_group_e4m3(make_uint2(w[j].x, w[j].y), s[j], i, tk[j], gr[j], D, true);
           }
         }
       }
@@ -556,7 +594,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
             // columns 2 t, 2 t + 1 are tokens of their own scales
             float s0 = 1.f, s1 = 1.f;
             if (L.x_type != ACT_BF16) {
-              const int gs = (k0 + g * 64) / L.x_group, ng = L.K / L.x_group;
+              const int gs = (k0 + g * 64) >> L.x_shift, ng = L.x_groups;
               s0 = __ldg(L.x_scale + (long long)(t0 + min(tt + 2 * t, nt - 1)) * ng + gs);
               s1 = __ldg(L.x_scale + (long long)(t0 + min(tt + 2 * t + 1, nt - 1)) * ng + gs);
             }
@@ -659,14 +697,13 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
         if (n >= hi) continue;
         if (L.A) v += lin_lora(L, n, lt + tok * 32);
         if (L.S > 1)
-          p[u] = v;                       // joined below
+          sums[(tile0 + j * step) * 16 * nt + u] = v;       // joined below
         else
           lin_store(L, t0 + tok, n, v);
       }
       if (wk > 1) bar_team(wk, team); else __syncwarp();
     }
     if (L.S > 1) {
-      // A pass has at most 8 tiles, so each warp or team has had one: tile q is where team q left it.
       cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
       cluster.sync();
 #pragma unroll 1
@@ -674,8 +711,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
         const int q = u / (16 * nt), at = u - q * 16 * nt, n = lo + q * 16 + (at & 15);
         if (n >= hi) continue;
         float v = 0.f;
-#pragma unroll 1
-        for (int w = 0; w < L.S; w++) v += cluster.map_shared_rank(red, w)[q * wk * 16 * TOK + at];
+#pragma unroll 2
+        for (int w = 0; w < L.S; w++) v += cluster.map_shared_rank(sums, w)[u];
         lin_store(L, t0 + (at >> 4), n, v);
       }
       cluster.sync();
