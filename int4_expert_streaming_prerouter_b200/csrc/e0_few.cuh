@@ -313,7 +313,7 @@ struct FewTok {
   }
 };
 __device__ __forceinline__ void few_phase1(const FewArgs &A, FewPlan &P, uint8_t *area, float *red) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, d = A.d;
+  const int tid = threadIdx.x, lane = tid & 31, warp = warp_id(), d = A.d;
   const FewTok K(A);
   const int pitch = d * 2 + kFewPad, vbytes = d / 64 * 4;
   uint8_t *hs = area + 8 * (pitch + vbytes);
@@ -505,7 +505,7 @@ __device__ __forceinline__ void few_route_share(const FewArgs &A) {
 constexpr int kFewCost4 = 4, kFewCost8 = 6, kFewCostMore = 11;
 
 __device__ __forceinline__ void few_plan(const FewArgs &A, FewPlan &P) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = warp_id();
   const int k = A.k, T = A.T, E = A.E;
   static_assert(kFewMaxT * kMaxK <= kFewThreads && kMaxE < kFewThreads, "an assignment, an expert a thread");
   if (tid < kMaxE) P.tok[tid] = 0;
@@ -693,7 +693,7 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
                                            uint32_t ring, float *out) {
   if (C.left <= 0) return;
   constexpr int TOK = N * (WIDE ? 8 : 4), STAGE = GU ? kFewStage : few_dn_stage(TOK);
-  const int lane = threadIdx.x & 31, t = lane & 3, r = lane >> 2, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, t = lane & 3, r = lane >> 2, warp = warp_id();
   const int K = GU ? A.d : A.I, stages = GU ? kFewDepth : depth;
   const uint32_t slots = ring, slots_end = slots + stages * kFewSlot;     // of scales, then the stages
   const uint32_t stages_at = slots_end, end = stages_at + stages * STAGE;
@@ -885,7 +885,7 @@ __device__ __forceinline__ void few_bound(const FewPlan &P, int per, int b, int 
 }
 
 __device__ __forceinline__ void few_phase2(const FewArgs &A, const FewPlan &P, uint8_t *area, uint32_t zero, uint32_t ring, float *red) {
-  const int per = A.I / 8, NB = A.d / 256, warp = threadIdx.x >> 5;
+  const int per = A.I / 8, NB = A.d / 256, warp = warp_id();
   int sl, fl, sh, fh;
   few_bound(P, per, blockIdx.x, sl, fl);
   few_bound(P, per, blockIdx.x + 1, sh, fh);
@@ -942,7 +942,7 @@ __device__ __forceinline__ void few_phase2(const FewArgs &A, const FewPlan &P, u
 // ---------------------------------------------------------------------------------------
 // t_d = A_d a_s of every token: 16 rows by 8 tokens, K split over the warps that are left
 __device__ __forceinline__ int few_td(const FewArgs &A, float *td) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k1 = A.k + 1;
+  const int lane = threadIdx.x & 31, warp = warp_id(), k1 = A.k + 1;
   const int rt = (A.r + 15) / 16, ntt = (A.T + 7) / 8, nb = A.I / 32;
   const int split = min(nb, kFewWarps / (rt * ntt)), u = warp;
   if (u < rt * ntt * split) {
@@ -966,7 +966,7 @@ __device__ __forceinline__ int few_td(const FewArgs &A, float *td) {
 
 // area: t_d, the results, the sums of the activations, the rings
 __device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, uint8_t *area, uint32_t zero) {
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = warp_id();
   const int lo = (int)((long long)A.d * blockIdx.x / gridDim.x), hi = (int)((long long)A.d * (blockIdx.x + 1) / gridDim.x);
   if (lo >= hi) return;
   const int G = A.I / 64, NB = A.I / 128, k1 = A.k + 1, nplace = P.nplace;

@@ -67,6 +67,10 @@ __device__ __forceinline__ void bar_team(int wk, int team) {
   asm volatile("bar.sync %0, %1;" ::"r"(16 / wk - 1 + team), "r"(wk * 32) : "memory");
 }
 
+// The warp's number, as a value that the compiler knows to be the same in every lane: what follows from
+// it (tiles, addresses of rows, loop counts) then stays on the uniform units.
+__device__ __forceinline__ int warp_id() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+
 // chunk c (of 16 bytes) of row r of 128 bytes lies at chunk c ^ row_swz(r): the lanes of a load, whether 16 or 8
 // bytes each, fall into distinct banks
 __device__ __forceinline__ int row_swz(int r) { return ((r & 1) << 2) ^ (r & 2); }
@@ -391,7 +395,7 @@ template <bool WIDE, int N, bool G128>
 __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_constant__ LinearArgs L) {
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int TOK = N * (WIDE ? 8 : 4), DEPTH = lin_depth(WIDE);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, lane = tid & 31, warp = warp_id(), r = lane >> 2, t = lane & 3;
   const int rank = blockIdx.x % L.S, part = blockIdx.x / L.S, parts = gridDim.x / L.S;
   const int t0 = blockIdx.y * L.tok, nt = min(L.tok, L.T - t0);
   // (the last blocks of a cluster may have fewer channels, or none)
