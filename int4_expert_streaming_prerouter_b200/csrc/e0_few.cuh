@@ -502,7 +502,7 @@ __device__ __forceinline__ void few_route_share(const FewArgs &A) {
 
 // Relative cost of a tile in phase 2 (measured; the weights bound the first): segments of experts
 // of at most 4 tokens, of at most 8, of more.
-constexpr int kFewCost4 = 4, kFewCost8 = 6, kFewCostMore = 11;
+constexpr int kFewCost4 = 4, kFewCost8 = 8, kFewCostMore = 14;
 
 __device__ __forceinline__ void few_plan(const FewArgs &A, FewPlan &P) {
   const int tid = threadIdx.x, lane = tid & 31, warp = warp_id();
