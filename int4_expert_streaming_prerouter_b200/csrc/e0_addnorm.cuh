@@ -37,17 +37,24 @@ struct AddNormArgs {
   int groups;
 };
 
-// bf16(a + b) of the exact sum.  Rounding the fp32 sum differs from it only where that sum is a
-// border between two bf16 values and not exact: what was lost (exact in fp32, by the order of the
-// subtractions) then tells the side.
-__device__ __forceinline__ uint16_t add_bf16(float a, float b) {
+// bf16(a + b) of the exact sum, b of 24 bits.  Rounding the fp32 sum differs from it only where that
+// sum is a border between two bf16 values and not exact: what was lost (exact in fp32, by the order
+// of the subtractions) then tells the side.  With b a bf16 the sum is exact, or so much nearer to
+// the larger than to a border that plain rounding is right.
+__device__ __forceinline__ float add_settled(float a, float b) {
   const float s = a + b;
   uint32_t u = __float_as_uint(s);
   if ((u & 0xFFFFu) == 0x8000u) {
     const float bb = s - a, lost = (a - (s - bb)) + (b - bb);
     if (lost != 0.f) u += (lost > 0.f) == (s > 0.f) ? 1u : 0xFFFFFFFFu;
   }
-  return f2bf(__uint_as_float(u));
+  return __uint_as_float(u);
+}
+// {lo, hi} of two fp32 numbers in bf16
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // bf16(h g rinv), rinv in 64 bits and rinv_f its fp32 rounding.  The fp32 product carries three
@@ -55,12 +62,15 @@ __device__ __forceinline__ uint16_t add_bf16(float a, float b) {
 // (The 64-bit form stays a call: inlined at every element it would be most of the code.)
 __device__ __noinline__ uint32_t norm_bf16_64(float h, float g, double rinv) { return d2bf((double)h * (double)g * rinv); }
 
-__device__ __forceinline__ uint32_t norm_bf16(float h, float g, double rinv, float rinv_f) {
-  const float p = h * rinv_f * g;
-  const uint32_t u = __float_as_uint(p);
-  const uint32_t e = (u >> 23) & 255u;
-  if ((u & 0xFFFFu) - 0x7FFCu <= 8u || e - 16u > 222u) return norm_bf16_64(h, g, rinv);
-  return f2bf(p);
+// Two channels (h, g bf16 pairs) at once.
+__device__ __forceinline__ uint32_t norm_bf16x2(uint32_t h, uint32_t g, double rinv, float rinv_f) {
+  const float p0 = bf_lo(h) * rinv_f * bf_lo(g), p1 = bf_hi(h) * rinv_f * bf_hi(g);
+  const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+  // within 4 ulp of a border, or outside [2^-111, 2^112)
+  const bool far = min((u0 & 0xFFFFu) - 0x7FFCu, (u1 & 0xFFFFu) - 0x7FFCu) > 8u &&
+                   fminf(fabsf(p0), fabsf(p1)) >= 0x1p-111f && fmaxf(fabsf(p0), fabsf(p1)) < 0x1p112f;
+  if (far) return bf16x2(p0, p1);
+  return norm_bf16_64(bf_lo(h), bf_lo(g), rinv) | norm_bf16_64(bf_hi(h), bf_hi(g), rinv) << 16;
 }
 
 // The exact factor that brings a group whose largest magnitude is `a` into the range where
@@ -71,197 +81,225 @@ __device__ __forceinline__ float q8_range(float a) {
 
 // x M / a moved off a rounding border in the direction of the exact quotient: p approximates
 // it to 2^-22 relative, t is the border next to it.
-__device__ __forceinline__ float q8_settle(float p, float t, float xm, float a) {
+__device__ __forceinline__ float q8_settle(float t, float xm, float a) {
   const float ta = t * a;
   const float up = __uint_as_float(__float_as_uint(t) + 64u), dn = __uint_as_float(__float_as_uint(t) - 64u);
   return xm > ta ? up : (xm < ta ? dn : t);
 }
 
-// code of x (already times q8_range) for inv ~ M / a
-__device__ __forceinline__ uint32_t q8_int8(float x, float inv, float a) {
-  float p = fabsf(x) * inv;
-  const float t = rintf(p - 0.5f) + 0.5f;              // the border k + 1/2 nearest to p
-  if (fabsf(p - t) < 0x1p-14f) p = q8_settle(p, t, fabsf(x) * 127.0f, a);
-  const int q = (int)rintf(p);
-  return (uint32_t)(x < 0.f ? -q : q) & 255u;
-}
-
-__device__ __forceinline__ uint32_t q8_e4m3(float x, float inv, float a) {
-  float p = fabsf(x) * inv;
-  float t;
-  if (p >= 0x1p-6f) {                                   // three bits below the leading one
-    t = __uint_as_float((__float_as_uint(p) & 0xFFF00000u) | 0x00080000u);
-  } else {                                              // spacing 2^-9
-    t = (rintf(p * 512.0f - 0.5f) + 0.5f) * 0x1p-9f;
-  }
-  if (fabsf(p - t) <= 0x1p-18f * t) p = q8_settle(p, t, fabsf(x) * 448.0f, a);
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(p));
-  return (uint32_t)r | (x < 0.f ? 0x80u : 0u);
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
-// One row per block; thread i holds the 8-element chunks i, i + blockDim, ... (V of them) in
-// registers, so every input is read once.  VEC: rows and strides allow 16-byte accesses and
-// d % 8 == 0; otherwise each element is accessed by itself.
+// The codes of 8 channels x (already times q8_range), each decided at its border; a call, like the
+// 64-bit form above, since few chunks need it.
+__device__ __noinline__ uint2 q8_settled(uint4 x, float f, float inv, float a, int e4m3) {
+  const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+  uint32_t q[2] = {0, 0};
+#pragma unroll 1
+  for (int j = 0; j < 8; j++) {
+    const uint32_t w = j < 2 ? xs[0] : j < 4 ? xs[1] : j < 6 ? xs[2] : xs[3];
+    const float v = (j & 1 ? bf_hi(w) : bf_lo(w)) * f;
+    float p = fabsf(v) * inv;
+    uint32_t code;
+    if (e4m3) {
+      // the border: three bits below the leading one, or (below 2^-6) odd multiples of 2^-10
+      const float t = p >= 0x1p-6f ? __uint_as_float((__float_as_uint(p) & 0xFFF00000u) | 0x00080000u)
+                                   : (rintf(p * 512.0f - 0.5f) + 0.5f) * 0x1p-9f;
+      if (fabsf(p - t) <= 0x1p-18f * t) p = q8_settle(t, fabsf(v) * 448.0f, a);
+      code = (e4m3x2(p, 0.f) & 0x7Fu) | (v < 0.f ? 0x80u : 0u);
+    } else {
+      const float t = rintf(p - 0.5f) + 0.5f;              // the border k + 1/2 nearest to p
+      if (fabsf(p - t) < 0x1p-14f) p = q8_settle(t, fabsf(v) * 127.0f, a);
+      const int c = (int)rintf(p);
+      code = (uint32_t)(v < 0.f ? -c : c) & 255u;
+    }
+    q[j >> 2] |= code << (8 * (j & 3));
+  }
+  return make_uint2(q[0], q[1]);
+}
+
+// The codes of 8 channels by plain rounding, unless one lies near a border.
+__device__ __forceinline__ uint2 q8_codes(uint4 x, float f, float inv, float a, int e4m3) {
+  const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+  float p[8];
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    p[2 * j] = bf_lo(xs[j]) * f * inv;
+    p[2 * j + 1] = bf_hi(xs[j]) * f * inv;
+  }
+  uint32_t q[2];
+  bool near = false;
+  if (e4m3) {
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      // below 2^-6 the spacing is that of [2^-6, 2^-5): looked at there
+      const float m = fabsf(p[j]), v = m < 0x1p-6f ? m + 0x1p-6f : m;
+      near |= (__float_as_uint(v) & 0xFFFFFu) - 0x7FFE0u <= 64u;
+    }
+    q[0] = e4m3x2(p[0], p[1]) | e4m3x2(p[2], p[3]) << 16;
+    q[1] = e4m3x2(p[4], p[5]) | e4m3x2(p[6], p[7]) << 16;
+  } else {
+    uint32_t c[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      const float k = p[j] + 12582912.0f;                  // 1.5 2^23: the integer is in the low bits
+      c[j] = __float_as_uint(k);
+      near |= fabsf(p[j] - (k - 12582912.0f)) > 0.5f - 0x1p-14f;
+    }
+    q[0] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    q[1] = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
+  }
+  return near ? q8_settled(x, f, inv, a, e4m3) : make_uint2(q[0], q[1]);
+}
+
+// 8 channels from c on (those past d are zero), one by one
+__device__ __forceinline__ uint4 load8_single(const uint16_t *p, int c, int d) {
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; j++)
+    if (c + j < d) w[j >> 1] |= (uint32_t)p[c + j] << (16 * (j & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8_single(uint16_t *p, int c, int d, uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 8; j++)
+    if (c + j < d) p[c + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+}
+
+constexpr int addnorm_threads(int V) { return V == 4 ? 1024 : 512; }
+
+// One row per block; thread i holds the 8-channel chunks i, i + blockDim, ... (V of them) in
+// registers, so every input is read once.  With many rows V is 8 and a block is one warp for each
+// 2048 channels: 32 loads of 16 bytes under way a warp, no barrier to wait at.  With few rows V is 1
+// and a row is spread over as many threads as it has chunks.  VEC: rows and strides allow 16-byte
+// accesses and d % 8 == 0; otherwise each element is accessed by itself.
 template <int V, bool VEC>
-__global__ void __launch_bounds__(1024) k_add_rmsnorm(AddNormArgs A) {
+__global__ void __launch_bounds__(addnorm_threads(V)) k_add_rmsnorm(const __grid_constant__ AddNormArgs A) {
   __shared__ double red[32];
   __shared__ uint32_t redm[32];
   const long long row = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
-  const int d = A.d;
+  const int tid = threadIdx.x, lane = tid & 31, nwarp = blockDim.x >> 5, d = A.d;
   const uint16_t *h = A.h + row * A.h_stride;
-  float hv[V][8];
+  uint4 x[V];
+  auto at = [&](int v) { return 8 * (tid + v * (int)blockDim.x); };
 #pragma unroll
   for (int v = 0; v < V; v++) {
-    const int c = 8 * (tid + v * (int)blockDim.x);
-    if (VEC) {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (c < d) w = *reinterpret_cast<const uint4 *>(h + c);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        hv[v][2 * j] = __uint_as_float(ws[j] << 16);
-        hv[v][2 * j + 1] = __uint_as_float(ws[j] & 0xFFFF0000u);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; j++) hv[v][j] = c + j < d ? bf(h[c + j]) : 0.f;
-    }
+    const int c = at(v);
+    if (VEC)
+      x[v] = c < d ? __ldcs(reinterpret_cast<const uint4 *>(h + c)) : make_uint4(0, 0, 0, 0);
+    else
+      x[v] = load8_single(h, c, d);
   }
-  if (A.delta) {
+  if (A.delta && !A.delta_f32) {
+    const uint16_t *p = (const uint16_t *)A.delta + row * A.delta_stride;
+    uint4 e[V];
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      const int c = 8 * (tid + v * (int)blockDim.x);
-      float dv[8];
-#pragma unroll
-      for (int j = 0; j < 8; j++) dv[j] = 0.f;
-      if (A.delta_f32) {
-        const float *p = (const float *)A.delta + row * A.delta_stride + c;
-        if (VEC) {
-          if (c < d) {
-            const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-            dv[0] = a.x; dv[1] = a.y; dv[2] = a.z; dv[3] = a.w;
-            dv[4] = b.x; dv[5] = b.y; dv[6] = b.z; dv[7] = b.w;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; j++)
-            if (c + j < d) dv[j] = p[j];
-        }
-      } else {
-        const uint16_t *p = (const uint16_t *)A.delta + row * A.delta_stride + c;
-        if (VEC) {
-          if (c < d) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(p);
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-              dv[2 * j] = __uint_as_float(ws[j] << 16);
-              dv[2 * j + 1] = __uint_as_float(ws[j] & 0xFFFF0000u);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; j++)
-            if (c + j < d) dv[j] = bf(p[j]);
-        }
-      }
-      uint16_t o[8];
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        o[j] = add_bf16(hv[v][j], dv[j]);
-        hv[v][j] = bf(o[j]);
-      }
-      if (A.h_out) {
-        uint16_t *p = A.h_out + row * A.h_out_stride + c;
-        if (VEC) {
-          if (c < d)
-            *reinterpret_cast<uint4 *>(p) = make_uint4(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16,
-                                                       o[4] | (uint32_t)o[5] << 16, o[6] | (uint32_t)o[7] << 16);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; j++)
-            if (c + j < d) p[j] = o[j];
-        }
-      }
+      const int c = at(v);
+      if (VEC)
+        e[v] = c < d ? __ldcs(reinterpret_cast<const uint4 *>(p + c)) : make_uint4(0, 0, 0, 0);
+      else
+        e[v] = load8_single(p, c, d);
     }
-  } else if (A.h_out && A.h_out != A.h) {
+#pragma unroll
+    for (int v = 0; v < V; v++)
+      x[v] = make_uint4(bf16x2(bf_lo(x[v].x) + bf_lo(e[v].x), bf_hi(x[v].x) + bf_hi(e[v].x)),
+                        bf16x2(bf_lo(x[v].y) + bf_lo(e[v].y), bf_hi(x[v].y) + bf_hi(e[v].y)),
+                        bf16x2(bf_lo(x[v].z) + bf_lo(e[v].z), bf_hi(x[v].z) + bf_hi(e[v].z)),
+                        bf16x2(bf_lo(x[v].w) + bf_lo(e[v].w), bf_hi(x[v].w) + bf_hi(e[v].w)));
+  } else if (A.delta) {
+    const float *p = (const float *)A.delta + row * A.delta_stride;
 #pragma unroll
     for (int v = 0; v < V; v++) {
-      const int c = 8 * (tid + v * (int)blockDim.x);
-      uint16_t *p = A.h_out + row * A.h_out_stride + c;
-      uint32_t o[8];
-#pragma unroll
-      for (int j = 0; j < 8; j++) o[j] = __float_as_uint(hv[v][j]) >> 16;
+      const int c = at(v);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
       if (VEC) {
-        if (c < d)
-          *reinterpret_cast<uint4 *>(p) = make_uint4(o[0] | o[1] << 16, o[2] | o[3] << 16, o[4] | o[5] << 16, o[6] | o[7] << 16);
+        if (c < d) {
+          a = __ldcs(reinterpret_cast<const float4 *>(p + c));
+          b = __ldcs(reinterpret_cast<const float4 *>(p + c + 4));
+        }
       } else {
+        float w[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++)
-          if (c + j < d) p[j] = (uint16_t)o[j];
+        for (int j = 0; j < 8; j++) w[j] = c + j < d ? p[c + j] : 0.f;
+        a = make_float4(w[0], w[1], w[2], w[3]);
+        b = make_float4(w[4], w[5], w[6], w[7]);
       }
+      x[v] = make_uint4(bf16x2(add_settled(bf_lo(x[v].x), a.x), add_settled(bf_hi(x[v].x), a.y)),
+                        bf16x2(add_settled(bf_lo(x[v].y), a.z), add_settled(bf_hi(x[v].y), a.w)),
+                        bf16x2(add_settled(bf_lo(x[v].z), b.x), add_settled(bf_hi(x[v].z), b.y)),
+                        bf16x2(add_settled(bf_lo(x[v].w), b.z), add_settled(bf_hi(x[v].w), b.w)));
     }
   }
+  auto store = [&](uint16_t *out, long long stride) {
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+      const int c = at(v);
+      if (VEC) {
+        if (c < d) *reinterpret_cast<uint4 *>(out + row * stride + c) = x[v];
+      } else {
+        store8_single(out + row * stride, c, d, x[v]);
+      }
+    }
+  };
+  if (A.h_out && (A.delta || A.h_out != A.h)) store(A.h_out, A.h_out_stride);
   if (!A.x && !A.q8) return;
   // sum of squares in 64 bits: a bf16's square and their sum keep every bit that matters
   double ss = 0.0;
 #pragma unroll
-  for (int v = 0; v < V; v++)
-#pragma unroll
-    for (int j = 0; j < 8; j++) ss = fma((double)hv[v][j], (double)hv[v][j], ss);
-  ss = warp_sum(ss);
-  if (lane == 0) red[warp] = ss;
-  __syncthreads();
-  ss = 0.0;
-  for (int w = 0; w < nwarp; w++) ss += red[w];         // the same order on every thread
-  const double rinv = rsqrt(ss / d + (double)A.eps);
-  const float rinv_f = (float)rinv;
-  uint32_t rowmax = 0;
-  uint32_t xb[V][4];
-#pragma unroll
   for (int v = 0; v < V; v++) {
-    const int c = 8 * (tid + v * (int)blockDim.x);
-    float g[8];
-    if (VEC) {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (c < d) w = __ldg(reinterpret_cast<const uint4 *>(A.gamma + c));
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        g[2 * j] = __uint_as_float(ws[j] << 16);
-        g[2 * j + 1] = __uint_as_float(ws[j] & 0xFFFF0000u);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; j++) g[j] = c + j < d ? bf(A.gamma[c + j]) : 0.f;
-    }
+    const uint32_t w[4] = {x[v].x, x[v].y, x[v].z, x[v].w};
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      const uint32_t b0 = c + 2 * j < d ? norm_bf16(hv[v][2 * j], g[2 * j], rinv, rinv_f) : 0u;
-      const uint32_t b1 = c + 2 * j + 1 < d ? norm_bf16(hv[v][2 * j + 1], g[2 * j + 1], rinv, rinv_f) : 0u;
-      xb[v][j] = b0 | (b1 << 16);
-    }
-    if (A.x) {
-      uint16_t *p = A.x + row * A.x_stride + c;
-      if (VEC) {
-        if (c < d) *reinterpret_cast<uint4 *>(p) = make_uint4(xb[v][0], xb[v][1], xb[v][2], xb[v][3]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-          if (c + j < d) p[j] = (uint16_t)(xb[v][j >> 1] >> (16 * (j & 1)));
-      }
+      const double lo = (double)bf_lo(w[j]), hi = (double)bf_hi(w[j]);
+      ss = fma(lo, lo, fma(hi, hi, ss));
     }
   }
-  if (!A.q8) return;
-  // largest magnitude of each group, compared as integers so that a NaN is the largest
-  uint32_t gm[V];
+  ss = warp_sum(ss);
+  if (nwarp > 1) {
+    if (lane == 0) red[tid >> 5] = ss;
+    __syncthreads();
+    ss = 0.0;
+#pragma unroll 4
+    for (int w = 0; w < nwarp; w++) ss += red[w];       // the same order on every thread
+  }
+  const double rinv = rsqrt(ss / d + (double)A.eps);
+  const float rinv_f = (float)rinv;
+  uint32_t gm[V], rowmax = 0;
 #pragma unroll
   for (int v = 0; v < V; v++) {
-    uint32_t m = 0;
+    const int c = at(v);
+    uint4 g = make_uint4(0, 0, 0, 0);
+    if (VEC) {
+      if (c < d) g = __ldg(reinterpret_cast<const uint4 *>(A.gamma + c));
+    } else {
+      g = load8_single(A.gamma, c, d);
+    }
+    // (past the end, h and gamma are zero: a NaN or 0 that is neither stored nor counted)
+    if (c < d)
+      x[v] = make_uint4(norm_bf16x2(x[v].x, g.x, rinv, rinv_f), norm_bf16x2(x[v].y, g.y, rinv, rinv_f),
+                        norm_bf16x2(x[v].z, g.z, rinv, rinv_f), norm_bf16x2(x[v].w, g.w, rinv, rinv_f));
+    if (!VEC && c < d && c + 8 > d) {
+      // the ragged last chunk: zero what lies past the end
+      const int n = d - c;
+      const uint32_t keep[4] = {n > 1 ? 0xFFFFFFFFu : 0xFFFFu, n > 3 ? 0xFFFFFFFFu : n > 2 ? 0xFFFFu : 0u,
+                                n > 5 ? 0xFFFFFFFFu : n > 4 ? 0xFFFFu : 0u, n > 6 ? 0xFFFFu : 0u};
+      x[v] = make_uint4(x[v].x & keep[0], x[v].y & keep[1], x[v].z & keep[2], x[v].w & keep[3]);
+    }
+    // largest magnitude, compared as integers so that a NaN is the largest
+    const uint32_t m = __vmaxu2(__vmaxu2(x[v].x & 0x7FFF7FFFu, x[v].y & 0x7FFF7FFFu),
+                                __vmaxu2(x[v].z & 0x7FFF7FFFu, x[v].w & 0x7FFF7FFFu));
+    gm[v] = max(m & 0xFFFFu, m >> 16);
+  }
+  if (A.x) store(A.x, A.x_stride);
+  if (!A.q8) return;
 #pragma unroll
-    for (int j = 0; j < 4; j++) m = max(m, max(xb[v][j] & 0x7FFFu, (xb[v][j] >> 16) & 0x7FFFu));
+  for (int v = 0; v < V; v++) {
+    uint32_t m = gm[v];
     if (A.q8_group) {
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -272,42 +310,36 @@ __global__ void __launch_bounds__(1024) k_add_rmsnorm(AddNormArgs A) {
     rowmax = max(rowmax, m);
   }
   if (!A.q8_group) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) rowmax = max(rowmax, __shfl_xor_sync(0xffffffffu, rowmax, o));
-    if (lane == 0) redm[warp] = rowmax;
-    __syncthreads();
-    for (int w = 0; w < nwarp; w++) rowmax = max(rowmax, redm[w]);
+    rowmax = __reduce_max_sync(0xffffffffu, rowmax);
+    if (nwarp > 1) {
+      if (lane == 0) redm[tid >> 5] = rowmax;
+      __syncthreads();
+#pragma unroll 4
+      for (int w = 0; w < nwarp; w++) rowmax = max(rowmax, redm[w]);
+    }
 #pragma unroll
     for (int v = 0; v < V; v++) gm[v] = rowmax;
   }
   const float M = A.q8_e4m3 ? 448.0f : 127.0f;
 #pragma unroll
   for (int v = 0; v < V; v++) {
-    const int c = 8 * (tid + v * (int)blockDim.x);
+    const int c = at(v);
     if (c >= d) continue;
     const float a = bf(gm[v]);
     const bool ok = gm[v] < 0x7F80u;
-    const float scale = ok ? a / M : __uint_as_float(0x7FC00000u);
-    if (A.q8_group ? c % A.q8_group == 0 : c == 0)
-      A.q8_scale[row * A.groups + (A.q8_group ? c / A.q8_group : 0)] = scale;
+    if (A.q8_group ? (c & (A.q8_group - 1)) == 0 : c == 0)
+      A.q8_scale[row * A.groups + (A.q8_group ? c / A.q8_group : 0)] = ok ? a / M : __uint_as_float(0x7FC00000u);
     const float f = q8_range(a), af = a * f;
-    const float inv = ok && a > 0.f ? M / af : 0.f;
-    uint32_t q[2] = {0, 0};
-    if (inv > 0.f) {
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        const float xv = __uint_as_float(j & 1 ? xb[v][j >> 1] & 0xFFFF0000u : xb[v][j >> 1] << 16) * f;
-        const uint32_t code = A.q8_e4m3 ? q8_e4m3(xv, inv, af) : q8_int8(xv, inv, af);
-        q[j >> 2] |= code << (8 * (j & 3));
-      }
-    }
+    const float inv = ok && a > 0.f ? __fdiv_rn(M, af) : 0.f;
+    uint2 q = make_uint2(0, 0);
+    if (inv > 0.f) q = q8_codes(x[v], f, inv, af, A.q8_e4m3);
     uint8_t *p = A.q8 + row * A.q8_stride + c;
     if (VEC) {
-      *reinterpret_cast<uint2 *>(p) = make_uint2(q[0], q[1]);
+      *reinterpret_cast<uint2 *>(p) = q;
     } else {
 #pragma unroll
       for (int j = 0; j < 8; j++)
-        if (c + j < d) p[j] = (uint8_t)(q[j >> 2] >> (8 * (j & 3)));
+        if (c + j < d) p[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
     }
   }
 }

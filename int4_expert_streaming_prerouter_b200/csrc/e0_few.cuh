@@ -363,9 +363,7 @@ __device__ __forceinline__ void few_phase1(const FewArgs &A, FewPlan &P, uint8_t
       if (dl) dv = *reinterpret_cast<const uint4 *>(dl + cn);
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        if (dl)
-          ws[j] = add_bf16(__uint_as_float(ws[j] << 16), __uint_as_float(es[j] << 16)) |
-                  (uint32_t)add_bf16(__uint_as_float(ws[j] & 0xFFFF0000u), __uint_as_float(es[j] & 0xFFFF0000u)) << 16;
+        if (dl) ws[j] = bf16x2(bf_lo(ws[j]) + bf_lo(es[j]), bf_hi(ws[j]) + bf_hi(es[j]));
         const double lo = (double)__uint_as_float(ws[j] << 16), hi = (double)__uint_as_float(ws[j] & 0xFFFF0000u);
         ss = fma(lo, lo, fma(hi, hi, ss));
       }
@@ -390,10 +388,8 @@ __device__ __forceinline__ void few_phase1(const FewArgs &A, FewPlan &P, uint8_t
       float v = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; j++) {
-        const uint32_t e0 = norm_bf16(__uint_as_float(ws[j] << 16), __uint_as_float(gs[j] << 16), rinv, rinv_f);
-        const uint32_t e1 = norm_bf16(__uint_as_float(ws[j] & 0xFFFF0000u), __uint_as_float(gs[j] & 0xFFFF0000u), rinv, rinv_f);
-        o[j] = e0 | (e1 << 16);
-        v += bf(e0) + bf(e1);
+        o[j] = norm_bf16x2(ws[j], gs[j], rinv, rinv_f);
+        v += bf_lo(o[j]) + bf_hi(o[j]);
       }
       v = group_sum(v, 8);                          // d is a multiple of 256: whole warps
       const uint4 xv = operand_order(make_uint4(o[0], o[1], o[2], o[3]));

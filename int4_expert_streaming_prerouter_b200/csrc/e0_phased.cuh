@@ -168,8 +168,6 @@ __device__ inline void ph_build_plan(const int32_t *idx, int ld, int B, int k, i
 __device__ __forceinline__ float ph_fold(float acc, float s, float mprime, float Pv, float X) {
   return fmaf(s, Pv, fmaf(mprime, X, acc));
 }
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // ---------------------------------------------------------------------------------------
 // K0: RMSNorm of every (layer, token): x in natural order and in pair order, and the
