@@ -62,15 +62,33 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 // (The 64-bit form stays a call: inlined at every element it would be most of the code.)
 __device__ __noinline__ uint32_t norm_bf16_64(float h, float g, double rinv) { return d2bf((double)h * (double)g * rinv); }
 
-// Two channels (h, g bf16 pairs) at once.
-__device__ __forceinline__ uint32_t norm_bf16x2(uint32_t h, uint32_t g, double rinv, float rinv_f) {
-  const float p0 = bf_lo(h) * rinv_f * bf_lo(g), p1 = bf_hi(h) * rinv_f * bf_hi(g);
-  const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-  // within 4 ulp of a border, or outside [2^-111, 2^112)
-  const bool far = min((u0 & 0xFFFFu) - 0x7FFCu, (u1 & 0xFFFFu) - 0x7FFCu) > 8u &&
-                   fminf(fabsf(p0), fabsf(p1)) >= 0x1p-111f && fmaxf(fabsf(p0), fabsf(p1)) < 0x1p112f;
-  if (far) return bf16x2(p0, p1);
-  return norm_bf16_64(bf_lo(h), bf_lo(g), rinv) | norm_bf16_64(bf_hi(h), bf_hi(g), rinv) << 16;
+// 8 channels of h and gamma (bf16) normed; the largest of their magnitudes (as bf16 bits: a NaN is the
+// largest) goes to `most`.  Results within 4 ulp of a border, or not in [2^-111, 2^112) (where the
+// fp32 product, or the 2^-133 spacing of small bf16 numbers, would need care), are done again.
+__device__ __forceinline__ uint4 norm_bf16x8(uint4 h, uint4 g, double rinv, float rinv_f, uint32_t &most) {
+  const uint32_t hs[4] = {h.x, h.y, h.z, h.w}, gs[4] = {g.x, g.y, g.z, g.w};
+  uint32_t o[4], border = 0xFFFFFFFFu, low = 0xFFFFFFFFu, high = 0;
+#pragma unroll
+  for (int j = 0; j < 4; j++) {
+    const float p0 = bf_lo(hs[j]) * rinv_f * bf_lo(gs[j]), p1 = bf_hi(hs[j]) * rinv_f * bf_hi(gs[j]);
+    o[j] = bf16x2(p0, p1);
+    // the 16 dropped bits of both, plus 0x8004: at most 8 next to a border, or 9 with the carry of
+    // the lower half
+    border = __vminu2(border, __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x5410) + 0x80048004u);
+    low = __vminu2(low, o[j] & 0x7FFF7FFFu);
+    high = __vmaxu2(high, o[j] & 0x7FFF7FFFu);
+  }
+  most = max(high & 0xFFFFu, high >> 16);
+  if (min(border & 0xFFFFu, border >> 16) <= 9u || (min(low & 0xFFFFu, low >> 16) < 0x0800u && rinv_f > 0.f) || most >= 0x7780u) {
+    most = 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const uint32_t lo = norm_bf16_64(bf_lo(hs[j]), bf_lo(gs[j]), rinv), hi = norm_bf16_64(bf_hi(hs[j]), bf_hi(gs[j]), rinv);
+      o[j] = lo | hi << 16;
+      most = max(most, max(lo & 0x7FFFu, hi & 0x7FFFu));
+    }
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 // The exact factor that brings a group whose largest magnitude is `a` into the range where
@@ -121,38 +139,37 @@ __device__ __noinline__ uint2 q8_settled(uint4 x, float f, float inv, float a, i
   return make_uint2(q[0], q[1]);
 }
 
-// The codes of 8 channels by plain rounding, unless one lies near a border.
+// The codes of 8 channels: where x times an inv a little larger and a little smaller (by more than
+// its error) round to the same codes, those; else each is decided at its border.
 __device__ __forceinline__ uint2 q8_codes(uint4 x, float f, float inv, float a, int e4m3) {
   const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-  float p[8];
-#pragma unroll
-  for (int j = 0; j < 4; j++) {
-    p[2 * j] = bf_lo(xs[j]) * f * inv;
-    p[2 * j + 1] = bf_hi(xs[j]) * f * inv;
-  }
-  uint32_t q[2];
-  bool near = false;
+  uint2 q;
+  bool same = f == 1.0f;
   if (e4m3) {
+    const float up = inv * (1.0f + 0x1p-19f), dn = inv * (1.0f - 0x1p-19f);
+    uint32_t u[4], w[4];
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-      // below 2^-6 the spacing is that of [2^-6, 2^-5): looked at there
-      const float m = fabsf(p[j]), v = m < 0x1p-6f ? m + 0x1p-6f : m;
-      near |= (__float_as_uint(v) & 0xFFFFFu) - 0x7FFE0u <= 64u;
+    for (int j = 0; j < 4; j++) {
+      u[j] = e4m3x2(bf_lo(xs[j]) * up, bf_hi(xs[j]) * up);
+      w[j] = e4m3x2(bf_lo(xs[j]) * dn, bf_hi(xs[j]) * dn);
     }
-    q[0] = e4m3x2(p[0], p[1]) | e4m3x2(p[2], p[3]) << 16;
-    q[1] = e4m3x2(p[4], p[5]) | e4m3x2(p[6], p[7]) << 16;
+    q = make_uint2(u[0] | u[1] << 16, u[2] | u[3] << 16);
+    same &= q.x == (w[0] | w[1] << 16) && q.y == (w[2] | w[3] << 16);
   } else {
-    uint32_t c[8];
+    // + 1.5 2^23: the integer is in the low bits
+    const float up = inv * (1.0f + 0x1p-20f), dn = inv * (1.0f - 0x1p-20f);
+    uint32_t u[8], w[8];
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      const float k = p[j] + 12582912.0f;                  // 1.5 2^23: the integer is in the low bits
-      c[j] = __float_as_uint(k);
-      near |= fabsf(p[j] - (k - 12582912.0f)) > 0.5f - 0x1p-14f;
+      const float v = j & 1 ? bf_hi(xs[j >> 1]) : bf_lo(xs[j >> 1]);
+      u[j] = __float_as_uint(fmaf(v, up, 12582912.0f));
+      w[j] = __float_as_uint(fmaf(v, dn, 12582912.0f));
     }
-    q[0] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-    q[1] = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
+    auto pack = [](const uint32_t *c) { return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410); };
+    q = make_uint2(pack(u), pack(u + 4));
+    same &= q.x == pack(w) && q.y == pack(w + 4);
   }
-  return near ? q8_settled(x, f, inv, a, e4m3) : make_uint2(q[0], q[1]);
+  return same ? q : q8_settled(x, f, inv, a, e4m3);
 }
 
 // 8 channels from c on (those past d are zero), one by one
@@ -173,9 +190,7 @@ __device__ __forceinline__ void store8_single(uint16_t *p, int c, int d, uint4 v
 constexpr int addnorm_threads(int V) { return V == 4 ? 1024 : 512; }
 
 // One row per block; thread i holds the 8-channel chunks i, i + blockDim, ... (V of them) in
-// registers, so every input is read once.  With many rows V is 8 and a block is one warp for each
-// 2048 channels: 32 loads of 16 bytes under way a warp, no barrier to wait at.  With few rows V is 1
-// and a row is spread over as many threads as it has chunks.  VEC: rows and strides allow 16-byte
+// registers, so every input is read once.  VEC: rows and strides allow 16-byte
 // accesses and d % 8 == 0; otherwise each element is accessed by itself.
 template <int V, bool VEC>
 __global__ void __launch_bounds__(addnorm_threads(V)) k_add_rmsnorm(const __grid_constant__ AddNormArgs A) {
@@ -280,20 +295,18 @@ __global__ void __launch_bounds__(addnorm_threads(V)) k_add_rmsnorm(const __grid
       g = load8_single(A.gamma, c, d);
     }
     // (past the end, h and gamma are zero: a NaN or 0 that is neither stored nor counted)
-    if (c < d)
-      x[v] = make_uint4(norm_bf16x2(x[v].x, g.x, rinv, rinv_f), norm_bf16x2(x[v].y, g.y, rinv, rinv_f),
-                        norm_bf16x2(x[v].z, g.z, rinv, rinv_f), norm_bf16x2(x[v].w, g.w, rinv, rinv_f));
+    gm[v] = 0;
+    if (c < d) x[v] = norm_bf16x8(x[v], g, rinv, rinv_f, gm[v]);
     if (!VEC && c < d && c + 8 > d) {
       // the ragged last chunk: zero what lies past the end
       const int n = d - c;
       const uint32_t keep[4] = {n > 1 ? 0xFFFFFFFFu : 0xFFFFu, n > 3 ? 0xFFFFFFFFu : n > 2 ? 0xFFFFu : 0u,
                                 n > 5 ? 0xFFFFFFFFu : n > 4 ? 0xFFFFu : 0u, n > 6 ? 0xFFFFu : 0u};
       x[v] = make_uint4(x[v].x & keep[0], x[v].y & keep[1], x[v].z & keep[2], x[v].w & keep[3]);
+      const uint32_t m = __vmaxu2(__vmaxu2(x[v].x & 0x7FFF7FFFu, x[v].y & 0x7FFF7FFFu),
+                                  __vmaxu2(x[v].z & 0x7FFF7FFFu, x[v].w & 0x7FFF7FFFu));
+      gm[v] = max(m & 0xFFFFu, m >> 16);
     }
-    // largest magnitude, compared as integers so that a NaN is the largest
-    const uint32_t m = __vmaxu2(__vmaxu2(x[v].x & 0x7FFF7FFFu, x[v].y & 0x7FFF7FFFu),
-                                __vmaxu2(x[v].z & 0x7FFF7FFFu, x[v].w & 0x7FFF7FFFu));
-    gm[v] = max(m & 0xFFFFu, m >> 16);
   }
   if (A.x) store(A.x, A.x_stride);
   if (!A.q8) return;
@@ -330,7 +343,7 @@ __global__ void __launch_bounds__(addnorm_threads(V)) k_add_rmsnorm(const __grid
     if (A.q8_group ? (c & (A.q8_group - 1)) == 0 : c == 0)
       A.q8_scale[row * A.groups + (A.q8_group ? c / A.q8_group : 0)] = ok ? a / M : __uint_as_float(0x7FC00000u);
     const float f = q8_range(a), af = a * f;
-    const float inv = ok && a > 0.f ? __fdiv_rn(M, af) : 0.f;
+    const float inv = ok && a > 0.f ? __fdividef(M, af) : 0.f;      // off by 2 ulp at most
     uint2 q = make_uint2(0, 0);
     if (inv > 0.f) q = q8_codes(x[v], f, inv, af, A.q8_e4m3);
     uint8_t *p = A.q8 + row * A.q8_stride + c;

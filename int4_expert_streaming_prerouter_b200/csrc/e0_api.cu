@@ -2079,19 +2079,16 @@ extern "C" int e0_add_rmsnorm(const void *h, long long h_stride, const void *del
                    (!delta || (!misaligned(delta, 16) && delta_stride % 8 == 0)) &&
                    (!h_out || (!misaligned(h_out, 16) && h_out_stride % 8 == 0)) &&
                    (!x || (!misaligned(x, 16) && x_stride % 8 == 0)) && (!q8 || (!misaligned(q8, 8) && q8_stride % 8 == 0));
-  // Many rows (enough for 8 warps an SM even at a warp for each 2048 channels): 8 chunks a thread;
-  // few: one, and more only where a row has more chunks than a block threads.
+  // A chunk of 8 channels a thread for few rows; two where there are many, so that a block's fixed
+  // work (the row's sum, its root) is shared by more, or a row has more chunks than a block threads.
   const int chunks = (d + 7) / 8;
-  int V = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4;
-  if (vec && (long long)T * ((chunks + 255) / 256) >= 1184 && chunks >= 256) V = 8;
-  if (!vec && V == 2) V = 4;
+  const int V = !vec ? (chunks <= 512 ? 1 : 4) : chunks > 1024 ? 4 : chunks > 512 || (T >= 1184 && chunks >= 64) ? 2 : 1;
   const int threads = ((chunks + V - 1) / V + 31) / 32 * 32;
   cudaStream_t s = (cudaStream_t)stream;
   if (vec) {
     if (V == 1) k_add_rmsnorm<1, true><<<T, threads, 0, s>>>(A);
     else if (V == 2) k_add_rmsnorm<2, true><<<T, threads, 0, s>>>(A);
-    else if (V == 4) k_add_rmsnorm<4, true><<<T, threads, 0, s>>>(A);
-    else k_add_rmsnorm<8, true><<<T, threads, 0, s>>>(A);
+    else k_add_rmsnorm<4, true><<<T, threads, 0, s>>>(A);
   } else {
     if (V == 1) k_add_rmsnorm<1, false><<<T, threads, 0, s>>>(A);
     else k_add_rmsnorm<4, false><<<T, threads, 0, s>>>(A);

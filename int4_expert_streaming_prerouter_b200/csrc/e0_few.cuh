@@ -382,17 +382,12 @@ __device__ __forceinline__ void few_phase1(const FewArgs &A, FewPlan &P, uint8_t
 #pragma unroll 1
     for (int c = c0; c < d; c += wpt * 256) {
       const uint4 w = *reinterpret_cast<const uint4 *>(xs + c * 2);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w}, gs[4] = {gm.x, gm.y, gm.z, gm.w};
+      uint32_t most;
+      const uint4 o = norm_bf16x8(w, gm, rinv, rinv_f, most);
       gm = __ldg(reinterpret_cast<const uint4 *>(A.gamma + min(c + wpt * 256, d - 8)));
-      uint32_t o[4];
-      float v = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        o[j] = norm_bf16x2(ws[j], gs[j], rinv, rinv_f);
-        v += bf_lo(o[j]) + bf_hi(o[j]);
-      }
+      float v = ((bf_lo(o.x) + bf_hi(o.x)) + (bf_lo(o.y) + bf_hi(o.y))) + ((bf_lo(o.z) + bf_hi(o.z)) + (bf_lo(o.w) + bf_hi(o.w)));
       v = group_sum(v, 8);                          // d is a multiple of 256: whole warps
-      const uint4 xv = operand_order(make_uint4(o[0], o[1], o[2], o[3]));
+      const uint4 xv = operand_order(o);
       *reinterpret_cast<uint4 *>(xs + c * 2) = xv;
       if ((lane & 7) == 0) *reinterpret_cast<float *>(area + 8 * pitch + tok * vbytes + c / 64 * 4) = v;
       if (K.member == 0) {
