@@ -79,7 +79,16 @@ __device__ __forceinline__ uint4 norm_bf16x8(uint4 h, uint4 g, double rinv, floa
     high = __vmaxu2(high, o[j] & 0x7FFF7FFFu);
   }
   most = max(high & 0xFFFFu, high >> 16);
-  if (min(border & 0xFFFFu, border >> 16) <= 9u || (min(low & 0xFFFFu, low >> 16) < 0x0800u && rinv_f > 0.f) || most >= 0x7780u) {
+  bool again = min(border & 0xFFFFu, border >> 16) <= 9u || most >= 0x7780u;
+  if (min(low & 0xFFFFu, low >> 16) < 0x0800u) {
+    // (a zero is what it is)
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const uint32_t lo = o[j] & 0x7FFFu, hi = (o[j] >> 16) & 0x7FFFu;
+      again |= (lo < 0x0800u && bf_lo(hs[j]) * bf_lo(gs[j]) != 0.f) || (hi < 0x0800u && bf_hi(hs[j]) * bf_hi(gs[j]) != 0.f);
+    }
+  }
+  if (again) {
     most = 0;
 #pragma unroll
     for (int j = 0; j < 4; j++) {
@@ -97,79 +106,34 @@ __device__ __forceinline__ float q8_range(float a) {
   return a < 0x1p-60f ? 0x1p70f : (a > 0x1p60f ? 0x1p-70f : 1.0f);
 }
 
-// x M / a moved off a rounding border in the direction of the exact quotient: p approximates
-// it to 2^-22 relative, t is the border next to it.
-__device__ __forceinline__ float q8_settle(float t, float xm, float a) {
-  const float ta = t * a;
-  const float up = __uint_as_float(__float_as_uint(t) + 64u), dn = __uint_as_float(__float_as_uint(t) - 64u);
-  return xm > ta ? up : (xm < ta ? dn : t);
-}
-
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
-// The codes of 8 channels x (already times q8_range), each decided at its border; a call, like the
-// 64-bit form above, since few chunks need it.
-__device__ __noinline__ uint2 q8_settled(uint4 x, float f, float inv, float a, int e4m3) {
-  const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-  uint32_t q[2] = {0, 0};
-#pragma unroll 1
-  for (int j = 0; j < 8; j++) {
-    const uint32_t w = j < 2 ? xs[0] : j < 4 ? xs[1] : j < 6 ? xs[2] : xs[3];
-    const float v = (j & 1 ? bf_hi(w) : bf_lo(w)) * f;
-    float p = fabsf(v) * inv;
-    uint32_t code;
-    if (e4m3) {
-      // the border: three bits below the leading one, or (below 2^-6) odd multiples of 2^-10
-      const float t = p >= 0x1p-6f ? __uint_as_float((__float_as_uint(p) & 0xFFF00000u) | 0x00080000u)
-                                   : (rintf(p * 512.0f - 0.5f) + 0.5f) * 0x1p-9f;
-      if (fabsf(p - t) <= 0x1p-18f * t) p = q8_settle(t, fabsf(v) * 448.0f, a);
-      code = (e4m3x2(p, 0.f) & 0x7Fu) | (v < 0.f ? 0x80u : 0u);
-    } else {
-      const float t = rintf(p - 0.5f) + 0.5f;              // the border k + 1/2 nearest to p
-      if (fabsf(p - t) < 0x1p-14f) p = q8_settle(t, fabsf(v) * 127.0f, a);
-      const int c = (int)rintf(p);
-      code = (uint32_t)(v < 0.f ? -c : c) & 255u;
-    }
-    q[j >> 2] |= code << (8 * (j & 3));
-  }
-  return make_uint2(q[0], q[1]);
+// p rounded to 18 significant bits (Veltkamp's splitting, each operation rounded by itself).
+__device__ __forceinline__ float to_18_bits(float p) {
+  const float c = __fmul_rn(p, 65.0f);
+  return __fsub_rn(c, __fsub_rn(c, p));
 }
 
-// The codes of 8 channels: where x times an inv a little larger and a little smaller (by more than
-// its error) round to the same codes, those; else each is decided at its border.
-__device__ __forceinline__ uint2 q8_codes(uint4 x, float f, float inv, float a, int e4m3) {
+// The codes of 8 channels; f, inv ~ M / a with x f inv = x M / a.  A quotient x M / a that is not a border
+// t between two codes differs from it by 2^-16 t or more: |x| M and t a are products of 8 bits by 7 (M) and
+// of 8 bits (t; 5 for e4m3) by 8, so in units of their last bit they are whole numbers below 2^16.  The fp32
+// product below is off by less than 2^-21, so rounding it to 18 bits gives t where x M / a = t, and a number
+// on the right side of t otherwise; rounding that to a code, ties to even, rounds x M / a.
+__device__ __forceinline__ uint2 q8_codes(uint4 x, float f, float inv, int e4m3) {
   const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-  uint2 q;
-  bool same = f == 1.0f;
-  if (e4m3) {
-    const float up = inv * (1.0f + 0x1p-19f), dn = inv * (1.0f - 0x1p-19f);
-    uint32_t u[4], w[4];
+  float p[8];
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
-      u[j] = e4m3x2(bf_lo(xs[j]) * up, bf_hi(xs[j]) * up);
-      w[j] = e4m3x2(bf_lo(xs[j]) * dn, bf_hi(xs[j]) * dn);
-    }
-    q = make_uint2(u[0] | u[1] << 16, u[2] | u[3] << 16);
-    same &= q.x == (w[0] | w[1] << 16) && q.y == (w[2] | w[3] << 16);
-  } else {
-    // + 1.5 2^23: the integer is in the low bits
-    const float up = inv * (1.0f + 0x1p-20f), dn = inv * (1.0f - 0x1p-20f);
-    uint32_t u[8], w[8];
+  for (int j = 0; j < 8; j++) p[j] = to_18_bits((j & 1 ? bf_hi(xs[j >> 1]) : bf_lo(xs[j >> 1])) * f * inv);
+  if (e4m3) return make_uint2(e4m3x2(p[0], p[1]) | e4m3x2(p[2], p[3]) << 16, e4m3x2(p[4], p[5]) | e4m3x2(p[6], p[7]) << 16);
+  uint32_t c[8];
 #pragma unroll
-    for (int j = 0; j < 8; j++) {
-      const float v = j & 1 ? bf_hi(xs[j >> 1]) : bf_lo(xs[j >> 1]);
-      u[j] = __float_as_uint(fmaf(v, up, 12582912.0f));
-      w[j] = __float_as_uint(fmaf(v, dn, 12582912.0f));
-    }
-    auto pack = [](const uint32_t *c) { return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410); };
-    q = make_uint2(pack(u), pack(u + 4));
-    same &= q.x == pack(w) && q.y == pack(w + 4);
-  }
-  return same ? q : q8_settled(x, f, inv, a, e4m3);
+  for (int j = 0; j < 8; j++) c[j] = __float_as_uint(p[j] + 12582912.0f);      // 1.5 2^23: the integer is in the low bits
+  return make_uint2(__byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410));
 }
 
 // 8 channels from c on (those past d are zero), one by one
@@ -345,7 +309,7 @@ __global__ void __launch_bounds__(addnorm_threads(V)) k_add_rmsnorm(const __grid
     const float f = q8_range(a), af = a * f;
     const float inv = ok && a > 0.f ? __fdividef(M, af) : 0.f;      // off by 2 ulp at most
     uint2 q = make_uint2(0, 0);
-    if (inv > 0.f) q = q8_codes(x[v], f, inv, af, A.q8_e4m3);
+    if (inv > 0.f) q = q8_codes(x[v], f, inv, A.q8_e4m3);
     uint8_t *p = A.q8 + row * A.q8_stride + c;
     if (VEC) {
       *reinterpret_cast<uint2 *>(p) = q;
