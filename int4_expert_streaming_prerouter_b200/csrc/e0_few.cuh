@@ -986,10 +986,11 @@ __device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, u
       const int p0 = P.seg_at[s0], p1 = P.seg_at[s1];
       __syncthreads();
       const int split = A.Ad && first ? few_td(A, td) : 0;
-      // sums by group of 64 of the tiles' sums
-#pragma unroll 1
+      // sums by group of 64 of the tiles' sums (u / G by its reciprocal: u < 2^16)
+      const uint32_t rg = 0xFFFFFFFFu / G + 1;
+#pragma unroll 4
       for (int u = tid; u < (p1 - p0) * G; u += kFewThreads) {
-        const int p = u / G, g = u - p * G;
+        const int p = __umulhi(u, rg), g = u - p * G;
         const float4 *q = reinterpret_cast<const float4 *>(A.a8 + (size_t)P.asg[p0 + p] * (A.I / 8) + g * 8);
         const float4 v = q[0], w = q[1];
         sums[u] = ((v.x + v.y) + (v.z + v.w)) + ((w.x + w.y) + (w.z + w.w));
