@@ -2308,13 +2308,12 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
   CK(cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev));
   if (!coop || nsm < kFewWarps) return fail(E0_ERR_CUDA, "moe_layer_few: the device has no cooperative launch");
   // shared memory: phase 2 holds the rings and as many activation rows as the rest takes; phase 3
-  // t_d, the results of every (token, slot), the sums of their activations and the rings, at least
-  // two stages each.  Tokens of a segment: 16 where both phases have room for them, else 8.
+  // t_d, the results of every (token, slot), the sums of their activations and the rings.  Tokens of a segment: 16 where both phases have room for them, else 8.
   const int smem = most, rest = smem - (int)few_plan_bytes() - kFewZeroBytes - kFewRedBytes;
   A.gu_rows = (rest - kFewRingBytes) / few_row_bytes(A.d);
   const int places = T * (A.k + 1), sum_bytes = A.I / 64 * 4;
   A.out_bytes = std::max(16384, places * 64);
-  const int least8 = kFewWarps * 2 * (few_dn_stage(8) + kFewSlot), least16 = kFewWarps * 2 * (few_dn_stage(16) + kFewSlot);
+  const int least8 = kFewWarps * std::max(few_dn_ring(4), few_dn_ring(8)), least16 = kFewWarps * few_dn_ring(16);
   const int wish = std::min(places, 16) * sum_bytes + 16;
   A.seg_cap = A.gu_rows >= 16 && rest - A.out_bytes - wish >= least16 ? 16 : 8;
   const int most_sums = rest - A.out_bytes - 16 - (A.seg_cap == 16 ? least16 : least8);

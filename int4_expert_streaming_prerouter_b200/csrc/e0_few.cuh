@@ -141,13 +141,9 @@ constexpr int kFewSlot = 16 * 32;
 constexpr int kFewRing = kFewDepth * (kFewStage + kFewSlot), kFewRingBytes = kFewWarps * kFewRing;
 constexpr int kFewDnHead = 16 * 64, kFewDnRow = 256 + 16;
 constexpr int few_dn_stage(int tokens) { return kFewDnHead + tokens * kFewDnRow; }
+constexpr int few_dn_depth(int tokens) { return tokens <= 4 ? 3 : 2; }
+constexpr int few_dn_ring(int tokens) { return few_dn_depth(tokens) * (few_dn_stage(tokens) + kFewSlot); }
 
-// all but the newest n (0..2) groups
-__device__ __forceinline__ void cp_async_wait_upto(int n) {
-  if (n <= 0) cp_async_wait_but<0>();
-  else if (n == 1) cp_async_wait_but<1>();
-  else cp_async_wait_but<2>();
-}
 // Activation rows in shared memory: bf16 rows `pitch` bytes apart, and their sums by group.
 struct FewOps {
   uint32_t x, v;              // shared addresses
@@ -264,16 +260,17 @@ __device__ __forceinline__ void few_mul128(uint32_t w0, uint32_t w1, uint32_t ws
   }
 }
 
-// A number whose order as an unsigned integer is the order of the floats; a NaN is the lowest
-// but one (0 is what has been taken).
+// A number whose order as an unsigned integer is the order of the floats, and back; a NaN is the
+// lowest but one (0 is what has been taken).
 __device__ __forceinline__ uint32_t few_key(float f) {
   const uint32_t u = __float_as_uint(f == f ? (f == 0.f ? 0.f : f) : -INFINITY);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+__device__ __forceinline__ float few_key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
 
 // Top-k of E <= 256 keys (lane l holds those of l, l + 32, ...; 0 past the end) over a warp,
-// descending, equal values by lower index.  Lane j < k gets the j-th index.
-__device__ __forceinline__ int few_topk(uint32_t (&key)[kMaxE / 32], int k, int lane) {
+// descending, equal values by lower index.  Lane j < k gets the j-th index and its key.
+__device__ __forceinline__ int few_topk(uint32_t (&key)[kMaxE / 32], int k, int lane, uint32_t &mine_key) {
   int mine = 0;
 #pragma unroll 1
   for (int s = 0; s < k; s++) {
@@ -286,7 +283,10 @@ __device__ __forceinline__ int few_topk(uint32_t (&key)[kMaxE / 32], int k, int 
     for (int i = kMaxE / 32 - 1; i >= 0; i--)
       if (key[i] == m) at = lane + 32 * i;
     at = __reduce_min_sync(0xffffffffu, at);
-    if (lane == s) mine = (int)at;
+    if (lane == s) {
+      mine = (int)at;
+      mine_key = m;
+    }
 #pragma unroll
     for (int i = 0; i < kMaxE / 32; i++)
       if ((uint32_t)(lane + 32 * i) == at) key[i] = 0;
@@ -444,28 +444,44 @@ __device__ __forceinline__ void few_residual(const FewArgs &A, const uint8_t *ar
 // ---------------------------------------------------------------------------------------
 // Routing of every token and the segments of (token, slot) assignments by expert
 // ---------------------------------------------------------------------------------------
-// A warp takes one token: lane j < k gets its j-th expert and gate.  `say`: report bad routing.
+// The given expert of lane j < k for token t, -1 where the token has none.
+__device__ __forceinline__ int few_given(const FewArgs &A, int t) {
+  const int lane = threadIdx.x & 31;
+  return A.route != nullptr && t < A.T && lane < A.k ? __ldg(A.route + (size_t)t * A.k + lane) : -1;
+}
+
+// A warp takes one token, whose given experts are `e` (few_given): lane j < k gets its j-th expert and
+// gate.  `say`: report bad routing.
 __device__ __forceinline__ void few_route(const FewArgs &A, int t, bool say, int &e, float &gate) {
   const int lane = threadIdx.x & 31, k = A.k, E = A.E;
   const float *lg = A.logits + (size_t)t * E;
-  uint32_t key[kMaxE / 32];
-  e = -1;
-  if (A.route != nullptr && lane < k) e = A.route[(size_t)t * k + lane];
-#pragma unroll
-  for (int i = 0; i < kMaxE / 32; i++) key[i] = lane + 32 * i < E ? few_key(lg[lane + 32 * i]) : 0u;
+  float l = -INFINITY;
   if (__shfl_sync(0xffffffffu, e, 0) < 0) {
-    e = few_topk(key, k, lane);
+    uint32_t key[kMaxE / 32], mine = 0;
+    float f[kMaxE / 32];
+#pragma unroll
+    for (int i = 0; i < kMaxE / 32; i++) f[i] = lane + 32 * i < E ? lg[lane + 32 * i] : 0.f;
+    unsigned nan = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxE / 32; i++) {
+      nan |= f[i] != f[i];
+      key[i] = lane + 32 * i < E ? few_key(f[i]) : 0u;
+    }
+    e = few_topk(key, k, lane, mine);
+    // (with a NaN among the logits the gates are the NaNs that they come to)
+    const bool look = __any_sync(0xffffffffu, nan);
+    if (lane < k) l = look ? lg[e] : few_key_value(mine);
   } else {
     int bad = 0;
     if (e < 0 || e >= E) {
       bad = DERR_INDEX;
       e = 0;
     }
+    if (lane < k) l = lg[e];
     const unsigned same = __match_any_sync(0xffffffffu, lane < k ? e : -1 - lane);
     if (same & (same - 1)) bad |= DERR_DUP;
     if (say && lane < k && bad && A.err) atomicOr(A.err, bad);
   }
-  const float l = lane < k ? lg[e] : -INFINITY;
   float mx = l;
 #pragma unroll
   for (int o = kMaxK / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -481,7 +497,7 @@ __device__ __forceinline__ void few_route_share(const FewArgs &A) {
   const int lane = threadIdx.x & 31;
   if (threadIdx.x >= 32) return;
   for (int t = blockIdx.x; t < A.T; t += gridDim.x) {
-    int e;
+    int e = few_given(A, t);
     float g;
     few_route(A, t, true, e, g);
     if (lane < A.k) {
@@ -495,14 +511,15 @@ __device__ __forceinline__ void few_route_share(const FewArgs &A) {
 // of at most 4 tokens, of at most 8, of more.
 constexpr int kFewCost4 = 4, kFewCost8 = 8, kFewCostMore = 14;
 
-__device__ __forceinline__ void few_plan(const FewArgs &A, FewPlan &P) {
+// given: few_given of the token that has the warp's number
+__device__ __forceinline__ void few_plan(const FewArgs &A, FewPlan &P, int given) {
   const int tid = threadIdx.x, lane = tid & 31, warp = warp_id();
   const int k = A.k, T = A.T, E = A.E;
   static_assert(kFewMaxT * kMaxK <= kFewThreads && kMaxE < kFewThreads, "an assignment, an expert a thread");
   if (tid < kMaxE) P.tok[tid] = 0;
   if (T <= kFewRouteAll) {
     if (warp < T) {
-      int e;
+      int e = given;
       float g;
       few_route(A, warp, blockIdx.x == 0, e, g);
       if (lane < k) {
@@ -676,16 +693,17 @@ __device__ __noinline__ void few_join(const FewPlan &P, int s, int i8, int wk, i
 }
 
 // Streams a warp's tiles, blocks ahead across the end of a tile too.  Down: rows r0.. (nr of
-// them), `depth` stages (2 to 4).  Sums go through few_emit / few_join, or (down) to
+// them).  Sums go through few_emit / few_join, or (down) to
 // out[place][16].
 template <bool GU, bool WIDE, int N>
 __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, const FewOps &O, int p0, FewCursor<GU> C,
-                                           int step, int per, const FewPart &W, int r0, int nr, int depth, uint32_t zero,
+                                           int step, int per, const FewPart &W, int r0, int nr, uint32_t zero,
                                            uint32_t ring, float *out) {
   if (C.left <= 0) return;
   constexpr int TOK = N * (WIDE ? 8 : 4), STAGE = GU ? kFewStage : few_dn_stage(TOK);
   const int lane = threadIdx.x & 31, t = lane & 3, r = lane >> 2, warp = warp_id();
-  const int K = GU ? A.d : A.I, stages = GU ? kFewDepth : depth;
+  constexpr int stages = GU ? kFewDepth : few_dn_depth(TOK);
+  const int K = GU ? A.d : A.I;
   const uint32_t slots = ring, slots_end = slots + stages * kFewSlot;     // of scales, then the stages
   const uint32_t stages_at = slots_end, end = stages_at + stages * STAGE;
   const int cs = K % 512 == 0 ? 4 : K % 256 == 0 ? 2 : 1;                 // 128 channels to a slot
@@ -788,7 +806,7 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
     }
 #pragma unroll 1
     for (int b = W.b0; b < W.b1; b++) {
-      if (GU) cp_async_wait_but<kFewDepth - 2>(); else cp_async_wait_upto(depth - 2);
+      cp_async_wait_but<stages - 2>();
       __syncwarp();                       // the block has arrived, and every lane has left the one before
       issue();
       const int at128 = (GU ? 2 * b : b) & (cs - 1);
@@ -803,8 +821,9 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
         X.advance(X.step);
       } else {
         FewCol<WIDE, N> Y = X;            // the stage's own columns
+        const uint32_t xbase = X.step ? st : 0u;
 #pragma unroll
-        for (int q = 0; q < N; q++) Y.x[q] = X.step ? X.x[q] + st : zero;
+        for (int q = 0; q < N; q++) Y.x[q] = X.x[q] + xbase;
         few_mul128<WIDE, N, 512>(st + o0, st + o1, lds32u(sc), lds32u(sc + 16), lds32u(sc + 256), lds32u(sc + 272), Y, code, acc);
         X.advance(0);
       }
@@ -914,15 +933,15 @@ __device__ __forceinline__ void few_phase2(const FewArgs &A, const FewPlan &P, u
     FewPart W;
     if (n8 < s1) {
       const int step = share(n8, P.nseg, C, W);
-      few_stream<true, true, 2>(A, P, O, p0, C, step, per, W, 0, 0, 0, zero, ring, red);
+      few_stream<true, true, 2>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
     }
     if (n4 < s1 && s0 < n8) {
       const int step = share(n4, n8, C, W);
-      few_stream<true, false, 2>(A, P, O, p0, C, step, per, W, 0, 0, 0, zero, ring, red);
+      few_stream<true, false, 2>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
     }
     if (s0 < n4) {
       const int step = share(0, n4, C, W);
-      few_stream<true, false, 1>(A, P, O, p0, C, step, per, W, 0, 0, 0, zero, ring, red);
+      few_stream<true, false, 1>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
     }
     s0 = s1;
   }
@@ -985,14 +1004,24 @@ __device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, u
       }
       const int p0 = P.seg_at[s0], p1 = P.seg_at[s1];
       __syncthreads();
-      const int split = A.Ad && first ? few_td(A, td) : 0;
-      // sums by group of 64 of the tiles' sums (u / G by its reciprocal: u < 2^16)
+      // sums by group of 64 of the tiles' sums (u / G by its reciprocal: u < 2^16); a thread's first
+      // is on its way while t_d is formed
       const uint32_t rg = 0xFFFFFFFFu / G + 1;
-#pragma unroll 4
-      for (int u = tid; u < (p1 - p0) * G; u += kFewThreads) {
+      const int nsum = (p1 - p0) * G;
+      auto tile_sums = [&](int u, float4 &v, float4 &w) {
         const int p = __umulhi(u, rg), g = u - p * G;
         const float4 *q = reinterpret_cast<const float4 *>(A.a8 + (size_t)P.asg[p0 + p] * (A.I / 8) + g * 8);
-        const float4 v = q[0], w = q[1];
+        v = q[0];
+        w = q[1];
+      };
+      float4 v0, w0;
+      if (tid < nsum) tile_sums(tid, v0, w0);
+      const int split = A.Ad && first ? few_td(A, td) : 0;
+      if (tid < nsum) sums[tid] = ((v0.x + v0.y) + (v0.z + v0.w)) + ((w0.x + w0.y) + (w0.z + w0.w));
+#pragma unroll 4
+      for (int u = tid + kFewThreads; u < nsum; u += kFewThreads) {
+        float4 v, w;
+        tile_sums(u, v, w);
         sums[u] = ((v.x + v.y) + (v.z + v.w)) + ((w.x + w.y) + (w.z + w.w));
       }
       __syncthreads();
@@ -1010,10 +1039,9 @@ __device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, u
       const FewOps O{kFewDnHead, smem_at(sums), kFewDnRow, G * 4};
       const int m4 = max(s0, min(s1, P.n4)), m8 = max(m4, min(s1, P.n8));
       auto cursor = [&](int a, int b) { return FewCursor<false>{a + team, 0, (b - a - team + step - 1) >> (4 - lg)}; };
-      auto depth = [&](int tokens) { return min(4, A.dn_ring / (few_dn_stage(tokens) + kFewSlot)); };
-      if (m8 < s1) few_stream<false, true, 2>(A, P, O, p0, cursor(m8, s1), step, 0, W, r0, nr, depth(16), zero, ring, o);
-      if (m4 < m8) few_stream<false, false, 2>(A, P, O, p0, cursor(m4, m8), step, 0, W, r0, nr, depth(8), zero, ring, o);
-      if (s0 < m4) few_stream<false, false, 1>(A, P, O, p0, cursor(s0, m4), step, 0, W, r0, nr, depth(4), zero, ring, o);
+      if (m8 < s1) few_stream<false, true, 2>(A, P, O, p0, cursor(m8, s1), step, 0, W, r0, nr, zero, ring, o);
+      if (m4 < m8) few_stream<false, false, 2>(A, P, O, p0, cursor(m4, m8), step, 0, W, r0, nr, zero, ring, o);
+      if (s0 < m4) few_stream<false, false, 1>(A, P, O, p0, cursor(s0, m4), step, 0, W, r0, nr, zero, ring, o);
       s0 = s1;
     }
     __syncthreads();
@@ -1063,6 +1091,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_moe_few(const __grid_constan
   if (threadIdx.x < sizeof(FewArgs) / 4)
     reinterpret_cast<uint32_t *>(&P.args)[threadIdx.x] = reinterpret_cast<const uint32_t *>(&A)[threadIdx.x];
   cooperative_groups::grid_group grid = cooperative_groups::this_grid();
+  const int given = few_given(A, threadIdx.x >> 5);
   few_phase1(A, P, rings, red);
   grid.sync();
   if (A.h_out) few_residual(A, rings);
@@ -1070,7 +1099,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_moe_few(const __grid_constan
     few_route_share(A);
     grid.sync();
   }
-  few_plan(A, P);
+  few_plan(A, P, given);
   few_phase2(A, P, area, smem_at(zero), ring, red);
   grid.sync();
   few_phase3(A, P, red_area, smem_at(zero));
