@@ -198,7 +198,9 @@ class _Torch:
         self.int8, self.e4m3 = torch.int8, torch.float8_e4m3fn
         self.act = {self.bf16: ACT_BF16, self.int8: ACT_INT8, self.e4m3: ACT_E4M3}
         self.empty, self.on_device, self.on_stream = torch.empty, torch.cuda.device, torch.cuda.stream
-        self.current_stream, self.current_device = torch.cuda.current_stream, torch.cuda.current_device
+        self.current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        L = lib()
+        self.add_rmsnorm, self.int4_linear, self.moe_layer_few = L.e0_add_rmsnorm, L.e0_int4_linear, L.e0_moe_layer_few
         # the handle of a device's current stream, without an object around it
         self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -261,10 +263,9 @@ def _few_workspace(dims, T, device, stream=None):
     return _empty(n.value, _torch().u8, device, stream)
 
 
-def _call(dev, stream, fn, *args):
+def _call(X, dev, stream, fn, *args):
     """Call a library function that enqueues on `stream` (default: the current one of device
     `dev`) with that device current."""
-    X = _torch()
     if dev < 0:
         raise ValueError("CUDA tensors are needed")
     raw = X.raw_stream(dev) if stream is None else stream.cuda_stream
@@ -292,14 +293,27 @@ def add_rmsnorm(h, norm_w, delta=None, eps=1e-6, h_out=None, x=None, q8=None, q8
     hp, hs = _rows(h, "h", shape, d, bf16, dev)
     if h_out is None and x is None and q8 is None:
         x = _empty(shape, bf16, h.device, stream)
+    # (whole tensors of the right kind, as nearly every call has them, are told apart here; _rows
+    # takes or refuses the others)
     dp = ds = f32 = op = os_ = xp = xs = qp = qs = fmt = sp = 0
     if delta is not None:
         f32 = delta.dtype is X.f32
-        dp, ds = _rows(delta, "delta", shape, d, X.f32 if f32 else bf16, dev)
+        if (f32 or delta.dtype is bf16) and delta.shape == shape and delta.get_device() == dev and delta.is_contiguous():
+            dp, ds = delta.data_ptr(), d
+        else:
+            dp, ds = _rows(delta, "delta", shape, d, X.f32 if f32 else bf16, dev)
     if h_out is not None:
-        op, os_ = _rows(h_out, "h_out", shape, d, bf16, dev)
+        if h_out is h:
+            op, os_ = hp, hs
+        elif h_out.dtype is bf16 and h_out.shape == shape and h_out.get_device() == dev and h_out.is_contiguous():
+            op, os_ = h_out.data_ptr(), d
+        else:
+            op, os_ = _rows(h_out, "h_out", shape, d, bf16, dev)
     if x is not None:
-        xp, xs = _rows(x, "x", shape, d, bf16, dev)
+        if x.dtype is bf16 and x.shape == shape and x.get_device() == dev and x.is_contiguous():
+            xp, xs = x.data_ptr(), d
+        else:
+            xp, xs = _rows(x, "x", shape, d, bf16, dev)
     if q8 is not None:
         fmt = _act_format(q8)
         if fmt == ACT_BF16:
@@ -309,10 +323,13 @@ def add_rmsnorm(h, norm_w, delta=None, eps=1e-6, h_out=None, x=None, q8=None, q8
         groups = -(-d // q8_group) if q8_group else 1
         if q8_scale is None:
             q8_scale = _empty((T, groups), X.f32, h.device, stream)
-        qp, qs = _rows(q8, "q8", shape, d, q8.dtype, dev)
+        if q8.shape == shape and q8.get_device() == dev and q8.is_contiguous():
+            qp, qs = q8.data_ptr(), d
+        else:
+            qp, qs = _rows(q8, "q8", shape, d, q8.dtype, dev)
         sp = _flat(q8_scale, "q8_scale", (T, groups), X.f32, dev)
-    _call(dev, stream, lib().e0_add_rmsnorm, hp, hs, dp, f32, ds, _flat(norm_w, "norm_w", (d,), bf16, dev), eps, T, d, op,
-          os_, xp, xs, qp, fmt, qs, q8_group, sp)
+    _call(X, dev, stream, X.add_rmsnorm, hp, hs, dp, f32, ds, _flat(norm_w, "norm_w", (d,), bf16, dev), eps, T, d, op, os_, xp, xs,
+          qp, fmt, qs, q8_group, sp)
     return h_out, x, q8, q8_scale
 
 
@@ -358,7 +375,7 @@ class Int4Linear:
             y = _empty((T, n), X.bf16, self.device, stream)
         f32 = y.dtype is X.f32
         yp, ys = _rows(y, "y", (T, n), n, X.f32 if f32 else X.bf16, dev)
-        _call(dev, stream, lib().e0_int4_linear, self._ref, xp, fmt, xs, sp, x_group, T, yp, f32, ys)
+        _call(X, dev, stream, X.int4_linear, self._ref, xp, fmt, xs, sp, x_group, T, yp, f32, ys)
         return y
 
 
@@ -396,7 +413,7 @@ def _moe_layer_few(dims, layer, h, delta, route_idx, h_out, y, y_f32, idx, gates
         y = _empty(shape, bf16, h.device, stream)
     if workspace is None:
         workspace = _few_workspace(dims, T, h.device, stream)
-    _call(dev, stream, lib().e0_moe_layer_few, ctypes.byref(dims), ctypes.byref(layer), hp,
+    _call(X, dev, stream, X.moe_layer_few, ctypes.byref(dims), ctypes.byref(layer), hp,
           _flat(delta, "delta", shape, bf16, dev), T, _flat(route_idx, "route_idx", per_k, i32, dev),
           _flat(h_out, "h_out", shape, bf16, dev), _flat(y, "y", shape, bf16, dev), _flat(y_f32, "y_f32", shape, f32, dev),
           _flat(idx, "idx", per_k, i32, dev), _flat(gates, "gates", per_k, f32, dev),
