@@ -208,6 +208,18 @@ def test_add_rmsnorm_sum_borders():
     run_norm(h, gamma, delta.to(BF16), 1e-6, None, 0)
 
 
+def test_add_rmsnorm_rows_farther_apart_than_32_bits():
+    import int4_expert_streaming_prerouter_b200 as e0
+    h, gamma, dl = stream_like(2, 256, 15)
+    big = torch.empty((2, (1 << 31) + 64), dtype=BF16, device="cuda")
+    big[:, :256] = h
+    big[:, 512:768] = dl.to(BF16)
+    out = e0.add_rmsnorm(big[:, :256], gamma, delta=big[:, 512:768], h_out=big[:, :256], x=big[:, 1024:1280])
+    h1, x, _, _ = norm_ref(f64(h), f64(gamma), f64(dl.to(BF16)), np.float64(np.float32(1e-6)), None, 0)
+    same(f64(out[0]), h1)
+    same(f64(out[1]), x)
+
+
 def test_add_rmsnorm_of_no_rows():
     import int4_expert_streaming_prerouter_b200 as e0
     e0.add_rmsnorm(torch.empty((0, 64), dtype=BF16, device="cuda"), torch.ones(64, dtype=BF16, device="cuda"))
@@ -374,6 +386,58 @@ def test_int4_linear_rows_apart():
             assert (yb == 5.0).all()
 
 
+def test_int4_linear_slices_of_matrices():
+    """Rows cut out of wider matrices: scales and mins then begin at any even address."""
+    import int4_expert_streaming_prerouter_b200 as e0
+    for K, g in ((512, 64), (256, 128), (192, 64)):
+        m = int4_mat(50, K, g, 11, r=8)
+        x, _, xv = acts(5, K, "bf16", 0, 12)
+        for lo, hi in ((1, 50), (3, 20), (7, 8)):
+            cut = {n: t[lo:hi] if n != "lora_A" else t for n, t in m.items()}
+            y = torch.empty((5, hi - lo), dtype=F32, device="cuda")
+            e0.Int4Linear(**cut)(x, y=y)
+            check_linear(y, *linear_ref(cut, g, xv))
+
+
+def test_int4_linear_longest_rows_and_largest_matrix():
+    """k = 2^18; codes past 2^31 bytes, whose last rows are looked at."""
+    import int4_expert_streaming_prerouter_b200 as e0
+    for T, K in ((1, 1 << 18), (9, 1 << 18)):
+        m = int4_mat(9, K, 64, 21)
+        x, _, xv = acts(T, K, "bf16", 0, 22)
+        y = torch.empty((T, 9), dtype=F32, device="cuda")
+        e0.Int4Linear(**m)(x, y=y)
+        check_linear(y, *linear_ref(m, 64, xv))
+    N, K = 70001, 65536
+    m = {"codes": torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device="cuda"),
+         "scale": torch.rand((N, K // 128), device="cuda").to(BF16), "min": torch.randn((N, K // 128), device="cuda").to(BF16)}
+    x, _, xv = acts(2, K, "bf16", 0, 23)
+    y = torch.empty((2, N), dtype=F32, device="cuda")
+    e0.Int4Linear(**m)(x, y=y)
+    for rows in (slice(0, 8), slice(N - 20, N)):
+        check_linear(y[:, rows], *linear_ref({n: t[rows] for n, t in m.items()}, 128, xv))
+
+
+def test_int4_linear_captured_at_its_first_call():
+    """A shape whose blocks form clusters (32 tokens of a long k), first seen inside a capture, and
+    replayed on other activations."""
+    import int4_expert_streaming_prerouter_b200 as e0
+    m = int4_mat(300, 4096, 128, 31, r=16)
+    lin = e0.Int4Linear(**m)
+    x, s, xv = acts(29, 4096, "int8", 128, 32)
+    y = torch.empty((29, 300), dtype=F32, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lin(x, x_scale=s, y=y)
+    for seed in (33, 34):
+        x2, s2, xv = acts(29, 4096, "int8", 128, seed)
+        x.copy_(x2)
+        s.copy_(s2)
+        graph.replay()
+        check_linear(y, *linear_ref(m, 128, xv))
+
+
 def test_int4_linear_of_no_tokens():
     import int4_expert_streaming_prerouter_b200 as e0
     y = e0.Int4Linear(**int4_mat(5, 64, 64, 1))(torch.empty((0, 64), dtype=BF16, device="cuda"))
@@ -475,6 +539,43 @@ def test_moe_few_given_routing(T, kind):
     elif kind == "own rows":
         route[:] = -1
     check_few(SMALL, 44, T, route=route, hseed=T)
+
+
+def test_moe_few_experts_past_32_bits():
+    """2.8 GB of experts of the widest dims; the last ones are chosen."""
+    import int4_expert_streaming_prerouter_b200 as e0
+    d = I = 4096
+    E, T, k = 100, 3, 2
+    size = synth.blob_bytes(d, I)
+    blobs = torch.randint(0, 256, (E + 1, size), dtype=torch.uint8, device="cuda")
+    for name, off, n, shape, dt in synth.blob_sections(d, I):
+        if not name.endswith("codes"):
+            v = torch.rand((E + 1, n // 2), device="cuda")
+            blobs[:, off:off + n] = (v * 0.015 + 0.005 if name.endswith("scale") else v * 0.2 - 0.1).to(BF16).view(torch.uint8)
+    h = bf16_tensor(synth.hidden(16, 0, 1, T, d)[0], "cuda")
+    ly = {"experts": blobs[:E], "shared": blobs[E], "router_w": (torch.randn((E, d), device="cuda") * 0.02).to(BF16),
+          "norm_w": torch.ones(d, dtype=BF16, device="cuda")}
+    route = torch.tensor([[99, 0], [98, 99], [76, 77]], dtype=torch.int32, device="cuda")
+    y, gates = torch.empty((T, d), device="cuda"), torch.empty((T, k), device="cuda")
+    e0.MoeLayer(e0.make_dims(d, E, I, k, 0), ly).few(h, route_idx=route, y_f32=y, gates=gates)
+    x = torch.from_numpy(O.rmsnorm(f64(h), bits_of(ly["norm_w"]), np.float64(np.float32(1e-6)))).cuda()
+
+    def ffn(blob, v):
+        m = {}
+        for name, off, n, shape, dt in synth.blob_sections(d, I):
+            p, part = name.split(".")
+            b = blob[off:off + n].clone()
+            m[p, part] = b.view(*shape) if part == "codes" else b.view(BF16).view(*shape).double().repeat_interleave(64, 1)
+
+        def w(p):
+            c = m[p, "codes"]
+            return torch.stack([c & 15, c >> 4], -1).flatten(1).double() * m[p, "scale"] + m[p, "min"]
+        g, u = w("gate") @ v, w("up") @ v
+        a = torch.from_numpy(O.round_bf16((g / (1 + torch.exp(-g)) * u).cpu().numpy())).cuda()
+        return w("down") @ a
+    for t in range(T):
+        ref = ffn(blobs[E], x[t]) + sum(gates[t, j].double() * ffn(blobs[int(route[t, j])], x[t]) for j in range(k))
+        check_y(f64(y[t]), f64(ref), f"token {t}")
 
 
 def test_moe_few_ties_go_to_the_lower_index():
