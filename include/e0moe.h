@@ -338,8 +338,10 @@ typedef struct {
  *           scale a row): as e0_add_rmsnorm writes them.
  * y         [T, n] bf16 (y_f32 = 0) or fp32 (1), rows y_stride elements apart; must not
  *           overlap the inputs.
- * Any n; any T up to 524,280, but made for few tokens: the weights are read once per 32 of
- * them.  codes and lora_A are 16-byte aligned.  T = 0 does nothing.
+ * n up to 2^26, k up to 2^18, T up to 524,280, but made for few tokens: the weights are read
+ * once per 32 of them (fewer where 32 rows of k do not fit a cluster's shared memory).  codes
+ * and lora_A are 16-byte aligned; scale and min may begin anywhere, and are read fastest where
+ * their rows begin at 16 bytes.  T = 0 does nothing.
  * Errors: INVALID_ARG, CUDA. */
 int e0_int4_linear(const e0_int4_mat *w, const void *x, int x_format, long long x_stride, const float *x_scale,
                    int x_group, int T, void *y, int y_f32, long long y_stride, void *stream);
@@ -350,7 +352,8 @@ int e0_int4_linear(const e0_int4_mat *w, const void *x, int x_format, long long 
  * h         [T, d] bf16;  delta [T, d] bf16 or NULL.
  * route_idx NULL, or [T, k] int32 device: a row whose first entry is negative uses the
  *           layer's own router.
- * h_out     [T, d] bf16 or NULL: h'; may be h or delta.
+ * h_out     [T, d] bf16 or NULL: h'; may be h or delta.  Other overlaps of outputs with
+ *           inputs or one another are not allowed.
  * y_bf16    [T, d] bf16 (required);  y_f32 [T, d] fp32 or NULL;  idx_out [T, k] int32 or
  *           NULL;  gate_out [T, k] fp32 or NULL.
  * workspace device memory of the size that e0_moe_layer_few_workspace gives for (dims, T),
