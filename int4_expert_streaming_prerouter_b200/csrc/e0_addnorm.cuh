@@ -25,6 +25,7 @@ struct AddNormArgs {
   const uint16_t *gamma;
   float eps;
   int T, d;
+  double inv_d;
   uint16_t *h_out;
   long long h_out_stride;
   uint16_t *x;
@@ -242,11 +243,11 @@ __global__ void __launch_bounds__(addnorm_threads(V)) k_add_rmsnorm(const __grid
   if (nwarp > 1) {
     if (lane == 0) red[tid >> 5] = ss;
     __syncthreads();
-    ss = 0.0;
-#pragma unroll 4
-    for (int w = 0; w < nwarp; w++) ss += red[w];       // the same order on every thread
+    // the same order on every thread: lane by lane over the warps, at most 32
+    ss = lane < nwarp ? red[lane] : 0.0;
+    ss = warp_sum(ss);
   }
-  const double rinv = rsqrt(ss / d + (double)A.eps);
+  const double rinv = rsqrt(fma(ss, A.inv_d, (double)A.eps));
   const float rinv_f = (float)rinv;
   uint32_t gm[V], rowmax = 0;
 #pragma unroll

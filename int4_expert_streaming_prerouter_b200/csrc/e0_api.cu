@@ -2069,7 +2069,7 @@ extern "C" int e0_add_rmsnorm(const void *h, long long h_stride, const void *del
   AddNormArgs A{};
   A.h = (const uint16_t *)h; A.h_stride = h_stride;
   A.delta = delta; A.delta_f32 = delta_f32; A.delta_stride = delta_stride;
-  A.gamma = (const uint16_t *)norm_w; A.eps = eps; A.T = T; A.d = d;
+  A.gamma = (const uint16_t *)norm_w; A.eps = eps; A.T = T; A.d = d; A.inv_d = 1.0 / d;
   A.h_out = (uint16_t *)h_out; A.h_out_stride = h_out_stride;
   A.x = (uint16_t *)x; A.x_stride = x_stride;
   A.q8 = (uint8_t *)q8; A.q8_stride = q8_stride; A.q8_e4m3 = q8_format == E0_ACT_E4M3; A.q8_group = q8_group;
@@ -2294,7 +2294,7 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
   A.Bu = (const uint16_t *)Y.lora_Bu; A.Ad = (const uint16_t *)Y.lora_Ad; A.Bd = (const uint16_t *)Y.lora_Bd;
   A.bl = blob_of(D.d_model, D.d_ff);
   A.T = T; A.d = D.d_model; A.E = D.n_experts; A.I = D.d_ff; A.k = D.top_k; A.r = D.lora_rank;
-  A.eps = D.rms_eps; A.c = D.lora_scale; A.route = route_idx;
+  A.inv_d = 1.0 / D.d_model; A.eps = D.rms_eps; A.c = D.lora_scale; A.route = route_idx;
   A.h_out = (uint16_t *)h_out; A.y = (uint16_t *)y_bf16; A.yf = y_f32; A.idx = idx_out; A.gates = gate_out;
   uint8_t *ws = (uint8_t *)workspace;
   A.xb = (uint16_t *)(ws + S.xb); A.logits = (float *)(ws + S.logits); A.lt = (float *)(ws + S.lt);

@@ -54,6 +54,7 @@ struct FewArgs {
   const uint16_t *Ag, *Bg, *Au, *Bu, *Ad, *Bd;
   Blob bl;
   int T, d, E, I, k, r;
+  double inv_d;
   float eps, c;
   const int32_t *route;
   uint16_t *h_out, *y;
@@ -180,8 +181,7 @@ struct FewCol {
 
 // Pair i of a word's 8 codes as 128 + q, in operand order: one shift and one three-input operation.
 // Mask and offset come from registers: given as constants, they become two operations, since an
-// instruction holds one (the integer pipe is what bounds the products: 179 instructions and 58 us
-// instead of 147 and 47 in phase 2 at 64 tokens).
+// instruction holds one (142 against 138 us at 64 tokens: the integer pipe is what bounds the products).
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i, const FewCode &K) {
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * i)), "r"(K.mask), "r"(K.offset));
@@ -374,10 +374,10 @@ __device__ __forceinline__ void few_phase1(const FewArgs &A, FewPlan &P, uint8_t
   if (lane == 0) P.part[warp] = ss;
   __syncthreads();
   if (mine) {
-    ss = 0.0;
-#pragma unroll 2
-    for (int w = 0; w < wpt; w++) ss += P.part[tok * wpt + w];
-    const double rinv = rsqrt(ss / d + (double)A.eps);
+    // (lanes l, l + wpt, ... hold the same: a butterfly over wpt of them)
+    ss = P.part[tok * wpt + (lane & (wpt - 1))];
+    for (int o = wpt >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const double rinv = rsqrt(fma(ss, A.inv_d, (double)A.eps));
     const float rinv_f = (float)rinv;
 #pragma unroll 1
     for (int c = c0; c < d; c += wpt * 256) {
