@@ -517,15 +517,17 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
 #pragma unroll 1
   for (int lo = row_lo; lo < row_hi; lo += pass) {
     const int hi = min(lo + pass, row_hi);
-    begin(lo, hi);                        // the first weights are on their way while the activations come
+    if (lo > row_lo) begin(lo, hi);
     if (lo == row_lo) {
       // ---- the activations of this block's channels, zeros behind the last: a warp takes 256 of a
-      // token, 8 lanes to a group of 64; four of them are under way at once
+      // token, 8 lanes to a group of 64; four of them are under way at once, the first four before
+      // the weights
       {
         const int i = lane & 7;
-        int ct = warp / NB1, cb = warp - ct * NB1;
+        int ct = NB > 0 ? warp / NB1 : nt, cb = warp - ct * NB1;
+        bool begun = false;
 #pragma unroll 1
-        while (ct < nt && NB > 0) {
+        do {
           uint4 w[4];
           float s[4];
           int tk[4], gr[4];
@@ -556,6 +558,8 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
               }
             }
           }
+          if (!begun) begin(lo, hi);
+          begun = true;
 #pragma unroll
           for (int j = 0; j < 4; j++) {
             if (tk[j] >= nt) break;                     // (the same for the whole warp)
@@ -563,7 +567,7 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
             else if (L.x_type == ACT_INT8) act_group_int8(make_uint2(w[j].x, w[j].y), s[j], i, tk[j], gr[j], D, true);
             else act_group_e4m3(make_uint2(w[j].x, w[j].y), s[j], i, tk[j], gr[j], D, true);
           }
-        }
+        } while (ct < nt);
       }
       // ---- t = A x of this block's channels, K split over the warps: 16 ranks by 8 tokens at a time
       if (L.A) {
