@@ -2189,7 +2189,7 @@ static int launch_linear(LinearArgs &L, cudaStream_t s) {
 
 template <bool G128>
 static int launch_linear_tokens(LinearArgs &L, cudaStream_t s) {
-  return L.T <= 4 ? launch_linear<false, 1, G128>(L, s) : L.T <= 8 ? launch_linear<false, 2, G128>(L, s)
+  return L.T <= 4 ? launch_linear<false, 1, G128>(L, s) : L.T <= 8 ? launch_linear<true, 1, G128>(L, s)
          : L.T <= 16 ? launch_linear<true, 2, G128>(L, s) : launch_linear<true, 4, G128>(L, s);
 }
 
@@ -2322,7 +2322,9 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
   if (A.gu_rows < 8 || A.dn_rows < std::min(places, A.seg_cap))
     return fail(E0_ERR_INVALID_ARG, "moe_layer_few: dims too large for the shared memory");
   A.code = FewCode{0x000F000Fu, 0x43004300u};
-  A.tpb = T <= 16 ? 1 : T <= 32 ? 2 : 4;
+  // tokens of a block in phase 1: 1, 2 or 4, until a block's share of the rows is 2 or less
+  const int rows = D.n_experts + (any ? 2 * D.lora_rank : 0);
+  for (A.tpb = 1; A.tpb < 4 && (long long)rows * ((T + A.tpb - 1) / A.tpb) > 2 * nsm; A.tpb *= 2) {}
   A.lora16 = !misaligned(Y.lora_Bg, 16) && !misaligned(Y.lora_Bu, 16) && !misaligned(Y.lora_Bd, 16);
   CK(cudaFuncSetAttribute(k_moe_few, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   void *args[] = {&A};
