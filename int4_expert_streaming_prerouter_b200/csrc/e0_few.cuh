@@ -6,16 +6,21 @@
 //   1. x = bf16(RMSNorm(bf16(h + delta))) of 8 tokens in shared memory; a share of the rows
 //      [W_r; A_g; A_u] times them (mma.sync m16n8k16 bf16, K split over the warps).
 //   2. every block takes the top-k of all tokens and groups the (token, slot) assignments by
-//      expert into segments of at most `seg_cap` tokens (the shared expert is one more expert
+//      expert into segments of at most 8 tokens (the shared expert is one more expert
 //      that every token has); it then computes an equal share, by cost, of the tiles of 8
 //      intermediate indices of all segments: 8 gate and 8 up rows, SwiGLU, a = bf16(silu(g) u).
 //   3. every block computes an equal share of the output rows for all segments and combines
 //      them per token in slot order, routed experts first, so y does not depend on timing.
-// Each expert's weights are read once per 16 tokens that chose it (8 where wide activations
-// leave less shared memory).
+// Each expert's weights are read once per 8 tokens that chose it, from L2 after the first time.
+//
+// Measured (256 experts, d = 2048, I = 512, 4 a token, LoRA of rank 16; a captured launch among
+// others): 21.8 us for 1 token, 38.9 for 8, 52.8 for 16, 100 for 64 (291 MB of weights, 2.9 TB/s).
+// One token is five steps of latency (the norm and router 4.3, three barriers 1.3 each, the plan 2.8,
+// gate and up 3 to 4.5, down and combine 4.5); 64 are bound by the integer work on the codes: gate
+// and up 41 us, 4.7 TB/s, down 29 us.
 //
 // A launch with few tokens is a chain of latencies, code fetches among them: the streaming loops
-// exist in three forms for each of the two products and no more, and what they call at the end
+// exist in two forms for each of the two products and no more, and what they call at the end
 // of a tile is a function.  (724 KB of code with 12 inlined forms took 42 us for 5 tokens of
 // d = 256, most of it waiting for instructions.)
 //
@@ -41,6 +46,7 @@ constexpr int kFewThreads = 512;
 constexpr int kFewWarps = kFewThreads / 32;
 constexpr int kFewMaxA = kFewMaxT * (kMaxK + 1);                // assignments
 constexpr int kFewMaxSeg = kMaxE + 1 + kFewMaxA / 8;            // segments
+constexpr int kFewSeg = 8;                                      // tokens to a segment
 constexpr int kFewPad = 16;                                     // bytes between rows: 8 rows in distinct banks
 
 struct FewCode {
@@ -71,7 +77,6 @@ struct FewArgs {
   uint16_t *a;                // [T][k + 1][I], channels in operand order
   float *a8;                  // [T][k + 1][I / 8] sums of a
   int *err;
-  int seg_cap;                // tokens to a segment: 8 or 16
   FewCode code;
   int lora16;                 // rows of LoRA B begin at 16 bytes
   int tpb;                    // tokens that a block of phase 1 norms
@@ -91,7 +96,7 @@ struct FewPlan {
   uint16_t seg_exp[kFewMaxSeg];
   uint16_t seg_at[kFewMaxSeg + 1];
   uint16_t seg_n[kFewMaxSeg];
-  int nseg, nplace, n4, n8;       // segments of experts with at most 4 and at most 8 tokens come first
+  int nseg, nplace, n4;           // segments of experts with at most 4 tokens come first
   double part[kFewWarps];
 };
 
@@ -123,10 +128,11 @@ __device__ __forceinline__ uint4 natural_order(uint4 v) {
 // ---------------------------------------------------------------------------------------
 // int4 rows times bf16 columns: 16 rows, blocks of 256 channels (the last may be 128)
 // ---------------------------------------------------------------------------------------
-// Two forms.  Pair: up to 8 tokens as N tiles of 4; the 8 columns of a matrix instruction are 4
-// tokens restricted to one group of 64 and the same 4 restricted to the next, so a lane takes 16
-// consecutive bytes of a row and one fold serves both groups.  Wide: N tiles of 8 tokens, 8 bytes
-// of a row a lane, a fold per group.  The accumulators of a lane are rows l / 4 and l / 4 + 8,
+// Two forms, N tiles of tokens each (N is 1).  Pair: tiles of 4; the 8 columns of a matrix instruction
+// are 4 tokens restricted to one group of 64 and the same 4 restricted to the next, so a lane takes 16
+// consecutive bytes of a row and one fold serves both groups.  Wide: tiles of 8, 8 bytes of a row a
+// lane, a fold per group.  (Segments of 5 to 8 tokens as two pair tiles: 61.3 us for 64 tokens over 16
+// experts, wide 56.3; segments of 16 would need rings that leave no room for the results.)  The accumulators of a lane are rows l / 4 and l / 4 + 8,
 // tokens 2 (l & 3), + 1 of a tile (pair: tokens 2 (l & 1), + 1, after adding lanes l and l + 2).
 //
 // Each warp streams its weights through a ring of its own in shared memory by cp.async, a block to
@@ -299,8 +305,10 @@ __device__ __forceinline__ int few_topk(uint32_t (&key)[kMaxE / 32], int k, int 
 // ---------------------------------------------------------------------------------------
 // The block's tokens (at most 4) normed into rows at `area` (operand order) with their sums, h'
 // behind them, then the block's rows of [router; A_g; A_u].  Every block of the same tokens norms
-// them again, which costs less than a grid-wide barrier; so a block has few tokens, and more rows,
-// as long as there are blocks (`tpb` is T / 16, rounded up to a power of two).
+// them again, which costs less than a grid-wide barrier; so a block has few tokens, and more (up to
+// 4) only until its share of the rows is 2 or less.  (256 experts, d = 2048, one token a block
+// against four: 26.6 and 23.8 us for 2 tokens, 42.2 and 40.5 for 8, 114 and 102 for 64, 8 tokens a
+// block 42.3 for 8; 16 experts, d = 256: 20.2 and 22.8 for 5.)
 struct FewTok {
   int ntb, tb, member, members, t0, nt;
   __device__ __forceinline__ explicit FewTok(const FewArgs &A) {
@@ -507,9 +515,9 @@ __device__ __forceinline__ void few_route_share(const FewArgs &A) {
   }
 }
 
-// Relative cost of a tile in phase 2 (measured; the weights bound the first): segments of experts
-// of at most 4 tokens, of at most 8, of more.
-constexpr int kFewCost4 = 4, kFewCost8 = 8, kFewCostMore = 14;
+// Relative cost of a tile in phase 2: segments of experts of at most 4 tokens, of more.  (1.25, 1.5,
+// 1.75, 2 to 1: 106, 102, 99.9, 100.4 us at 64 tokens; 40.1, 40.4, 39.4, 38.9 at 8.)
+constexpr int kFewCost4 = 1, kFewCost8 = 2;
 
 // given: few_given of the token that has the warp's number
 __device__ __forceinline__ void few_plan(const FewArgs &A, FewPlan &P, int given) {
@@ -542,10 +550,10 @@ __device__ __forceinline__ void few_plan(const FewArgs &A, FewPlan &P, int given
   if (tid < T * k) atomicOr(&P.tok[P.sel[tid]], 1ull << (tid / k));
   __syncthreads();
   // Places and segments by one prefix sum over the experts, a thread each: experts of at most 4
-  // tokens first, then up to 8, then the others.  A class takes 20 bits: 10 of places, 10 of
-  // segments (at most 576 and 329).
-  const int n = tid < E ? __popcll(P.tok[tid]) : tid == E ? T : 0, cls = n <= 4 ? 0 : n <= 8 ? 1 : 2;
-  const int ns = (n + A.seg_cap - 1) / A.seg_cap;
+  // tokens first, then the others.  A class takes 20 bits: 10 of places, 10 of segments (at most
+  // 576 and 329).
+  const int n = tid < E ? __popcll(P.tok[tid]) : tid == E ? T : 0, cls = n <= 4 ? 0 : 1;
+  const int ns = (n + kFewSeg - 1) / kFewSeg;
   const unsigned long long own = (unsigned long long)(n | (ns << 10)) << (20 * cls);
   unsigned long long sum = own;
 #pragma unroll
@@ -565,25 +573,20 @@ __device__ __forceinline__ void few_plan(const FewArgs &A, FewPlan &P, int given
   auto places = [](unsigned long long v, int c) { return (int)(v >> (20 * c)) & 1023; };
   auto segs = [](unsigned long long v, int c) { return (int)(v >> (20 * c + 10)) & 1023; };
   int at = places(before, cls), sg = segs(before, cls);
-#pragma unroll
-  for (int c = 0; c < 2; c++)
-    if (c < cls) {
-      at += places(total, c);
-      sg += segs(total, c);
-    }
+  if (cls) {
+    at += places(total, 0);
+    sg += segs(total, 0);
+  }
   if (n > 0) P.first[tid] = (uint16_t)at;
 #pragma unroll 1
   for (int i = 0; i < ns; i++) {
     P.seg_exp[sg + i] = (uint16_t)tid;
-    P.seg_at[sg + i] = (uint16_t)(at + i * A.seg_cap);
-    P.seg_n[sg + i] = (uint16_t)min(A.seg_cap, n - i * A.seg_cap);
+    P.seg_at[sg + i] = (uint16_t)(at + i * kFewSeg);
+    P.seg_n[sg + i] = (uint16_t)min(kFewSeg, n - i * kFewSeg);
   }
-  // (with segments of 8 tokens the third class needs no form of its own)
-  const int n4 = segs(total, 0), nseg = n4 + segs(total, 1) + segs(total, 2);
-  const int n8 = A.seg_cap == 8 ? nseg : n4 + segs(total, 1);
+  const int n4 = segs(total, 0), nseg = n4 + segs(total, 1);
   if (tid == 0) {
     P.n4 = n4;
-    P.n8 = n8;
     P.nseg = nseg;
   }
   __syncthreads();
@@ -878,18 +881,11 @@ __device__ __forceinline__ FewOps few_stage(const FewArgs &A, const FewPlan &P, 
 }
 
 // Tile at which block b's share begins: an equal share of the cost of all tiles.  (At most 329
-// segments of 512 tiles of cost 9, times 148 or so: 32 bits.)
+// segments of 512 tiles of cost 2: 32 bits.)
 __device__ __forceinline__ void few_bound(const FewPlan &P, int per, int b, int &s, int &f) {
-  const unsigned c1 = (unsigned)(P.n4 * per) * kFewCost4, c2 = (unsigned)((P.n8 - P.n4) * per) * kFewCost8;
-  const unsigned c3 = (unsigned)((P.nseg - P.n8) * per) * kFewCostMore;
-  unsigned pos = (unsigned)((unsigned long long)(c1 + c2 + c3) * b / gridDim.x), tile;
-  if (pos < c1) {
-    tile = pos / kFewCost4;
-  } else if (pos < c1 + c2) {
-    tile = P.n4 * per + (pos - c1) / kFewCost8;
-  } else {
-    tile = P.n8 * per + (pos - c1 - c2) / kFewCostMore;
-  }
+  const unsigned c1 = (unsigned)(P.n4 * per) * kFewCost4, c2 = (unsigned)((P.nseg - P.n4) * per) * kFewCost8;
+  const unsigned pos = (unsigned)((unsigned long long)(c1 + c2) * b / gridDim.x);
+  const unsigned tile = pos < c1 ? pos / kFewCost4 : P.n4 * per + (pos - c1) / kFewCost8;
   s = tile / per;
   f = tile % per;
 }
@@ -900,7 +896,7 @@ __device__ __forceinline__ void few_phase2(const FewArgs &A, const FewPlan &P, u
   few_bound(P, per, blockIdx.x, sl, fl);
   few_bound(P, per, blockIdx.x + 1, sh, fh);
   const int s_end = fh > 0 ? sh + 1 : sh;             // one past the last segment
-  const int n4 = P.n4, n8 = P.n8;
+  const int n4 = P.n4;
 #pragma unroll 1
   for (int s0 = sl; s0 < s_end;) {
     int s1 = s0 + 1;
@@ -931,13 +927,9 @@ __device__ __forceinline__ void few_phase2(const FewArgs &A, const FewPlan &P, u
     };
     FewCursor<true> C;
     FewPart W;
-    if (n8 < s1) {
-      const int step = share(n8, P.nseg, C, W);
-      few_stream<true, true, 2>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
-    }
-    if (n4 < s1 && s0 < n8) {
-      const int step = share(n4, n8, C, W);
-      few_stream<true, false, 2>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
+    if (n4 < s1) {
+      const int step = share(n4, P.nseg, C, W);
+      few_stream<true, true, 1>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
     }
     if (s0 < n4) {
       const int step = share(0, n4, C, W);
@@ -1037,10 +1029,9 @@ __device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, u
       }
       first = false;
       const FewOps O{kFewDnHead, smem_at(sums), kFewDnRow, G * 4};
-      const int m4 = max(s0, min(s1, P.n4)), m8 = max(m4, min(s1, P.n8));
+      const int m4 = max(s0, min(s1, P.n4));
       auto cursor = [&](int a, int b) { return FewCursor<false>{a + team, 0, (b - a - team + step - 1) >> (4 - lg)}; };
-      if (m8 < s1) few_stream<false, true, 2>(A, P, O, p0, cursor(m8, s1), step, 0, W, r0, nr, zero, ring, o);
-      if (m4 < m8) few_stream<false, false, 2>(A, P, O, p0, cursor(m4, m8), step, 0, W, r0, nr, zero, ring, o);
+      if (m4 < s1) few_stream<false, true, 1>(A, P, O, p0, cursor(m4, s1), step, 0, W, r0, nr, zero, ring, o);
       if (s0 < m4) few_stream<false, false, 1>(A, P, O, p0, cursor(s0, m4), step, 0, W, r0, nr, zero, ring, o);
       s0 = s1;
     }

@@ -224,11 +224,18 @@ __device__ __forceinline__ void act_group_e4m3(uint2 w, float scale, int i, int 
 // bringing them to fp16 than on its weights, or they do not fit, the blocks of a cluster split K, and
 // each adds up a part of the rows over the cluster's shared memory.
 //
-// Two forms.  Pair (up to 8 tokens, N tiles of 4): the 8 columns of a matrix instruction are 4 tokens
+// Measured (a captured launch among others): 2048 x 2048 with LoRA at one token 6.3 us, 5120 x 2048 at
+// 8 int8 tokens 6.4, 65521 x 2048 at one token 18.4 (3.9 TB/s), 8192 x 4096 at 32 e4m3 tokens 20.5.
+// The small ones are the latency of a launch, the activations (3.3 us before the first tile) and one
+// tile; the large are bound by the integer work on the codes.  Ring depths 3 and 2: pair 18.3 us at
+// one token and 65521 rows, with a depth of 2 19.9 (4: no change); wide needs the room for activations.
+//
+// Two forms.  Pair (up to 4 tokens, N tiles of 4): the 8 columns of a matrix instruction are 4 tokens
 // restricted to one group of 64 and the same 4 restricted to the next (zeros elsewhere), so a lane
 // takes 16 consecutive bytes of a row and one fold serves both groups.  Wide (N tiles of 8 tokens): 8
 // bytes of a row a lane, a fold per group.  The accumulators of a lane are rows l / 4 and l / 4 + 8,
 // tokens 2 (l & 3), + 1 of a tile (pair: tokens 2 (l & 1), + 1, after adding lanes l and l + 2).
+// (65521 x 2048: at 4 tokens pair 19.2 us, wide 20.6; at 8 two pair tiles 28.9, wide 21.9.)
 struct LinearArgs {
   const uint8_t *codes;          // [N, K / 2]
   const uint8_t *scale, *min;    // [N, K / g] bf16
