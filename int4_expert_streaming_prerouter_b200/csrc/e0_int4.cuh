@@ -227,7 +227,8 @@ __device__ __forceinline__ void act_group_e4m3(uint2 w, float scale, int i, int 
 // Measured (a captured launch among others): 2048 x 2048 with LoRA at one token 6.3 us, 5120 x 2048 at
 // 8 int8 tokens 6.4, 65521 x 2048 at one token 18.4 (3.9 TB/s), 8192 x 4096 at 32 e4m3 tokens 20.5.
 // The small ones are the latency of a launch, the activations (3.3 us before the first tile) and one
-// tile; the large are bound by the integer work on the codes.  Ring depths 3 and 2: pair 18.3 us at
+// tile; 65521 rows by the weights and the wait for the first activations; 32 tokens by shared-memory
+// reads and the matrix instructions.  Ring depths 3 and 2: pair 18.3 us at
 // one token and 65521 rows, with a depth of 2 19.9 (4: no change); wide needs the room for activations.
 //
 // Two forms.  Pair (up to 4 tokens, N tiles of 4): the 8 columns of a matrix instruction are 4 tokens
