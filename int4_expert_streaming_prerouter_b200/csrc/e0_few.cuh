@@ -241,7 +241,8 @@ __device__ __forceinline__ void few_mul128(uint32_t w0, uint32_t w1, uint32_t ws
     }
   } else {
     const uint4 wa = lds128(w0), wb = lds128(w0 + HALF);
-    // (one tile of tokens: two chains of dependent instructions, joined at the fold)
+    // (two chains of dependent instructions, joined at the fold)
+    static_assert(WIDE || N == 1, "one tile of tokens");
     float p[N][4], p2[4];
 #pragma unroll
     for (int w = 0; w < 4; w++) {
@@ -254,14 +255,12 @@ __device__ __forceinline__ void few_mul128(uint32_t w0, uint32_t w1, uint32_t ws
         const uint4 x = lds128(X.x[q] + w * 16);
         if (w == 0) mma_bf16_first(p[q], a0, b0, a1, b1, x.x, x.y);
         else mma_bf16_acc(p[q], a0, b0, a1, b1, x.x, x.y);
-        if (N > 1) mma_bf16_acc(p[q], a2, b2, a3, b3, x.z, x.w);
-        else if (w == 0) mma_bf16_first(p2, a2, b2, a3, b3, x.z, x.w);
+        if (w == 0) mma_bf16_first(p2, a2, b2, a3, b3, x.z, x.w);
         else mma_bf16_acc(p2, a2, b2, a3, b3, x.z, x.w);
       }
     }
-    if (N == 1)
 #pragma unroll
-      for (int i = 0; i < 4; i++) p[0][i] += p2[i];
+    for (int i = 0; i < 4; i++) p[0][i] += p2[i];
     few_fold<N>(p, wsa, wma, wsb, wmb, t >> 1 ? 0x3244u : 0x1044u, X.v0, X.v1, 0, acc);
   }
 }

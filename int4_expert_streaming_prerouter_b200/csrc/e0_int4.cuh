@@ -350,7 +350,8 @@ __device__ __forceinline__ void lin_mul128(uint32_t w0, uint32_t w1, uint32_t ws
     }
   } else {
     const uint4 wa = lds128(w0), wb = lds128(w0 + 1024);
-    // (one tile of tokens: two chains of dependent instructions, joined at the fold)
+    // (two chains of dependent instructions, joined at the fold)
+    static_assert(WIDE || N == 1, "one tile of tokens");
     float p[N][4], p2[4];
 #pragma unroll
     for (int w = 0; w < 4; w++) {
@@ -362,14 +363,12 @@ __device__ __forceinline__ void lin_mul128(uint32_t w0, uint32_t w1, uint32_t ws
         const uint4 x = lds128(X.x[q] + (w & 1) * 64 + (w >> 1) * 16);
         if (w == 0) mma_f16_first(p[q], xa & LO, xb & LO, xa & HI, xb & HI, x.x, x.y);
         else mma_f16_acc(p[q], xa & LO, xb & LO, xa & HI, xb & HI, x.x, x.y);
-        if (N > 1) mma_f16_acc(p[q], ya & LO, yb & LO, ya & HI, yb & HI, x.z, x.w);
-        else if (w == 0) mma_f16_first(p2, ya & LO, yb & LO, ya & HI, yb & HI, x.z, x.w);
+        if (w == 0) mma_f16_first(p2, ya & LO, yb & LO, ya & HI, yb & HI, x.z, x.w);
         else mma_f16_acc(p2, ya & LO, yb & LO, ya & HI, yb & HI, x.z, x.w);
       }
     }
-    if (N == 1)
 #pragma unroll
-      for (int i = 0; i < 4; i++) p[0][i] += p2[i];
+    for (int i = 0; i < 4; i++) p[0][i] += p2[i];
     lin_fold<N>(p, wsa, wma, wsb, wmb, (G128 ? hi : t >> 1) ? 0x3244u : 0x1044u, X.sv, acc);
   }
 }

@@ -353,6 +353,18 @@ def test_int4_linear_wide_range_activations():
     assert np.abs(f64(y[5:]) - ref[5:]).max() <= 1024 * 512 * 2.0 ** -149 + bound[5:].max()
 
 
+@pytest.mark.parametrize("T,K,N", [(5, 40960, 33), (8, 40960, 161), (7, 2112, 500), (8, 1 << 18, 17)])
+@pytest.mark.parametrize("fmt,xg", [("bf16", 0), ("int8", 64), ("e4m3", 0)])
+def test_int4_linear_five_to_eight_tokens(T, K, N, fmt, xg):
+    """One tile of 8 tokens: K over a cluster's blocks, an adapter's partial sums, a ragged last block."""
+    import int4_expert_streaming_prerouter_b200 as e0
+    m = int4_mat(N, K, 64, 31, r=9)
+    x, s, xv = acts(T, K, fmt, xg, 32)
+    y = torch.empty((T, N), dtype=F32, device="cuda")
+    e0.Int4Linear(**m)(x, x_scale=s, y=y)
+    check_linear(y, *linear_ref(m, 64, xv))
+
+
 @pytest.mark.parametrize("T", [3, 20])
 def test_int4_linear_token_that_is_not_finite_stays_alone(T):
     import int4_expert_streaming_prerouter_b200 as e0
