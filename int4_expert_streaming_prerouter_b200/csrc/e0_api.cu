@@ -2320,7 +2320,6 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
   A.dn_ring = (rest - A.out_bytes - (A.dn_rows * sum_bytes + 15) / 16 * 16) / kFewWarps / 16 * 16;
   if (A.gu_rows < kFewSeg || A.dn_rows < std::min(places, kFewSeg))
     return fail(E0_ERR_INVALID_ARG, "moe_layer_few: dims too large for the shared memory");
-  A.code = FewCode{0x000F000Fu, 0x43004300u};
   // tokens of a block in phase 1: 1, 2 or 4, until a block's share of the rows is 2 or less
   const int rows = D.n_experts + (any ? 2 * D.lora_rank : 0);
   for (A.tpb = 1; A.tpb < 4 && (long long)rows * ((T + A.tpb - 1) / A.tpb) > 2 * nsm; A.tpb *= 2) {}

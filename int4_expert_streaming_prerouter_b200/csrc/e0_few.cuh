@@ -24,13 +24,12 @@
 // of a tile is a function.  (724 KB of code with 12 inlined forms took 42 us for 5 tokens of
 // d = 256, most of it waiting for instructions.)
 //
-// Products: bf16 matrix instructions on the activations as they are.  A weight code q is held as
-// the bf16 number 128 + q (0x4300 + q, one mask and one or with the shift that brings its nibble
-// down), so   sum w x = s sum (128 + q) x + (m - 128 s) sum x   per group of 64; the sums of x
-// come with the activations.  The products are exact; the sums carry 128 times the sum of x on
-// top, which costs 4 bits of fp32's 24 where the x of a group agree in sign.  (e0_int4_linear,
-// which may return fp32, uses fp16 operands without that term, and pays for it by bringing the
-// activations to fp16's range; here each block would have to do that for every expert's a.)
+// Products: bf16 matrix instructions on the activations as they are.  A weight word holds 8 codes
+// n0..n7; masked in place, the pairs (n0, n4) and, after a shift by 8, (n2, n6) read as the bf16
+// subnormals q 2^-133, the pairs (n1, n5) and (n3, n7) as q 2^-129; one bf16 product with a power of
+// two brings each to q 2^-6, the most that a power of two within bf16 reaches.  So a code's products
+// q x 2^-6 are exact and the fp32 sums carry nothing beside them; the sums of x, which come with the
+// activations, carry 2^-6 too, and the end result is multiplied by 64.
 // Rows of x and a are stored with each 8 channels in the order 0 4 1 5 2 6 3 7, so that 16 bytes
 // are the operands that meet one word of codes.
 #pragma once
@@ -49,9 +48,7 @@ constexpr int kFewMaxSeg = kMaxE + 1 + kFewMaxA / 8;            // segments
 constexpr int kFewSeg = 8;                                      // tokens to a segment
 constexpr int kFewPad = 16;                                     // bytes between rows: 8 rows in distinct banks
 
-struct FewCode {
-  uint32_t mask, offset;        // 0x000F000F, 0x43004300
-};
+constexpr float kFewUnit = 64.0f;                               // what sums of products and of x are divided by
 
 struct FewArgs {
   const uint16_t *h, *delta;
@@ -69,15 +66,14 @@ struct FewArgs {
   float *gates;
   // workspace
   uint16_t *xb;               // [T][d], channels in operand order
-  float *xv;                  // [T][d / 64] sums of x
+  float *xv;                  // [T][d / 64] sums of x / kFewUnit
   float *logits;              // [T][E]
   float *lt;                  // [T][2][r]
   int32_t *rsel;              // [T][k] routing and gates, where one block routes for all
   float *rgate;
   uint16_t *a;                // [T][k + 1][I], channels in operand order
-  float *a8;                  // [T][k + 1][I / 8] sums of a
+  float *a8;                  // [T][k + 1][I / 8] sums of a / kFewUnit
   int *err;
-  FewCode code;
   int lora16;                 // rows of LoRA B begin at 16 bytes
   int tpb;                    // tokens that a block of phase 1 norms
   int gu_rows;                // activation rows that fit the staging area of phase 2
@@ -185,12 +181,12 @@ struct FewCol {
   }
 };
 
-// Pair i of a word's 8 codes as 128 + q, in operand order: one shift and one three-input operation.
-// Mask and offset come from registers: given as constants, they become two operations, since an
-// instruction holds one (142 against 138 us at 64 tokens: the integer pipe is what bounds the products).
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i, const FewCode &K) {
+// Pair i of a word's 8 codes as q 2^-6, in operand order.  (As 128 + q, by one mask and one or, a pair
+// is an instruction less, but 128 times the sum of x then stands in the fp32 sums: 4 of their bits.)
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
+  const uint32_t v = (w >> (i & 2 ? 8 : 0)) & (i & 1 ? 0x00F000F0u : 0x000F000Fu);
   uint32_t r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * i)), "r"(K.mask), "r"(K.offset));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(i & 1 ? 0x7D007D00u : 0x7F007F00u));   // 2^123, 2^127
   return r;
 }
 
@@ -201,7 +197,7 @@ __device__ __forceinline__ void few_fold(const float (&p)[N][4], uint32_t wsa, u
                                          uint32_t sel, const uint32_t (&v0)[N], const uint32_t (&v1)[N], int at,
                                          float (&acc)[N][4]) {
   auto pick = [&](uint32_t w) { return __uint_as_float(__byte_perm(w, 0u, sel)); };
-  const float sa = pick(wsa), sb = pick(wsb), ma = fmaf(-128.f, sa, pick(wma)), mb = fmaf(-128.f, sb, pick(wmb));
+  const float sa = pick(wsa), sb = pick(wsb), ma = pick(wma), mb = pick(wmb);
 #pragma unroll
   for (int q = 0; q < N; q++) {
     const float x0 = lds32(v0[q] + at), x1 = lds32(v1[q] + at);
@@ -217,7 +213,7 @@ __device__ __forceinline__ void few_fold(const float (&p)[N][4], uint32_t wsa, u
 // l / 4 + 8) of the two groups.
 template <bool WIDE, int N, int HALF>
 __device__ __forceinline__ void few_mul128(uint32_t w0, uint32_t w1, uint32_t wsa, uint32_t wma, uint32_t wsb, uint32_t wmb,
-                                           const FewCol<WIDE, N> &X, const FewCode &K, float (&acc)[N][4]) {
+                                           const FewCol<WIDE, N> &X, float (&acc)[N][4]) {
   const int t = threadIdx.x & 3;
   if (WIDE) {
 #pragma unroll
@@ -227,8 +223,8 @@ __device__ __forceinline__ void few_mul128(uint32_t w0, uint32_t w1, uint32_t ws
 #pragma unroll
       for (int w = 0; w < 2; w++) {
         const uint32_t xa = w ? wa.y : wa.x, xb = w ? wb.y : wb.x;
-        const uint32_t a0 = code_pair(xa, 0, K), a1 = code_pair(xa, 1, K), a2 = code_pair(xa, 2, K), a3 = code_pair(xa, 3, K);
-        const uint32_t b0 = code_pair(xb, 0, K), b1 = code_pair(xb, 1, K), b2 = code_pair(xb, 2, K), b3 = code_pair(xb, 3, K);
+        const uint32_t a0 = code_pair(xa, 0), a1 = code_pair(xa, 1), a2 = code_pair(xa, 2), a3 = code_pair(xa, 3);
+        const uint32_t b0 = code_pair(xb, 0), b1 = code_pair(xb, 1), b2 = code_pair(xb, 2), b3 = code_pair(xb, 3);
 #pragma unroll
         for (int q = 0; q < N; q++) {
           const uint4 x = lds128(X.x[q] + g * 128 + w * 16);
@@ -248,8 +244,8 @@ __device__ __forceinline__ void few_mul128(uint32_t w0, uint32_t w1, uint32_t ws
     for (int w = 0; w < 4; w++) {
       const uint32_t xa = w == 0 ? wa.x : w == 1 ? wa.y : w == 2 ? wa.z : wa.w;
       const uint32_t xb = w == 0 ? wb.x : w == 1 ? wb.y : w == 2 ? wb.z : wb.w;
-      const uint32_t a0 = code_pair(xa, 0, K), a1 = code_pair(xa, 1, K), a2 = code_pair(xa, 2, K), a3 = code_pair(xa, 3, K);
-      const uint32_t b0 = code_pair(xb, 0, K), b1 = code_pair(xb, 1, K), b2 = code_pair(xb, 2, K), b3 = code_pair(xb, 3, K);
+      const uint32_t a0 = code_pair(xa, 0), a1 = code_pair(xa, 1), a2 = code_pair(xa, 2), a3 = code_pair(xa, 3);
+      const uint32_t b0 = code_pair(xb, 0), b1 = code_pair(xb, 1), b2 = code_pair(xb, 2), b3 = code_pair(xb, 3);
 #pragma unroll
       for (int q = 0; q < N; q++) {
         const uint4 x = lds128(X.x[q] + w * 16);
@@ -393,7 +389,7 @@ __device__ __forceinline__ void few_phase1(const FewArgs &A, FewPlan &P, uint8_t
       const uint4 o = norm_bf16x8(w, gm, rinv, rinv_f, most);
       gm = __ldg(reinterpret_cast<const uint4 *>(A.gamma + min(c + wpt * 256, d - 8)));
       float v = ((bf_lo(o.x) + bf_hi(o.x)) + (bf_lo(o.y) + bf_hi(o.y))) + ((bf_lo(o.z) + bf_hi(o.z)) + (bf_lo(o.w) + bf_hi(o.w)));
-      v = group_sum(v, 8);                          // d is a multiple of 256: whole warps
+      v = group_sum(v * (1.0f / kFewUnit), 8);                          // d is a multiple of 256: whole warps
       const uint4 xv = operand_order(o);
       *reinterpret_cast<uint4 *>(xs + c * 2) = xv;
       if ((lane & 7) == 0) *reinterpret_cast<float *>(area + 8 * pitch + tok * vbytes + c / 64 * 4) = v;
@@ -636,11 +632,13 @@ struct FewPart {                  // what a warp does of K, and where its team s
 };
 
 // SwiGLU of one token (a lane's index l / 4 of tile i8 of segment s), with the shared expert's
-// LoRA; a to the workspace in operand order, and the sum of the tile's 8.
+// LoRA; a to the workspace in operand order, and the sum of the tile's 8.  g, u: in units of kFewUnit.
 __device__ __noinline__ void few_emit(const FewPlan &P, int s, int i8, int tok, float g, float u) {
   const FewArgs &A = P.args;
   const int q = (int)(threadIdx.x & 31) >> 2, n = P.seg_n[s], i = i8 * 8 + q;
   const int asg = P.asg[P.seg_at[s] + min(tok, n - 1)];
+  g *= kFewUnit;
+  u *= kFewUnit;
   if (P.seg_exp[s] == A.E && A.Ag) {
     const float *lt = A.lt + (size_t)(asg / (A.k + 1)) * 2 * A.r;
     const uint16_t *bg = A.Bg + (size_t)i * A.r, *bu = A.Bu + (size_t)i * A.r;
@@ -664,7 +662,7 @@ __device__ __noinline__ void few_emit(const FewPlan &P, int s, int i8, int tok, 
     u = fmaf(A.c, lu, u);
   }
   const uint32_t bits = f2bf(g / (1.0f + expf(-g)) * u);
-  float sum = bf(bits);
+  float sum = bf(bits) * (1.0f / kFewUnit);
   sum += __shfl_xor_sync(0xffffffffu, sum, 4);
   sum += __shfl_xor_sync(0xffffffffu, sum, 8);
   sum += __shfl_xor_sync(0xffffffffu, sum, 16);
@@ -786,7 +784,6 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
 #pragma unroll 1
   for (int u = 1; u < stages; u++) issue();
   uint32_t st = stages_at, sl = slots_end - kFewSlot;
-  const FewCode code = A.code;
   // the lane's codes in a stage: pair, chunk t (and, phase 2, 4 + t); wide, the 8 bytes of groups
   // 0 and 1 (and 2 and 3, 64 bytes on before the permutation)
   const int swz = GU ? row_swz(r) : r & 2, pitch = GU ? 128 : 64;
@@ -816,17 +813,17 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
       const uint32_t sc = sl + r * 32 + at128 * 4;
       if (GU) {
         const uint2 s0 = lds64(sc), m0 = lds64(sc + 16), s8 = lds64(sc + 256), m8 = lds64(sc + 272);
-        few_mul128<WIDE, N, 1024>(st + o0, st + o1, s0.x, m0.x, s8.x, m8.x, X, code, acc);
+        few_mul128<WIDE, N, 1024>(st + o0, st + o1, s0.x, m0.x, s8.x, m8.x, X, acc);
         X.advance(X.step);
         // chunk c + 4 lies 64 bytes from chunk c, on the side that the permutation leaves
-        few_mul128<WIDE, N, 1024>(st + (o0 ^ 64), st + (o1 ^ 64), s0.y, m0.y, s8.y, m8.y, X, code, acc);
+        few_mul128<WIDE, N, 1024>(st + (o0 ^ 64), st + (o1 ^ 64), s0.y, m0.y, s8.y, m8.y, X, acc);
         X.advance(X.step);
       } else {
         FewCol<WIDE, N> Y = X;            // the stage's own columns
         const uint32_t xbase = X.step ? st : 0u;
 #pragma unroll
         for (int q = 0; q < N; q++) Y.x[q] = X.x[q] + xbase;
-        few_mul128<WIDE, N, 512>(st + o0, st + o1, lds32u(sc), lds32u(sc + 16), lds32u(sc + 256), lds32u(sc + 272), Y, code, acc);
+        few_mul128<WIDE, N, 512>(st + o0, st + o1, lds32u(sc), lds32u(sc + 16), lds32u(sc + 256), lds32u(sc + 272), Y, acc);
         X.advance(0);
       }
       st = st + STAGE == end ? stages_at : st + STAGE;
@@ -1046,6 +1043,7 @@ __device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, u
         float v = p[0];
 #pragma unroll 1
         for (int w = 1; w < parts; w++) v += p[(size_t)w * nplace * 16];
+        v *= kFewUnit;
         y = j < A.k ? fmaf(P.gate[t * A.k + j], v, y) : y + v;
       }
       if (A.Ad) {

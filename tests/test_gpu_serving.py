@@ -687,6 +687,93 @@ def test_moe_few_agrees_with_the_context_path():
     ctx.close()
 
 
+def few_matrices(d, I, T_experts, mats):
+    """Blobs [T_experts, bytes]: per expert the matrices gate, up, down as (codes [n, k], scale [n, k/64], min [n, k/64])
+    float64 arrays of numbers that the format holds."""
+    out = np.zeros((T_experts, synth.blob_bytes(d, I)), np.uint8)
+    for e, trio in mats.items():
+        for name, off, n, shape, dt in synth.blob_sections(d, I):
+            p, part = name.split(".")
+            codes, scale, mins = trio[p]
+            if part == "codes":
+                c = codes.astype(np.uint8)
+                v = (c[:, 0::2] | c[:, 1::2] << 4).reshape(-1)
+            else:
+                v = O.f64_to_bf16_bits(scale if part == "scale" else mins).astype(np.uint16).reshape(-1).view(np.uint8)
+            out[e, off:off + n] = v
+    return torch.from_numpy(out).cuda()
+
+
+def few_exact_case(kind, T, I=128, d=256):
+    """A layer and hidden states all of whose sums fp32 holds exactly, however they are ordered, if each product is
+    q x: (layer, h, y).  Where an operand carries more than q, the channels whose code is 0 take the low bits of the
+    others away.  Only the shared expert adds to y (the routed one's weights are zeros)."""
+    rng = np.random.default_rng(100 * T + len(kind))
+    # 64 of 256 channels are not zero: mean h^2 = (v / 2)^2, so x = 2 gamma (eps moves it by 4e-12 of itself)
+    live = np.arange(65) != 63
+    channels = np.flatnonzero(live)
+    gamma = np.ones(d)
+    gamma[channels] = rng.integers(128, 256, 64) / 128.0
+    small = channels[32:63]                       # the second half of the first group
+    gamma[small] *= 2.0 ** -8
+    gamma[64] = 1.0                               # the one channel of the second group
+    h = np.zeros((T, d))
+    h[:, channels] = 1024.0
+    h[:, small] *= rng.choice([-1, 1], (T, len(small)))
+    x = 2 * np.sign(h) * gamma
+    zero = (np.zeros((I, d)), np.zeros((I, d // 64)), np.zeros((I, d // 64)))
+    gate = (zero[0], zero[1], zero[2].copy())
+    gate[2][:, 1] = 16.0                          # g = 32: silu(g) = g in fp32
+    up = (zero[0].copy(), zero[1].copy(), zero[2].copy())
+    down = (np.zeros((d, I)), np.zeros((d, I // 64)), np.zeros((d, I // 64)))
+    down[1][:] = 1.0
+    if kind == "up":                              # codes on the small channels, zeros on the large ones
+        up[0][:, small] = rng.integers(0, 16, (I, len(small)))
+        up[1][:, 0] = 1.0
+        for n in range(d):                        # a row of y sums four numbers of a
+            down[0][n, rng.permutation(I)[:4]] = 1
+    else:                                         # u by index from the mins; large and small a in the groups of down
+        up[2][:, 1] = rng.integers(128, 256, I) / 128.0 * np.where(np.arange(I) % 2, 2.0 ** -9, 1.0)
+        down[0][:, 1::2] = rng.integers(0, 16, (d, I // 2))
+    W = {p: m[0] * np.repeat(m[1], 64, 1) + np.repeat(m[2], 64, 1) for p, m in (("gate", gate), ("up", up), ("down", down))}
+    g, u = x @ W["gate"].T, x @ W["up"].T
+    assert (g == 32).all()
+    y = O.round_bf16(32 * u) @ W["down"].T
+    blobs = few_matrices(d, I, 2, {1: {"gate": gate, "up": up, "down": down}})
+    bf = lambda v: torch.from_numpy(v).to(BF16).cuda()  # noqa: E731
+    layer = {"experts": blobs[:1], "shared": blobs[1], "router_w": torch.zeros((1, d), dtype=BF16, device="cuda"), "norm_w": bf(gamma)}
+    return layer, bf(h), y
+
+
+@pytest.mark.parametrize("T", [1, 4, 5, 8, 21])
+@pytest.mark.parametrize("kind", ["up", "down"])
+def test_moe_few_products_are_of_the_codes_alone(kind, T):
+    """Sums that fp32 holds exactly come out exactly: codes of 0 beside large activations add nothing."""
+    import int4_expert_streaming_prerouter_b200 as e0
+    layer, h, y = few_exact_case(kind, T)
+    got = torch.empty((T, 256), device="cuda")
+    e0.MoeLayer(e0.make_dims(256, 1, 128, 1, 0), layer).few(h, y_f32=got)
+    same(f64(got), y, kind)
+
+
+def test_moe_few_large_activations():
+    """a of 2^121 (its group of 64 sums to 2^127): finite, as its products with the codes are."""
+    import int4_expert_streaming_prerouter_b200 as e0
+    d, I = 256, 128
+    ones = lambda n, k, v: np.full((n, k // 64), v)  # noqa: E731
+    mats = {"gate": (np.zeros((I, d)), ones(I, d, 0.0), ones(I, d, 0.25)),       # x = 1: g = 64
+            "up": (np.zeros((I, d)), ones(I, d, 0.0), ones(I, d, 2.0 ** 107)),   # u = 2^115
+            "down": (np.ones((d, I)), ones(d, I, 2.0 ** -10), ones(d, I, 0.0))}
+    blobs = few_matrices(d, I, 2, {1: mats})
+    layer = {"experts": blobs[:1], "shared": blobs[1], "router_w": torch.zeros((1, d), dtype=BF16, device="cuda"),
+             "norm_w": torch.ones(d, dtype=BF16, device="cuda")}
+    for T in (1, 7):
+        got = torch.empty((T, d), device="cuda")
+        h = torch.full((T, d), 1024.0, dtype=BF16, device="cuda")
+        e0.MoeLayer(e0.make_dims(d, 1, I, 1, 0), layer).few(h, y_f32=got)
+        same(f64(got), np.full((T, d), 2.0 ** 118))
+
+
 def test_two_streams_at_once():
     """Calls on two streams, each with buffers of its own, give what one stream gives."""
     import int4_expert_streaming_prerouter_b200 as e0
