@@ -290,7 +290,8 @@ int e0_moe_layer_forward_noalloc(const e0_dims *dims, const e0_layer *layer, con
  * add_rmsnorm -> int4_linear (queries, keys, values) -> attention -> int4_linear (output) ->
  * moe_layer_few -> the next layer's add_rmsnorm.  None of the three needs a context, none
  * allocates, each enqueues one kernel on `stream`, which belongs to the current device, and
- * may be captured into a graph.  They compute for inference: none has a backward pass. */
+ * may be captured into a graph.  An address that is no multiple of its elements' size is
+ * refused.  They compute for inference: none has a backward pass. */
 
 /* Formats of 8-bit activations (and of x in e0_int4_linear). */
 enum { E0_ACT_BF16 = 0, E0_ACT_INT8 = 1, E0_ACT_E4M3 = 2 };
@@ -341,8 +342,8 @@ typedef struct {
  *           overlap the inputs.
  * n up to 2^26, k up to 2^18, T up to 524,280, but made for few tokens: the weights are read
  * once per 32 of them (fewer where 32 rows of k do not fit a cluster's shared memory).  codes
- * and lora_A are 16-byte aligned; scale and min may begin anywhere, and are read fastest where
- * their rows begin at 16 bytes.  T = 0 does nothing.
+ * and lora_A are 16-byte aligned; scale and min may begin at any element, and are read fastest
+ * where their rows begin at 16 bytes.  T = 0 does nothing.
  * Errors: INVALID_ARG, CUDA. */
 int e0_int4_linear(const e0_int4_mat *w, const void *x, int x_format, long long x_stride, const float *x_scale,
                    int x_group, int T, void *y, int y_f32, long long y_stride, void *stream);

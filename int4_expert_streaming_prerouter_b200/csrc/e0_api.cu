@@ -2066,6 +2066,9 @@ extern "C" int e0_add_rmsnorm(const void *h, long long h_stride, const void *del
   if (h_stride < d || (delta && delta_stride < d) || (h_out && h_out_stride < d) || (x && x_stride < d) ||
       (q8 && q8_stride < d))
     return fail(E0_ERR_INVALID_ARG, "add_rmsnorm: a row stride is below d");
+  if (misaligned(h, 2) || misaligned(norm_w, 2) || misaligned(h_out, 2) || misaligned(x, 2) ||
+      misaligned(delta, delta_f32 ? 4 : 2) || (q8 && misaligned(q8_scale, 4)))
+    return fail(E0_ERR_INVALID_ARG, "add_rmsnorm: an address is not aligned to its elements");
   AddNormArgs A{};
   A.h = (const uint16_t *)h; A.h_stride = h_stride;
   A.delta = delta; A.delta_f32 = delta_f32; A.delta_stride = delta_stride;
@@ -2222,6 +2225,9 @@ extern "C" int e0_int4_linear(const e0_int4_mat *w, const void *x, int x_format,
   if (x_stride < w->k || y_stride < w->n) return fail(E0_ERR_INVALID_ARG, "int4_linear: a row stride is below its length");
   if (misaligned(w->codes, 16) || misaligned(x, bf16x ? 16 : 8) || x_stride % 8 || misaligned(w->lora_A, 16))
     return fail(E0_ERR_INVALID_ARG, "int4_linear: codes, lora_A and bf16 x are 16-byte aligned, 8-bit x 8-byte, x_stride a multiple of 8");
+  if (misaligned(w->scale, 2) || misaligned(w->min, 2) || misaligned(w->lora_B, 2) || misaligned(x_scale, 4) ||
+      misaligned(y, y_f32 ? 4 : 2))
+    return fail(E0_ERR_INVALID_ARG, "int4_linear: an address is not aligned to its elements");
   LinearArgs L{};
   L.codes = (const uint8_t *)w->codes; L.scale = (const uint8_t *)w->scale; L.min = (const uint8_t *)w->min;
   L.N = w->n; L.K = w->k;
@@ -2285,6 +2291,10 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
       misaligned(Y.lora_Ag, 16) || misaligned(Y.lora_Au, 16) || misaligned(Y.lora_Ad, 16) || misaligned(h, 16) ||
       misaligned(delta, 16) || misaligned(h_out, 16))
     return fail(E0_ERR_INVALID_ARG, "moe_layer_few: weights, h, delta and h_out are 16-byte aligned");
+  if (misaligned(Y.lora_Bg, 2) || misaligned(Y.lora_Bu, 2) || misaligned(Y.lora_Bd, 2) || misaligned(route_idx, 4) ||
+      misaligned(y_bf16, 2) || misaligned(y_f32, 4) || misaligned(idx_out, 4) || misaligned(gate_out, 4) ||
+      misaligned(dev_status, 4))
+    return fail(E0_ERR_INVALID_ARG, "moe_layer_few: an address is not aligned to its elements");
   const FewSpace S = few_space(D, T);
   if (!workspace || misaligned(workspace, 256) || workspace_bytes < S.bytes)
     return fail(E0_ERR_INVALID_ARG, "moe_layer_few: %zu bytes of workspace are needed, 256-byte aligned", S.bytes);

@@ -136,3 +136,22 @@ def test_the_binding_refuses_what_does_not_fit():
         ml.few(torch.zeros(1, 128, dtype=bf16), y=torch.zeros(1, 256, dtype=bf16), workspace=codes)
     with pytest.raises(e0.E0Error):
         ml.few_workspace(65)
+
+
+@pytest.mark.parametrize("call,bad", [
+    (norm, dict(h=P + 1)), (norm, dict(norm_w=P + 1)), (norm, dict(x=P + 1)), (norm, dict(h_out=P + 1, h_out_stride=256)),
+    (norm, dict(delta=P + 1, delta_stride=256)), (norm, dict(delta=P + 2, delta_stride=256, delta_f32=1)),
+    (norm, dict(q8=P, q8_stride=256, q8_format=1, q8_scale=P + 2)),
+    (linear, dict(mat=dict(scale=P + 1))), (linear, dict(mat=dict(min=P + 1))),
+    (linear, dict(mat=dict(lora_A=P, lora_B=P + 1, lora_rank=4))), (linear, dict(x_format=1, x_scale=P + 2)),
+    (linear, dict(y=P + 1)), (linear, dict(y=P + 2, y_f32=1)),
+    (few, dict(y=P + 1)), (few, dict(y_f32=P + 2)), (few, dict(route_idx=P + 2)), (few, dict(idx=P + 2)), (few, dict(gates=P + 2)),
+    (few, dict(dev_status=P + 2)),
+    (few, dict(layer=dict(lora_Ag=P, lora_Bg=P + 1, lora_Au=P, lora_Bu=P, lora_Ad=P, lora_Bd=P))),
+    (few, dict(layer=dict(lora_Ag=P, lora_Bg=P, lora_Au=P, lora_Bu=P + 1, lora_Ad=P, lora_Bd=P))),
+    (few, dict(layer=dict(lora_Ag=P, lora_Bg=P, lora_Au=P, lora_Bu=P, lora_Ad=P, lora_Bd=P + 1))),
+])
+def test_addresses_between_elements_are_refused(call, bad):
+    """An address that is no multiple of its element's size would be a misaligned access on the device."""
+    assert call(**bad) == -1
+    assert b"aligned" in e0.lib().e0_last_error()
