@@ -17,7 +17,7 @@ from typing import Optional
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libe0moe.so")
 
-E0_OK = 0
+E0_OK, E0_ERR_INVALID_ARG = 0, -1
 STATUS = {0: "OK", -1: "INVALID_ARG", -2: "CUDA", -3: "OOM", -4: "STAGING", -5: "SLOT_MISMATCH",
           -6: "TIMEOUT", -7: "DEVICE"}
 
@@ -441,6 +441,7 @@ class Context:
             lib().e0_destroy(self._h)
             self._h = None
             self._keep = []
+            self._layers = ()
 
     def __del__(self):
         try:
@@ -484,6 +485,8 @@ class Context:
                       workspace=None, dev_status=None, stream=None):
         """The MoE block of a registered layer for 1..64 tokens in one launch (see MoeLayer.few;
         it uses none of the context's workspaces)."""
+        if self._h is None:
+            raise E0Error(E0_ERR_INVALID_ARG, "moe_layer_few: the context is closed")
         if not 0 <= layer < len(self._layers):
             raise IndexError(f"layer {layer} of {len(self._layers)} registered")
         return _moe_layer_few(self.dims, self._layers[layer], h, delta, route_idx, h_out, y, y_f32, idx, gates, workspace,

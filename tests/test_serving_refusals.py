@@ -155,3 +155,61 @@ def test_addresses_between_elements_are_refused(call, bad):
     """An address that is no multiple of its element's size would be a misaligned access on the device."""
     assert call(**bad) == -1
     assert b"aligned" in e0.lib().e0_last_error()
+
+
+class FakeLibrary:
+    """Answers the calls of a context's life without a GPU; records that nothing is launched."""
+
+    def __init__(self):
+        self.launched = 0
+
+    def e0_create(self, dims, n, tokens, out):
+        out._obj.value = 1
+        return 0
+
+    def e0_register_model(self, ctx, layers, heads):
+        return 0
+
+    def e0_destroy(self, ctx):
+        return 0
+
+    def e0_last_error(self):
+        return b""
+
+    def e0_moe_layer_few(self, *args):
+        self.launched += 1
+        return 0
+
+    def e0_moe_layer_few_workspace(self, dims, T, n):
+        n._obj.value = 64
+        return 0
+
+
+def few_layer(d=256, E=16, I=128, r=8, device="cpu"):
+    bf16 = dict(dtype=torch.bfloat16, device=device)
+    blob = 3 * (I * d // 2 + 4 * I * (d // 64))
+    return {"experts": torch.zeros((E, blob), dtype=torch.uint8, device=device),
+            "shared": torch.zeros(blob, dtype=torch.uint8, device=device),
+            "router_w": torch.zeros((E, d), **bf16), "norm_w": torch.zeros(d, **bf16),
+            "lora_Ag": torch.zeros((r, d), **bf16), "lora_Bg": torch.zeros((I, r), **bf16),
+            "lora_Au": torch.zeros((r, d), **bf16), "lora_Bu": torch.zeros((I, r), **bf16),
+            "lora_Ad": torch.zeros((r, I), **bf16), "lora_Bd": torch.zeros((d, r), **bf16)}
+
+
+def test_a_closed_context_runs_no_layer(monkeypatch):
+    """close() lets go of the weights; a call after it would read freed memory."""
+    fake = FakeLibrary()
+    monkeypatch.setattr(e0, "lib", lambda: fake)
+    monkeypatch.setattr(e0, "_call", lambda X, dev, stream, fn, *args: fake.e0_moe_layer_few(*args))
+    monkeypatch.setattr(e0, "_torch_names", None)
+    monkeypatch.setattr(FakeLibrary, "e0_add_rmsnorm", None, raising=False)
+    monkeypatch.setattr(FakeLibrary, "e0_int4_linear", None, raising=False)
+    ctx = e0.Context(256, 16, 128, 4, 8, 1, 8)
+    ctx.register_model([few_layer()])
+    h = torch.zeros((1, 256), dtype=torch.bfloat16)
+    ctx.moe_layer_few(0, h)
+    assert fake.launched == 1
+    ctx.close()
+    with pytest.raises(e0.E0Error):
+        ctx.moe_layer_few(0, h)
+    assert fake.launched == 1
