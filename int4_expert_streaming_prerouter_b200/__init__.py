@@ -379,27 +379,44 @@ class Int4Linear:
         return y
 
 
+def _layer_shapes(dims):
+    """Shapes of a layer's tensors: the experts' bytes as uint8, the others bf16."""
+    d, E, I, r = dims.d_model, dims.n_experts, dims.d_ff, dims.lora_rank
+    blob = 3 * (I * d // 2 + 4 * I * (d // 64))         # codes, scales and mins of gate, up and down
+    return {"experts": (E, blob), "shared": (blob,), "router_w": (E, d), "norm_w": (d,),
+            "lora_Ag": (r, d), "lora_Bg": (I, r), "lora_Au": (r, d), "lora_Bu": (I, r), "lora_Ad": (r, I), "lora_Bd": (d, r)}
+
+
 class MoeLayer:
     """One MoE layer's resident weights, for few tokens without a context (see
     e0_moe_layer_few in the C header).  `layer` is a dict of torch tensors as for
-    Context.register_model; it keeps them."""
+    Context.register_model, all on one device; it keeps them."""
 
     def __init__(self, dims: Dims, layer: dict):
-        self.dims = dims
-        self._keep = dict(layer)
+        X = _torch()
+        self.dims = Dims.from_buffer_copy(dims)
+        self._keep = {f: layer.get(f) for f, _ in Layer._fields_}
+        there = {f: t for f, t in self._keep.items() if t is not None}
+        self.device = next((t.device for t in there.values()), None)
+        self._dev = -1 if self.device is None or self.device.type != "cuda" else next(iter(there.values())).get_device()
+        shapes = _layer_shapes(dims)
         self._layer = Layer()
-        for f, _ in Layer._fields_:
-            setattr(self._layer, f, _ptr(layer.get(f)))
+        for f, t in there.items():
+            if t.device != self.device:
+                raise ValueError(f"{f}: on {t.device}, the layer's other tensors are on {self.device}")
+            setattr(self._layer, f, _flat(t, f, shapes[f], X.u8 if f in ("experts", "shared") else X.bf16, t.get_device()))
 
     def few_workspace(self, T: int):
         """A workspace for calls of at most T tokens (calls that may overlap need one each)."""
-        return _few_workspace(self.dims, T, self._keep["router_w"].device)
+        return _few_workspace(self.dims, T, self.device)
 
     def few(self, h, delta=None, route_idx=None, h_out=None, y=None, y_f32=None, idx=None, gates=None, workspace=None,
             dev_status=None, stream=None):
         """The MoE block of 1..64 tokens in one launch: h' = bf16(h + delta) [T, d] (to h_out
         where given; it may be h), y [T, d] bf16 = the block's output for h'.  Without
         `workspace` one is allocated for the call."""
+        if h.get_device() != self._dev:
+            raise ValueError(f"h: on {h.device}, the layer is on {self.device}")
         return _moe_layer_few(self.dims, self._layer, h, delta, route_idx, h_out, y, y_f32, idx, gates,
                               workspace, dev_status, stream)
 
@@ -430,7 +447,7 @@ class Context:
         self.dims = make_dims(d, E, I, k, r, head_hidden, head_onehot, eps, lora_scale)
         self.n_layers, self.max_tokens = n_layers, max_tokens
         self._keep = []
-        self._layers = ()
+        self._layers, self._few = [], {}
         h = _P()
         _check(lib().e0_create(ctypes.byref(self.dims), n_layers, max_tokens, ctypes.byref(h)))
         self._h = h
@@ -441,7 +458,7 @@ class Context:
             lib().e0_destroy(self._h)
             self._h = None
             self._keep = []
-            self._layers = ()
+            self._layers, self._few = [], {}
 
     def __del__(self):
         try:
@@ -467,7 +484,7 @@ class Context:
                 setattr(H[i], f, _ptr(t))
                 self._keep.append(t)
         _check(lib().e0_register_model(self._h, L, H))
-        self._layers = L
+        self._layers, self._few = [dict(ly) for ly in layers], {}
 
     # -- one MoE block ------------------------------------------------------------------
     def moe_layer_forward(self, layer, h, route_idx=None, y=None, y_f32=None, idx=None, gates=None,
@@ -489,8 +506,9 @@ class Context:
             raise E0Error(E0_ERR_INVALID_ARG, "moe_layer_few: the context is closed")
         if not 0 <= layer < len(self._layers):
             raise IndexError(f"layer {layer} of {len(self._layers)} registered")
-        return _moe_layer_few(self.dims, self._layers[layer], h, delta, route_idx, h_out, y, y_f32, idx, gates, workspace,
-                              dev_status, stream)
+        if layer not in self._few:
+            self._few[layer] = MoeLayer(self.dims, self._layers[layer])
+        return self._few[layer].few(h, delta, route_idx, h_out, y, y_f32, idx, gates, workspace, dev_status, stream)
 
     def prerouter_predict(self, layer, x, cur=None, prev=None, pred=None, logits=None, stream=None):
         import torch

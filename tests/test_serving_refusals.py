@@ -213,3 +213,65 @@ def test_a_closed_context_runs_no_layer(monkeypatch):
     with pytest.raises(e0.E0Error):
         ctx.moe_layer_few(0, h)
     assert fake.launched == 1
+
+
+def few_handles(monkeypatch, layer, dims=(256, 16, 128, 4, 8)):
+    """The two ways to a layer: a call of one token that MoeLayer and one that a context makes, counted by the library."""
+    fake = FakeLibrary()
+    monkeypatch.setattr(e0, "lib", lambda: fake)
+    monkeypatch.setattr(e0, "_call", lambda X, dev, stream, fn, *args: fake.e0_moe_layer_few(*args))
+    monkeypatch.setattr(e0, "_torch_names", None)
+    monkeypatch.setattr(FakeLibrary, "e0_add_rmsnorm", None, raising=False)
+    monkeypatch.setattr(FakeLibrary, "e0_int4_linear", None, raising=False)
+    h = torch.zeros((1, dims[0]), dtype=torch.bfloat16)
+
+    def by_handle():
+        e0.MoeLayer(e0.make_dims(*dims), layer).few(h)
+
+    def by_context():
+        ctx = e0.Context(*dims, 1, 8)
+        ctx.register_model([layer])
+        ctx.moe_layer_few(0, h)
+    return fake, (by_handle, by_context)
+
+
+@pytest.mark.parametrize("change", [
+    dict(experts=lambda t: t[:15]), dict(experts=lambda t: t[:, :-64].contiguous()), dict(experts=lambda t: t.view(torch.int8)),
+    dict(shared=lambda t: t[:-2]), dict(shared=lambda t: t[None]), dict(router_w=lambda t: t.float()),
+    dict(router_w=lambda t: t[:, :128].contiguous()), dict(router_w=lambda t: t.half()), dict(norm_w=lambda t: t[:255]),
+    dict(norm_w=lambda t: t.view(torch.int16)), dict(lora_Ag=lambda t: t[:7]), dict(lora_Bg=lambda t: t[:, :4].contiguous()),
+    dict(lora_Au=lambda t: t.T.contiguous()), dict(lora_Bu=lambda t: t[:64]), dict(lora_Ad=lambda t: t.repeat(2, 1)),
+    dict(lora_Bd=lambda t: t.float()), dict(router_w=lambda t: t.to("meta")), dict(experts=lambda t: t.T),
+])
+def test_moe_layer_weights_that_do_not_fit_the_dims(change, monkeypatch):
+    """Tensors of another shape or type, or on another device, would be read past their ends, or as what they are not."""
+    (name, make), = change.items()
+    layer = few_layer()
+    layer[name] = make(layer[name])
+    fake, calls = few_handles(monkeypatch, layer)
+    for call in calls:
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    assert fake.launched == 0
+
+
+def test_moe_layer_weights_that_fit(monkeypatch):
+    plain = few_layer()
+    no_lora = {n: t for n, t in plain.items() if not n.startswith("lora_")}
+    for layer, dims in ((plain, (256, 16, 128, 4, 8)), (no_lora, (256, 16, 128, 4, 8)), (no_lora, (256, 16, 128, 4, 0)),
+                        (few_layer(r=3), (256, 16, 128, 4, 3)), (plain | {"lora_Ag": None, "lora_Bg": None}, (256, 16, 128, 4, 8))):
+        fake, calls = few_handles(monkeypatch, layer, dims)
+        for call in calls:
+            call()
+        assert fake.launched == 2
+
+
+def test_moe_layer_on_another_device_than_its_input(monkeypatch):
+    fake, _ = few_handles(monkeypatch, few_layer())
+    ml = e0.MoeLayer(e0.make_dims(256, 16, 128, 4, 8), few_layer())
+    h = torch.zeros((1, 256), dtype=torch.bfloat16)
+    ml.few(h)
+    ml._dev = 1                                          # as weights of the second GPU have it
+    with pytest.raises(ValueError):
+        ml.few(h)
+    assert fake.launched == 1
