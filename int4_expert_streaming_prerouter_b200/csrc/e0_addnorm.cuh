@@ -64,12 +64,16 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 
 // bf16(h g rinv), rinv in 64 bits and rinv_f its fp32 rounding.  The fp32 product carries three
 // roundings of half an ulp each, so it is off by at most 3 ulp.
+// That holds where nothing on the way is below fp32's normal numbers, 2^-126.  rinv_f is NaN where rinv
+// itself is (norm_rinv), and h rinv can be only where the result is below 2^-111 or gamma is 2^15 or more.
 // (The 64-bit form stays a call: inlined at every element it would be most of the code.)
+__device__ __forceinline__ float norm_rinv(double rinv) { return rinv >= 0x1p-126 ? (float)rinv : __uint_as_float(0x7FC00000u); }
 __device__ __noinline__ uint32_t norm_bf16_64(float h, float g, double rinv) { return d2bf((double)h * (double)g * rinv); }
 
 // 8 channels of h and gamma (bf16) normed; the largest of their magnitudes (as bf16 bits: a NaN is the
 // largest) goes to `most`.  Results within 4 ulp of a border, or not in [2^-111, 2^112) (where the
-// fp32 product, or the 2^-133 spacing of small bf16 numbers, would need care), are done again.
+// fp32 product, or the 2^-133 spacing of small bf16 numbers, would need care), or under a gamma of 2^15
+// or more are done again.
 __device__ __forceinline__ uint4 norm_bf16x8(uint4 h, uint4 g, double rinv, float rinv_f, uint32_t &most) {
   const uint32_t hs[4] = {h.x, h.y, h.z, h.w}, gs[4] = {g.x, g.y, g.z, g.w};
   uint32_t o[4], border = 0xFFFFFFFFu, low = 0xFFFFFFFFu, high = 0;
@@ -92,6 +96,11 @@ __device__ __forceinline__ uint4 norm_bf16x8(uint4 h, uint4 g, double rinv, floa
       const uint32_t lo = o[j] & 0x7FFFu, hi = (o[j] >> 16) & 0x7FFFu;
       again |= (lo < 0x0800u && bf_lo(hs[j]) * bf_lo(gs[j]) != 0.f) || (hi < 0x0800u && bf_hi(hs[j]) * bf_hi(gs[j]) != 0.f);
     }
+  }
+  if ((gs[0] | gs[1] | gs[2] | gs[3]) & 0x40004000u) {
+    // (a gamma of 2 or more: rare enough to look closer at)
+#pragma unroll
+    for (int j = 0; j < 4; j++) again |= (gs[j] & 0x7FFFu) >= 0x4700u || (gs[j] & 0x7FFF0000u) >= 0x47000000u;
   }
   if (again) {
     most = 0;
@@ -252,7 +261,7 @@ __global__ void __launch_bounds__(addnorm_threads(V)) k_add_rmsnorm(const __grid
     ss = warp_sum(ss);
   }
   const double rinv = rsqrt(fma(ss, A.inv_d, (double)A.eps));
-  const float rinv_f = (float)rinv;
+  const float rinv_f = norm_rinv(rinv);
   uint32_t gm[V], rowmax = 0;
 #pragma unroll
   for (int v = 0; v < V; v++) {

@@ -381,7 +381,7 @@ __device__ __forceinline__ void few_phase1(const FewArgs &A, FewPlan &P, uint8_t
     ss = P.part[tok * wpt + (lane & (wpt - 1))];
     for (int o = wpt >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const double rinv = rsqrt(fma(ss, A.inv_d, (double)A.eps));
-    const float rinv_f = (float)rinv;
+    const float rinv_f = norm_rinv(rinv);
 #pragma unroll 1
     for (int c = c0; c < d; c += wpt * 256) {
       const uint4 w = *reinterpret_cast<const uint4 *>(xs + c * 2);

@@ -220,6 +220,27 @@ def test_add_rmsnorm_rows_farther_apart_than_32_bits():
     same(f64(out[1]), x)
 
 
+def wide_range_rows(d=2048):
+    """Rows whose norm leaves fp32's normal range on the way: (h, gamma)."""
+    rng = np.random.default_rng(7)
+    h = rng.integers(128, 256, (4, d)) * 2.0 ** -82 * rng.choice([-1, 1], (4, d))
+    gamma = rng.integers(128, 256, d) * 2.0 ** 33
+    # 0, 1: h / rms of 2^-132 under a gamma of 2^40; 2: rms of 2^127.9, whose reciprocal is a subnormal;
+    # 3: a gamma of 2^40 where nothing is small
+    h[:2, ::64] = rng.integers(200, 256, (2, 1)) * 2.0 ** 53
+    h[2] = rng.integers(240, 256, d) * 2.0 ** 120
+    h[3] = rng.integers(128, 256, d) / 64.0
+    return torch.from_numpy(h).to(BF16).cuda(), torch.from_numpy(gamma).to(BF16).cuda()
+
+
+@pytest.mark.parametrize("dtype,group", [(None, 0), (E4M3, 64), (torch.int8, 0)])
+def test_add_rmsnorm_beyond_fp32_on_the_way(dtype, group):
+    """x in range, h / rms or 1 / rms below fp32's normal numbers: still the exact value rounded once."""
+    for d in (2048, 16392):
+        h, gamma = wide_range_rows(d)
+        run_norm(h, gamma, None, 0.0, dtype, group)
+
+
 def test_add_rmsnorm_of_no_rows():
     import int4_expert_streaming_prerouter_b200 as e0
     e0.add_rmsnorm(torch.empty((0, 64), dtype=BF16, device="cuda"), torch.ones(64, dtype=BF16, device="cuda"))
