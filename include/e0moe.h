@@ -336,7 +336,7 @@ typedef struct {
  * x         [T, k]: bf16, or 8-bit codes (int8, e4m3) times x_scale; rows x_stride elements
  *           apart, a multiple of 8; 16-byte aligned (8-bit: 8).
  * x_scale   NULL for bf16, else fp32 [T, k / x_group] contiguous, x_group 64, 128 or 0 (one
- *           scale a row): as e0_add_rmsnorm writes them.  A scale of 2^117 or more counts as
+ *           scale a row): as e0_add_rmsnorm writes them.  A scale of 2^121 or more counts as
  *           infinite.
  * y         [T, n] bf16 (y_f32 = 0) or fp32 (1), rows y_stride elements apart; must not
  *           overlap the inputs.

@@ -103,10 +103,11 @@ __device__ __forceinline__ void bf16_mul(uint4 a, uint4 b, uint4 x, float (&acc)
 // at 16 t, then the 8 channels 16 t + 8 w + {0, 4, 1, 5, 2, 6, 3, 7}, the odd ones divided by
 // 16 (their codes sit 4 bits higher).  Lane t of a matrix instruction reads its operands of a
 // word in one 16-byte access.  `sv` holds, for each group and pair of tokens, {factor of the
-// first, of the second, sum of the first, of the second}.  factor and sum carry 2^-9, which
-// the end result is multiplied with once, so that no factor overflows.
+// first, of the second, sum of the first, of the second}.  factor and sum carry 2^-12, by which
+// the end result is divided once: a group of bf16's largest numbers times codes of 15 comes to
+// 2^138, with it to less than fp32's largest.
 enum { ACT_BF16 = 0, ACT_INT8 = 1, ACT_E4M3 = 2 };
-constexpr float kActUnit = 512.0f;
+constexpr float kActUnit = 4096.0f;
 constexpr int kActPad = 64;               // per token, so that the tokens of a load fall into distinct banks
 
 __device__ __forceinline__ uint32_t half2_of(float a, float b) {
@@ -165,14 +166,19 @@ __device__ __forceinline__ void act_group_bf16(uint4 w, int i, int tok, int grp,
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
   m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-  // largest in [2^(eb-127), 2^(eb-126)) -> [2^15, 2^16); an infinity (eb = 255) makes the factor
-  // infinite and a NaN the sum, so the token's outputs are not finite
+  // largest in [2^(eb-127), 2^(eb-126)) -> [2^15, 2^16); an infinity or a NaN stays one in its place
+  // and in the sum, so the token's outputs are not finite
   const uint32_t eb = max(__float_as_uint(m) >> 23, 15u);
-  const float up = __uint_as_float((269u - eb) << 23), up16 = up * 0.0625f, factor = __uint_as_float(eb << 23);
-  const float s = group_sum(sum8(v) * (1.0f / kActUnit), 8);
+  const float up = __uint_as_float((269u - eb) << 23), up16 = up * 0.0625f, factor = __uint_as_float((eb - 3) << 23);
+#pragma unroll
+  for (int j = 0; j < 8; j++) v[j] *= j & 1 ? up16 : up;
+  // the sum, of the numbers in range (exact, but for what is 2^-24 of the largest and less), back by
+  // 2^(eb-142) / kActUnit in two factors, as one would be below fp32's normal numbers
+  const float s8 = fmaf(16.0f, (v[1] + v[3]) + (v[5] + v[7]), (v[0] + v[2]) + (v[4] + v[6]));
+  const float s = group_sum(s8, 8) * 0x1p-24f * factor;
+  static_assert(kActUnit == 4096.0f, "factor is 2^(eb - 142) 2^24 / kActUnit, the factor of the sum 2^(eb - 142) / kActUnit");
   if (put)
-    D.put(tok, grp, i, make_uint4(half2_of(v[0] * up, v[4] * up), half2_of(v[1] * up16, v[5] * up16),
-                                  half2_of(v[2] * up, v[6] * up), half2_of(v[3] * up16, v[7] * up16)), factor, s);
+    D.put(tok, grp, i, make_uint4(half2_of(v[0], v[4]), half2_of(v[1], v[5]), half2_of(v[2], v[6]), half2_of(v[3], v[7])), factor, s);
 }
 
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
@@ -181,7 +187,7 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   return r;
 }
 
-// Codes times 32 (odd channels times 2): exact in fp16; the factor is scale 2^24 / 2^5 / 2^9.
+// Codes times 32 (odd channels times 2): exact in fp16; the factor is scale 2^24 / 2^5 / 2^12.
 __device__ __forceinline__ void act_group_int8(uint2 w, float scale, int i, int tok, int grp, const ActDst &D, bool put) {
   constexpr uint32_t X32 = 0x50005000u, X2 = 0x40004000u;             // 32, 2
   constexpr uint32_t O32 = 0xF880F880u, O2 = 0xE880E880u;             // -1152 * 32, -1152 * 2
@@ -194,7 +200,7 @@ __device__ __forceinline__ void act_group_int8(uint2 w, float scale, int i, int 
   n += __shfl_xor_sync(0xffffffffu, n, 1);
   n += __shfl_xor_sync(0xffffffffu, n, 2);
   n += __shfl_xor_sync(0xffffffffu, n, 4);
-  if (put) D.put(tok, grp, i, p, scale * 1024.0f, (float)n * (scale * (1.0f / kActUnit)));
+  if (put) D.put(tok, grp, i, p, scale * (0x1p19f / kActUnit), (float)n * (scale * (1.0f / kActUnit)));
 }
 
 __device__ __forceinline__ void act_group_e4m3(uint2 w, float scale, int i, int tok, int grp, const ActDst &D, bool put) {
@@ -211,7 +217,7 @@ __device__ __forceinline__ void act_group_e4m3(uint2 w, float scale, int i, int 
   const uint4 p = make_uint4(hfma2(__byte_perm(h[0], h[2], 0x5410), X32, none), hfma2(__byte_perm(h[0], h[2], 0x7632), X2, none),
                              hfma2(__byte_perm(h[1], h[3], 0x5410), X32, none), hfma2(__byte_perm(h[1], h[3], 0x7632), X2, none));
   const float s = group_sum(sum8(v), 8);
-  if (put) D.put(tok, grp, i, p, scale * 1024.0f, s * (scale * (1.0f / kActUnit)));
+  if (put) D.put(tok, grp, i, p, scale * (0x1p19f / kActUnit), s * (scale * (1.0f / kActUnit)));
 }
 
 // ---------------------------------------------------------------------------------------

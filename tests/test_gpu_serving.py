@@ -374,6 +374,26 @@ def test_int4_linear_wide_range_activations():
     assert np.abs(f64(y[5:]) - ref[5:]).max() <= 1024 * 512 * 2.0 ** -149 + bound[5:].max()
 
 
+@pytest.mark.parametrize("T", [2, 7, 20])
+def test_int4_linear_largest_activations(T):
+    """Groups of bf16's largest numbers: what their sums with small weights come to is finite."""
+    import int4_expert_streaming_prerouter_b200 as e0
+    N, K = 32, 256
+    m = int4_mat(N, K, 64, 61)
+    m["scale"] = m["scale"] * 2.0 ** -16
+    m["min"] = m["min"] * 2.0 ** -16 * (torch.arange(N, device="cuda") % 2)[:, None]
+    m["min"] = m["min"].to(BF16)
+    m["codes"][:4] = 255
+    gen = torch.Generator().manual_seed(62)
+    x = torch.randn((T, K), generator=gen)
+    x[0] = (torch.randint(128, 256, (K,), generator=gen) * 2.0 ** 120)
+    x[1] = (torch.randint(250, 256, (K,), generator=gen) * 2.0 ** 120 * (1 - 2 * (torch.arange(K) % 2)))
+    x = x.to(BF16).cuda()
+    y = torch.empty((T, N), dtype=F32, device="cuda")
+    e0.Int4Linear(**m)(x, y=y)
+    check_linear(y, *linear_ref(m, 64, f64(x)))
+
+
 @pytest.mark.parametrize("T,K,N", [(5, 40960, 33), (8, 40960, 161), (7, 2112, 500), (8, 1 << 18, 17)])
 @pytest.mark.parametrize("fmt,xg", [("bf16", 0), ("int8", 64), ("e4m3", 0)])
 def test_int4_linear_five_to_eight_tokens(T, K, N, fmt, xg):
