@@ -355,6 +355,43 @@ def test_int4_linear_of_small_integers_is_exact(T, g):
     same(f64(y), (x.double().numpy() * np.repeat(scale.double().numpy(), g, 1)) @ (qs + mn).T)
 
 
+def integer_linear(T, N, K, g, fmt, r):
+    """Integers (8-bit activations times powers of two) with an integer adapter: (matrix, x, x_scale, c, y).  Every sum
+    of any of a row's terms is a multiple of 1/8 below 2^21, so fp32 holds it: the whole y, exact."""
+    rng = np.random.default_rng(T + K)
+    codes = rng.integers(0, 3, (N, K), dtype=np.uint8)
+    mins = rng.integers(-1, 2, (N, K // g))
+    x = rng.integers(-1, 2, (T, K))
+    A, B = rng.integers(-1, 2, (r, K)) * (rng.random((r, K)) < 0.25), rng.integers(-1, 2, (N, r))
+    c = 0.25
+    m = {"codes": torch.from_numpy(codes[:, 0::2] | codes[:, 1::2] << 4), "scale": torch.ones((N, K // g), dtype=BF16),
+         "min": torch.from_numpy(mins).to(BF16), "lora_A": torch.from_numpy(A).to(BF16), "lora_B": torch.from_numpy(B).to(BF16)}
+    xs, v = None, x.astype(np.float64)
+    if fmt != BF16:
+        xs = 2.0 ** rng.integers(-1, 2, (T, K // 64))
+        v = v * np.repeat(xs, 64, 1)
+        xs = torch.from_numpy(xs).float().cuda()
+    W = codes + np.repeat(mins, g, 1).astype(np.float64)
+    y = v @ W.T + c * (v @ A.T.astype(np.float64)) @ B.T.astype(np.float64)
+    size = np.abs(v) @ (codes + 1.0).T + c * (np.abs(v) @ np.abs(A).T) @ np.abs(B).T
+    assert size.max() < 2 ** 21
+    xt = torch.from_numpy(x).to(F32).to(fmt).cuda()
+    return {n: t.cuda() for n, t in m.items()}, xt, xs, c, y
+
+
+@pytest.mark.parametrize("K,N", [(4096, 161), (20480, 33), (33024, 20), (1 << 18, 17)])
+@pytest.mark.parametrize("T", [3, 8, 16, 32])
+@pytest.mark.parametrize("fmt,g", [(BF16, 64), (torch.int8, 128), (E4M3, 64)])
+def test_int4_linear_over_clusters_is_exact(T, K, N, fmt, g):
+    """K over the blocks of a cluster, ragged last ones among them, with an adapter: no block's share, no row's, no rank's
+    may be missing, doubled or another's."""
+    import int4_expert_streaming_prerouter_b200 as e0
+    m, x, xs, c, y = integer_linear(T, N, K, g, fmt, 4)
+    got = torch.full((T, N), float("nan"), dtype=F32, device="cuda")
+    e0.Int4Linear(**m, lora_scale=c)(x, x_scale=xs, y=got)
+    same(f64(got), y)
+
+
 def test_int4_linear_wide_range_activations():
     """Channels from 2^-60 to 2^100, groups of zeros, of subnormals; bf16 has no fp16 range."""
     import int4_expert_streaming_prerouter_b200 as e0
