@@ -16,6 +16,7 @@
 // TB/s; issue slots bound it, conversions and border tests), 64 rows of 4096 8.1 us,
 // one row 2.65 us (a launch and its latency).
 #pragma once
+#include "e0_bf16.cuh"
 #include "e0_device.cuh"
 
 namespace e0 {

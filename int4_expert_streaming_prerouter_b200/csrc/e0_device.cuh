@@ -39,10 +39,6 @@ __host__ __device__ inline Blob blob_of(int d, int I) {
 
 __device__ __forceinline__ float bf(uint32_t bits) { return __uint_as_float(bits << 16); }
 
-// the two bf16 numbers of a word
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
 __device__ __forceinline__ uint16_t f2bf(float f) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }

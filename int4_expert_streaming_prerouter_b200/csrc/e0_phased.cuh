@@ -36,6 +36,7 @@
 #pragma once
 #include <algorithm>
 #include <vector>
+#include "e0_bf16.cuh"
 #include "e0_device.cuh"
 #include "e0_kernels.cuh"
 #include "e0_decode.cuh"

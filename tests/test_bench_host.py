@@ -91,3 +91,10 @@ def test_code_digest_ignores_comments_and_layout_but_not_code(bench, tmp_path):
     assert bench.code_digest(str(a)) == bench.code_digest(str(b))
     assert bench.code_digest(str(a)) != bench.code_digest(str(c))
 
+
+
+@pytest.mark.parametrize("workload", ["decode_b1_l40", "prefill_t4096_l40"])
+def test_traffic_pins_hold(bench, workload):
+    """The committed ncu traffic belongs to the kernels as they are: their code is the code captured."""
+    nbytes, how = bench.kernel_traffic(workload)
+    assert nbytes is not None, how
