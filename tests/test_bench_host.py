@@ -98,3 +98,39 @@ def test_traffic_pins_hold(bench, workload):
     """The committed ncu traffic belongs to the kernels as they are: their code is the code captured."""
     nbytes, how = bench.kernel_traffic(workload)
     assert nbytes is not None, how
+
+
+RANGE = "one-launch decode: an activation beyond the fp16 operand range (|v| >= 65520); e0_debug_force_general ..."
+
+
+@pytest.mark.parametrize("chained,code,msg,excused", [
+    (True, -7, RANGE, True), (False, -7, RANGE, False), (True, -7, "routing rejected on the device", False),
+    (True, -6, "a bounded device wait gave up", False), (True, -2, "launch k_decode: out of memory", False), (True, -1, RANGE, False)])
+def test_a_decode_variant_excuses_the_fp16_range_alone(bench, chained, code, msg, excused):
+    import int4_expert_streaming_prerouter_b200 as e0
+    modes = []
+
+    def steps_in(mode):
+        modes.append(mode)
+        if mode != 2:
+            raise e0.E0Error(code, msg)
+        return 1.0, {}, 7
+    if not excused:
+        with pytest.raises(e0.E0Error):
+            bench._timed_variant(steps_in, 0, chained)
+        assert modes == [0]
+        return
+    timed, mode, kernel = bench._timed_variant(steps_in, 0, chained)
+    assert timed == (1.0, {}, 7) and mode == 2 and modes == [0, 2] and "fp16 operand range" in kernel
+
+
+def test_a_decode_variant_without_an_error_is_the_one_asked_for(bench):
+    timed, mode, kernel = bench._timed_variant(lambda mode: (2.0, {}, mode), 1, False)
+    assert timed == (2.0, {}, 1) and mode == 1 and "k_decode" in kernel
+
+
+def test_the_library_says_what_is_excused():
+    """The words that the excuse looks for are the library's own."""
+    src = open(os.path.join(ROOT, "int4_expert_streaming_prerouter_b200", "csrc", "e0_api.cu"), encoding="utf-8").read()
+    at = src.index("err & kDerrRange")
+    assert "E0_ERR_DEVICE" in src[at:at + 200] and "fp16 operand range" in src[at:at + 200]
