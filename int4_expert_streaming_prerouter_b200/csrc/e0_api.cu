@@ -1711,12 +1711,13 @@ extern "C" int e0_sync_status(e0_ctx *C) {
   CK(cudaMemset(C->err, 0, sizeof(int)));
   if (err & DERR_SLOT) return fail(E0_ERR_SLOT_MISMATCH, "a kernel found a pool slot holding another expert");
   if (err & DERR_TIMEOUT) return fail(E0_ERR_TIMEOUT, "a bounded device wait gave up");
-  if (err & (DERR_INDEX | DERR_DUP))
-    return fail(E0_ERR_DEVICE, "routing rejected on the device (%s)",
-                (err & DERR_INDEX) ? "expert index out of range" : "duplicate expert in a token");
+  // (before the routing: the infinities that it leaves behind can come back as NaN logits and as indices)
   if (err & kDerrRange)
     return fail(E0_ERR_DEVICE, "one-launch decode: an activation beyond the fp16 operand range (|v| >= 65520); "
                                "e0_debug_force_general(ctx, 1) runs such steps on the per-layer kernels");
+  if (err & (DERR_INDEX | DERR_DUP))
+    return fail(E0_ERR_DEVICE, "routing rejected on the device (%s)",
+                (err & DERR_INDEX) ? "expert index out of range" : "duplicate expert in a token");
   return E0_OK;
 }
 

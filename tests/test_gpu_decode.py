@@ -230,6 +230,28 @@ def test_one_launch_decode_reports_activations_beyond_fp16(cuda_ok):
     ctx.close()
 
 
+def test_one_launch_decode_names_the_range_before_the_routing(cuda_ok):
+    """An activation beyond fp16 can come back, over the layers that follow, as NaN logits and from them as an expert
+    index out of range; of the two errors the activation's is reported.  (Here each has a layer of its own: a norm
+    weight of 2e5, and one whose x is infinite.)"""
+    import int4_expert_streaming_prerouter_b200 as e0
+    ctx, lys, _ = build(SMALL, 95, 4)
+    ctx.debug_decode_mode(1)
+    h = bf16_tensor(synth.hidden(95, 0, SMALL.L, 1, SMALL.d), "cuda")
+    saved = lys[2]["norm_w"].clone()
+    lys[2]["norm_w"].fill_(float("inf"))
+    ctx.stack_decode(h, 0)
+    with pytest.raises(e0.E0Error, match="index out of range"):
+        ctx.sync_status()
+    lys[0]["norm_w"].fill_(2.0e5)
+    ctx.stack_decode(h, 0)
+    with pytest.raises(e0.E0Error, match="fp16 operand range") as ei:
+        ctx.sync_status()
+    assert ei.value.status == "DEVICE"
+    lys[2]["norm_w"].copy_(saved)
+    ctx.close()
+
+
 @pytest.mark.parametrize("B", [1, 5])
 def test_graph_replay_decode_matches_oracle(cuda_ok, B):
     """The decode step replayed as a captured CUDA graph of the per-layer kernels."""
