@@ -2322,8 +2322,8 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
   if (!coop || nsm < kFewWarps) return fail(E0_ERR_CUDA, "moe_layer_few: the device has no cooperative launch");
   // shared memory: phase 2 holds the rings and as many activation rows as the rest takes; phase 3
   // t_d, the results of every (token, slot), the sums of their activations and the rings
-  const int smem = most, rest = smem - (int)few_plan_bytes() - kFewZeroBytes - kFewRedBytes;
-  A.gu_rows = (rest - kFewRingBytes) / few_row_bytes(A.d);
+  const int smem = most, room = smem - (int)few_plan_bytes() - kFewZeroBytes, rest = room - kFewTdBytes;
+  A.gu_rows = (room - kFewRedBytes - kFewRingBytes) / few_row_bytes(A.d);
   const int places = T * (A.k + 1), sum_bytes = A.I / 64 * 4;
   A.out_bytes = std::max(16384, places * 64);
   const int most_sums = rest - A.out_bytes - 16 - kFewWarps * std::max(few_dn_ring(4), few_dn_ring(kFewSeg));
@@ -2333,7 +2333,7 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
     return fail(E0_ERR_INVALID_ARG, "moe_layer_few: dims too large for the shared memory");
   // tokens of a block in phase 1: 1, 2 or 4, until a block's share of the rows is 2 or less
   const int rows = D.n_experts + (any ? 2 * D.lora_rank : 0);
-  for (A.tpb = 1; A.tpb < 4 && (long long)rows * ((T + A.tpb - 1) / A.tpb) > 2 * nsm; A.tpb *= 2) {}
+  for (A.tpb = 1; A.tpb < kFewNorm && (long long)rows * ((T + A.tpb - 1) / A.tpb) > 2 * nsm; A.tpb *= 2) {}
   A.lora16 = !misaligned(Y.lora_Bg, 16) && !misaligned(Y.lora_Bu, 16) && !misaligned(Y.lora_Bd, 16);
   CK(cudaFuncSetAttribute(k_moe_few, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   void *args[] = {&A};

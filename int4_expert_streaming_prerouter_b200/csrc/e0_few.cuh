@@ -3,9 +3,10 @@
 // with its unmerged LoRA, weighted combine.
 //
 // Three phases with a grid-wide barrier between them, one block per SM:
-//   1. x = bf16(RMSNorm(bf16(h + delta))) of 8 tokens in shared memory; a share of the rows
+//   1. x = bf16(RMSNorm(bf16(h + delta))) of 1, 2 or 4 tokens in shared memory; a share of the rows
 //      [W_r; A_g; A_u] times them (mma.sync m16n8k16 bf16, K split over the warps).
-//   2. every block takes the top-k of all tokens and groups the (token, slot) assignments by
+//   2. every block takes the top-k of all tokens (of more than 16 tokens: of its own, and a barrier
+//      hands the result round) and groups the (token, slot) assignments by
 //      expert into segments of at most 8 tokens (the shared expert is one more expert
 //      that every token has); it then computes an equal share, by cost, of the tiles of 8
 //      intermediate indices of all segments: 8 gate and 8 up rows, SwiGLU, a = bf16(silu(g) u).
@@ -47,6 +48,7 @@ constexpr int kFewMaxA = kFewMaxT * (kMaxK + 1);                // assignments
 constexpr int kFewMaxSeg = kMaxE + 1 + kFewMaxA / 8;            // segments
 constexpr int kFewSeg = 8;                                      // tokens to a segment
 constexpr int kFewPad = 16;                                     // bytes between rows: 8 rows in distinct banks
+constexpr int kFewNorm = 4;                                     // tokens that a block of phase 1 norms, at most
 
 constexpr float kFewUnit = 64.0f;                               // what sums of products and of x are divided by
 
@@ -98,7 +100,8 @@ struct FewPlan {
 
 __host__ __device__ inline size_t few_plan_bytes() { return (sizeof(FewPlan) + 127) & ~(size_t)127; }
 constexpr int kFewZeroBytes = 128;
-constexpr int kFewRedBytes = kFewWarps * 16 * 16 * 4;            // partial sums of 16 warps: 16 rows x 16 tokens
+constexpr int kFewRedBytes = kFewWarps * 16 * kFewSeg * 4;       // partial sums of 16 warps: 16 rows x 8 tokens
+constexpr int kFewTdBytes = 16384;                              // parts of t_d (few_td): at most 128 rows of kMaxR
 // bytes of an activation row of phase 2 with its sums
 __host__ __device__ inline int few_row_bytes(int channels) { return channels * 2 + kFewPad + channels / 64 * 4; }
 
@@ -124,9 +127,9 @@ __device__ __forceinline__ uint4 natural_order(uint4 v) {
 // ---------------------------------------------------------------------------------------
 // int4 rows times bf16 columns: 16 rows, blocks of 256 channels (the last may be 128)
 // ---------------------------------------------------------------------------------------
-// Two forms, N tiles of tokens each (N is 1).  Pair: tiles of 4; the 8 columns of a matrix instruction
+// Two forms.  Pair: 4 tokens; the 8 columns of a matrix instruction
 // are 4 tokens restricted to one group of 64 and the same 4 restricted to the next, so a lane takes 16
-// consecutive bytes of a row and one fold serves both groups.  Wide: tiles of 8, 8 bytes of a row a
+// consecutive bytes of a row and one fold serves both groups.  Wide: 8 tokens, 8 bytes of a row a
 // lane, a fold per group.  (Segments of 5 to 8 tokens as two pair tiles: 61.3 us for 64 tokens over 16
 // experts, wide 56.3; segments of 16 would need rings that leave no room for the results.)  The accumulators of a lane are rows l / 4 and l / 4 + 8,
 // tokens 2 (l & 3), + 1 of a tile (pair: tokens 2 (l & 1), + 1, after adding lanes l and l + 2).
@@ -153,31 +156,24 @@ struct FewOps {
   int pitch, vp;              // bytes between rows of x and of v
 };
 
-// A lane's columns: N tiles of tokens (wide: 8 each, pair: 4), n tokens in all, at row `at` of x
-// and `vat` of the sums; advanced by 128 channels at a time.
-template <bool WIDE, int N>
+// A lane's columns: n tokens at row `at` of x and `vat` of the sums; advanced by 128 channels at a time.
+template <bool WIDE>
 struct FewCol {
-  uint32_t x[N], v0[N], v1[N];
+  uint32_t x, v0, v1;
   uint32_t step;              // bytes from 128 channels to the next: 256, or 0 at the zeros
   __device__ __forceinline__ void set(const FewOps &O, int at, int vat, int n, uint32_t zero) {
     const int lane = threadIdx.x & 31, t = lane & 3, c = lane >> 2;
     const bool mine = WIDE || (t >> 1) == (c >> 2);
     step = mine ? 256 : 0;
-#pragma unroll
-    for (int q = 0; q < N; q++) {
-      const int tok = WIDE ? 8 * q + c : 4 * q + (c & 3), pair = WIDE ? 8 * q + 2 * t : 4 * q + 2 * (t & 1);
-      x[q] = mine ? O.x + (at + min(tok, n - 1)) * O.pitch + (WIDE ? t * 32 : t * 64) : zero;
-      v0[q] = O.v + (vat + min(pair, n - 1)) * O.vp + (WIDE ? 0 : (t >> 1) * 4);
-      v1[q] = O.v + (vat + min(pair + 1, n - 1)) * O.vp + (WIDE ? 0 : (t >> 1) * 4);
-    }
+    const int tok = WIDE ? c : c & 3, pair = WIDE ? 2 * t : 2 * (t & 1);
+    x = mine ? O.x + (at + min(tok, n - 1)) * O.pitch + (WIDE ? t * 32 : t * 64) : zero;
+    v0 = O.v + (vat + min(pair, n - 1)) * O.vp + (WIDE ? 0 : (t >> 1) * 4);
+    v1 = O.v + (vat + min(pair + 1, n - 1)) * O.vp + (WIDE ? 0 : (t >> 1) * 4);
   }
   __device__ __forceinline__ void advance(uint32_t xs) {
-#pragma unroll
-    for (int q = 0; q < N; q++) {
-      x[q] += xs;
-      v0[q] += 8;
-      v1[q] += 8;
-    }
+    x += xs;
+    v0 += 8;
+    v1 += 8;
   }
 };
 
@@ -191,73 +187,60 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i) {
 }
 
 // One fold: the sums p of a group (pair: of a lane's group of two) with its scales and mins, the
-// low (sel 0x1044) or high (0x3244) halves of the words.  at: byte offset of the group's sums.
-template <int N>
-__device__ __forceinline__ void few_fold(const float (&p)[N][4], uint32_t wsa, uint32_t wma, uint32_t wsb, uint32_t wmb,
-                                         uint32_t sel, const uint32_t (&v0)[N], const uint32_t (&v1)[N], int at,
-                                         float (&acc)[N][4]) {
+// low (sel 0x1044) or high (0x3244) halves of the words.  v0, v1: addresses of the tokens' sums.
+__device__ __forceinline__ void few_fold(const float (&p)[4], uint32_t wsa, uint32_t wma, uint32_t wsb, uint32_t wmb,
+                                         uint32_t sel, uint32_t v0, uint32_t v1, float (&acc)[4]) {
   auto pick = [&](uint32_t w) { return __uint_as_float(__byte_perm(w, 0u, sel)); };
-  const float sa = pick(wsa), sb = pick(wsb), ma = pick(wma), mb = pick(wmb);
-#pragma unroll
-  for (int q = 0; q < N; q++) {
-    const float x0 = lds32(v0[q] + at), x1 = lds32(v1[q] + at);
-    acc[q][0] = fmaf(sa, p[q][0], fmaf(ma, x0, acc[q][0]));
-    acc[q][1] = fmaf(sa, p[q][1], fmaf(ma, x1, acc[q][1]));
-    acc[q][2] = fmaf(sb, p[q][2], fmaf(mb, x0, acc[q][2]));
-    acc[q][3] = fmaf(sb, p[q][3], fmaf(mb, x1, acc[q][3]));
-  }
+  const float sa = pick(wsa), sb = pick(wsb), ma = pick(wma), mb = pick(wmb), x0 = lds32(v0), x1 = lds32(v1);
+  acc[0] = fmaf(sa, p[0], fmaf(ma, x0, acc[0]));
+  acc[1] = fmaf(sa, p[1], fmaf(ma, x1, acc[1]));
+  acc[2] = fmaf(sb, p[2], fmaf(mb, x0, acc[2]));
+  acc[3] = fmaf(sb, p[3], fmaf(mb, x1, acc[3]));
 }
 
 // 128 channels: the lane's codes at shared address w0 (pair: 16 bytes; wide: 8 bytes, those of the
 // second group at w1), `HALF` bytes on those of 8 rows further; scale words (s, m of rows l / 4,
 // l / 4 + 8) of the two groups.
-template <bool WIDE, int N, int HALF>
+template <bool WIDE, int HALF>
 __device__ __forceinline__ void few_mul128(uint32_t w0, uint32_t w1, uint32_t wsa, uint32_t wma, uint32_t wsb, uint32_t wmb,
-                                           const FewCol<WIDE, N> &X, float (&acc)[N][4]) {
+                                           const FewCol<WIDE> &X, float (&acc)[4]) {
   const int t = threadIdx.x & 3;
   if (WIDE) {
 #pragma unroll
     for (int g = 0; g < 2; g++) {
       const uint2 wa = lds64(g ? w1 : w0), wb = lds64((g ? w1 : w0) + HALF);
-      float p[N][4];
+      float p[4];
 #pragma unroll
       for (int w = 0; w < 2; w++) {
         const uint32_t xa = w ? wa.y : wa.x, xb = w ? wb.y : wb.x;
         const uint32_t a0 = code_pair(xa, 0), a1 = code_pair(xa, 1), a2 = code_pair(xa, 2), a3 = code_pair(xa, 3);
         const uint32_t b0 = code_pair(xb, 0), b1 = code_pair(xb, 1), b2 = code_pair(xb, 2), b3 = code_pair(xb, 3);
-#pragma unroll
-        for (int q = 0; q < N; q++) {
-          const uint4 x = lds128(X.x[q] + g * 128 + w * 16);
-          if (w == 0) mma_bf16_first(p[q], a0, b0, a1, b1, x.x, x.y);
-          else mma_bf16_acc(p[q], a0, b0, a1, b1, x.x, x.y);
-          mma_bf16_acc(p[q], a2, b2, a3, b3, x.z, x.w);
-        }
+        const uint4 x = lds128(X.x + g * 128 + w * 16);
+        if (w == 0) mma_bf16_first(p, a0, b0, a1, b1, x.x, x.y);
+        else mma_bf16_acc(p, a0, b0, a1, b1, x.x, x.y);
+        mma_bf16_acc(p, a2, b2, a3, b3, x.z, x.w);
       }
-      few_fold<N>(p, wsa, wma, wsb, wmb, g ? 0x3244u : 0x1044u, X.v0, X.v1, g * 4, acc);
+      few_fold(p, wsa, wma, wsb, wmb, g ? 0x3244u : 0x1044u, X.v0 + g * 4, X.v1 + g * 4, acc);
     }
   } else {
     const uint4 wa = lds128(w0), wb = lds128(w0 + HALF);
     // (two chains of dependent instructions, joined at the fold)
-    static_assert(WIDE || N == 1, "one tile of tokens");
-    float p[N][4], p2[4];
+    float p[4], p2[4];
 #pragma unroll
     for (int w = 0; w < 4; w++) {
       const uint32_t xa = w == 0 ? wa.x : w == 1 ? wa.y : w == 2 ? wa.z : wa.w;
       const uint32_t xb = w == 0 ? wb.x : w == 1 ? wb.y : w == 2 ? wb.z : wb.w;
       const uint32_t a0 = code_pair(xa, 0), a1 = code_pair(xa, 1), a2 = code_pair(xa, 2), a3 = code_pair(xa, 3);
       const uint32_t b0 = code_pair(xb, 0), b1 = code_pair(xb, 1), b2 = code_pair(xb, 2), b3 = code_pair(xb, 3);
-#pragma unroll
-      for (int q = 0; q < N; q++) {
-        const uint4 x = lds128(X.x[q] + w * 16);
-        if (w == 0) mma_bf16_first(p[q], a0, b0, a1, b1, x.x, x.y);
-        else mma_bf16_acc(p[q], a0, b0, a1, b1, x.x, x.y);
-        if (w == 0) mma_bf16_first(p2, a2, b2, a3, b3, x.z, x.w);
-        else mma_bf16_acc(p2, a2, b2, a3, b3, x.z, x.w);
-      }
+      const uint4 x = lds128(X.x + w * 16);
+      if (w == 0) mma_bf16_first(p, a0, b0, a1, b1, x.x, x.y);
+      else mma_bf16_acc(p, a0, b0, a1, b1, x.x, x.y);
+      if (w == 0) mma_bf16_first(p2, a2, b2, a3, b3, x.z, x.w);
+      else mma_bf16_acc(p2, a2, b2, a3, b3, x.z, x.w);
     }
 #pragma unroll
-    for (int i = 0; i < 4; i++) p[0][i] += p2[i];
-    few_fold<N>(p, wsa, wma, wsb, wmb, t >> 1 ? 0x3244u : 0x1044u, X.v0, X.v1, 0, acc);
+    for (int i = 0; i < 4; i++) p[i] += p2[i];
+    few_fold(p, wsa, wma, wsb, wmb, t >> 1 ? 0x3244u : 0x1044u, X.v0, X.v1, acc);
   }
 }
 
@@ -319,7 +302,7 @@ __device__ __forceinline__ void few_phase1(const FewArgs &A, FewPlan &P, uint8_t
   const int tid = threadIdx.x, lane = tid & 31, warp = warp_id(), d = A.d;
   const FewTok K(A);
   const int pitch = d * 2 + kFewPad, vbytes = d / 64 * 4;
-  uint8_t *hs = area + 8 * (pitch + vbytes);
+  uint8_t *hs = area + kFewNorm * (pitch + vbytes);
   // the first 16 rows are fetched before they are needed: 4 chunks of 32 channels a warp
   const int R = A.E + (A.Ag ? 2 * A.r : 0);
   const int r0 = (int)((long long)R * K.member / K.members), r1 = (int)((long long)R * (K.member + 1) / K.members);
@@ -346,8 +329,8 @@ __device__ __forceinline__ void few_phase1(const FewArgs &A, FewPlan &P, uint8_t
     }
   };
   if (r0 < r1) fetch(r0, b0);
-  // 16 warps over nt tokens, 2 to 16 warps each
-  const int wpt = K.nt > 4 ? 2 : K.nt > 2 ? 4 : K.nt > 1 ? 8 : 16, tok = warp / wpt, sub = warp % wpt;
+  // 16 warps over nt tokens, 4 to 16 warps each
+  const int wpt = K.nt > 2 ? 4 : K.nt > 1 ? 8 : 16, tok = warp / wpt, sub = warp % wpt;
   const bool mine = tok < K.nt;
   uint8_t *xs = area + tok * pitch;
   const int c0 = (sub * 32 + lane) * 8, cl = min(c0, d - 8);
@@ -392,7 +375,7 @@ __device__ __forceinline__ void few_phase1(const FewArgs &A, FewPlan &P, uint8_t
       v = group_sum(v * (1.0f / kFewUnit), 8);                          // d is a multiple of 256: whole warps
       const uint4 xv = operand_order(o);
       *reinterpret_cast<uint4 *>(xs + c * 2) = xv;
-      if ((lane & 7) == 0) *reinterpret_cast<float *>(area + 8 * pitch + tok * vbytes + c / 64 * 4) = v;
+      if ((lane & 7) == 0) *reinterpret_cast<float *>(area + kFewNorm * pitch + tok * vbytes + c / 64 * 4) = v;
       if (K.member == 0) {
         *reinterpret_cast<uint4 *>(A.xb + (size_t)(K.t0 + tok) * d + c) = xv;
         if ((lane & 7) == 0) A.xv[(size_t)(K.t0 + tok) * (d / 64) + c / 64] = v;
@@ -438,7 +421,7 @@ __device__ __forceinline__ void few_phase1(const FewArgs &A, FewPlan &P, uint8_t
 __device__ __forceinline__ void few_residual(const FewArgs &A, const uint8_t *area) {
   const FewTok K(A);
   if (K.member) return;
-  const uint8_t *hs = area + 8 * (A.d * 2 + kFewPad + A.d / 64 * 4);
+  const uint8_t *hs = area + kFewNorm * (A.d * 2 + kFewPad + A.d / 64 * 4);
 #pragma unroll 1
   for (int c = threadIdx.x * 8; c < K.nt * A.d; c += kFewThreads * 8)
     *reinterpret_cast<uint4 *>(A.h_out + (size_t)K.t0 * A.d + c) = *reinterpret_cast<const uint4 *>(hs + c * 2);
@@ -672,20 +655,20 @@ __device__ __noinline__ void few_emit(const FewPlan &P, int s, int i8, int tok, 
   }
 }
 
-// The join of a team's partial sums (red: [warp][16 rows][16 tokens]).
+// The join of a team's partial sums (red: [warp][16 rows][8 tokens]).
 __device__ __noinline__ void few_join(const FewPlan &P, int s, int i8, int wk, int team, int sub, const float *red) {
   const int lane = threadIdx.x & 31, n = P.seg_n[s];
   bar_team(wk, team);
   // 4 tokens of 8 indices to a warp at a time: lane = token + 4 index
-  const float *base = red + team * wk * 256 + (lane >> 2) * 16;
+  const float *base = red + team * wk * 16 * kFewSeg + (lane >> 2) * kFewSeg;
 #pragma unroll 1
   for (int t0 = sub * 4; t0 < n; t0 += wk * 4) {
     const int tok = t0 + (lane & 3), tk = min(tok, n - 1);
     float g = 0.f, u = 0.f;
 #pragma unroll 2
     for (int w = 0; w < wk; w++) {
-      g += base[w * 256 + tk];
-      u += base[w * 256 + 128 + tk];
+      g += base[w * 16 * kFewSeg + tk];
+      u += base[w * 16 * kFewSeg + 8 * kFewSeg + tk];
     }
     few_emit(P, s, i8, tok, g, u);
   }
@@ -695,12 +678,12 @@ __device__ __noinline__ void few_join(const FewPlan &P, int s, int i8, int wk, i
 // Streams a warp's tiles, blocks ahead across the end of a tile too.  Down: rows r0.. (nr of
 // them).  Sums go through few_emit / few_join, or (down) to
 // out[place][16].
-template <bool GU, bool WIDE, int N>
+template <bool GU, bool WIDE>
 __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, const FewOps &O, int p0, FewCursor<GU> C,
                                            int step, int per, const FewPart &W, int r0, int nr, uint32_t zero,
                                            uint32_t ring, float *out) {
   if (C.left <= 0) return;
-  constexpr int TOK = N * (WIDE ? 8 : 4), STAGE = GU ? kFewStage : few_dn_stage(TOK);
+  constexpr int TOK = WIDE ? 8 : 4, STAGE = GU ? kFewStage : few_dn_stage(TOK);
   const int lane = threadIdx.x & 31, t = lane & 3, r = lane >> 2, warp = warp_id();
   constexpr int stages = GU ? kFewDepth : few_dn_depth(TOK);
   const int K = GU ? A.d : A.I;
@@ -767,7 +750,7 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
         const uint32_t xd = lst + kFewDnHead + (lane >> 4) * kFewDnRow + (lane & 15) * 16;
 #pragma unroll
         for (int i = 0; i < TOK / 2; i++)
-          if (2 * i < xn) {                       // (the whole warp; an odd last token is copied twice)
+          if (2 * i < xn) {                       // (the whole warp; with an odd last token half of it)
             if ((lane >> 4) + 2 * i < xn) cp_async16(xd + 2 * i * kFewDnRow, xp[GU ? 0 : i]);
             xp[GU ? 0 : i] += 256;
           }
@@ -789,20 +772,15 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
   const int swz = GU ? row_swz(r) : r & 2, pitch = GU ? 128 : 64;
   const uint32_t o0 = r * pitch + (((WIDE ? t >> 1 : t) ^ swz) << 4) + (WIDE ? (t & 1) * 8 : 0);
   const uint32_t o1 = r * pitch + (((2 + (t >> 1)) ^ swz) << 4) + (t & 1) * 8;
-  FewCol<WIDE, N> X;
+  FewCol<WIDE> X;
 #pragma unroll 1
   for (; C.left > 0; C.next(step, per)) {
     const int n = P.seg_n[C.s], at = P.seg_at[C.s];
-    float acc[N][4];
-#pragma unroll
-    for (int q = 0; q < N; q++) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
     X.set(O, GU ? at - p0 : 0, at - p0, n, zero);
-#pragma unroll
-    for (int q = 0; q < N; q++) {
-      X.x[q] += GU ? 2 * W.b0 * X.step : 0;
-      X.v0[q] += (GU ? 16 : 8) * W.b0;
-      X.v1[q] += (GU ? 16 : 8) * W.b0;
-    }
+    X.x += GU ? 2 * W.b0 * X.step : 0;
+    X.v0 += (GU ? 16 : 8) * W.b0;
+    X.v1 += (GU ? 16 : 8) * W.b0;
 #pragma unroll 1
     for (int b = W.b0; b < W.b1; b++) {
       cp_async_wait_but<stages - 2>();
@@ -813,44 +791,39 @@ __device__ __forceinline__ void few_stream(const FewArgs &A, const FewPlan &P, c
       const uint32_t sc = sl + r * 32 + at128 * 4;
       if (GU) {
         const uint2 s0 = lds64(sc), m0 = lds64(sc + 16), s8 = lds64(sc + 256), m8 = lds64(sc + 272);
-        few_mul128<WIDE, N, 1024>(st + o0, st + o1, s0.x, m0.x, s8.x, m8.x, X, acc);
+        few_mul128<WIDE, 1024>(st + o0, st + o1, s0.x, m0.x, s8.x, m8.x, X, acc);
         X.advance(X.step);
         // chunk c + 4 lies 64 bytes from chunk c, on the side that the permutation leaves
-        few_mul128<WIDE, N, 1024>(st + (o0 ^ 64), st + (o1 ^ 64), s0.y, m0.y, s8.y, m8.y, X, acc);
+        few_mul128<WIDE, 1024>(st + (o0 ^ 64), st + (o1 ^ 64), s0.y, m0.y, s8.y, m8.y, X, acc);
         X.advance(X.step);
       } else {
-        FewCol<WIDE, N> Y = X;            // the stage's own columns
-        const uint32_t xbase = X.step ? st : 0u;
-#pragma unroll
-        for (int q = 0; q < N; q++) Y.x[q] = X.x[q] + xbase;
-        few_mul128<WIDE, N, 512>(st + o0, st + o1, lds32u(sc), lds32u(sc + 16), lds32u(sc + 256), lds32u(sc + 272), Y, acc);
+        FewCol<WIDE> Y = X;               // the stage's own columns
+        Y.x += X.step ? st : 0u;
+        few_mul128<WIDE, 512>(st + o0, st + o1, lds32u(sc), lds32u(sc + 16), lds32u(sc + 256), lds32u(sc + 272), Y, acc);
         X.advance(0);
       }
       st = st + STAGE == end ? stages_at : st + STAGE;
     }
     // pair: lanes l and l + 2 hold the same two tokens and take one each; wide: both tokens
+    if (!WIDE)
 #pragma unroll
-    for (int q = 0; q < N; q++) {
-      if (!WIDE)
+      for (int i = 0; i < 4; i++) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], 2);
 #pragma unroll
-        for (int i = 0; i < 4; i++) acc[q][i] += __shfl_xor_sync(0xffffffffu, acc[q][i], 2);
-#pragma unroll
-      for (int j = 0; j < (WIDE ? 2 : 1); j++) {
-        const int odd = WIDE ? j : t >> 1, tok = WIDE ? 8 * q + 2 * t + j : 4 * q + 2 * (t & 1) + odd;
-        const float va = odd ? acc[q][1] : acc[q][0], vb = odd ? acc[q][3] : acc[q][2];
-        if (!GU) {
-          if (tok < n) {
-            float *p = out + (size_t)(at + tok) * 16 + r;
-            p[0] = va;
-            p[8] = vb;
-          }
-        } else if (W.wk == 1) {
-          few_emit(P, C.s, C.i, tok, va, vb);
-        } else if (tok < n) {
-          float *p = out + warp * 256 + r * 16 + tok;
+    for (int j = 0; j < (WIDE ? 2 : 1); j++) {
+      const int odd = WIDE ? j : t >> 1, tok = WIDE ? 2 * t + j : 2 * (t & 1) + odd;
+      const float va = odd ? acc[1] : acc[0], vb = odd ? acc[3] : acc[2];
+      if (!GU) {
+        if (tok < n) {
+          float *p = out + (size_t)(at + tok) * 16 + r;
           p[0] = va;
-          p[128] = vb;
+          p[8] = vb;
         }
+      } else if (W.wk == 1) {
+        few_emit(P, C.s, C.i, tok, va, vb);
+      } else if (tok < n) {
+        float *p = out + (warp * 16 + r) * kFewSeg + tok;
+        p[0] = va;
+        p[8 * kFewSeg] = vb;
       }
     }
     if (GU && W.wk > 1) few_join(P, C.s, C.i, W.wk, W.team, W.sub, out);
@@ -925,11 +898,11 @@ __device__ __forceinline__ void few_phase2(const FewArgs &A, const FewPlan &P, u
     FewPart W;
     if (n4 < s1) {
       const int step = share(n4, P.nseg, C, W);
-      few_stream<true, true, 1>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
+      few_stream<true, true>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
     }
     if (s0 < n4) {
       const int step = share(0, n4, C, W);
-      few_stream<true, false, 1>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
+      few_stream<true, false>(A, P, O, p0, C, step, per, W, 0, 0, zero, ring, red);
     }
     s0 = s1;
   }
@@ -938,7 +911,8 @@ __device__ __forceinline__ void few_phase2(const FewArgs &A, const FewPlan &P, u
 // ---------------------------------------------------------------------------------------
 // Phase 3
 // ---------------------------------------------------------------------------------------
-// t_d = A_d a_s of every token: 16 rows by 8 tokens, K split over the warps that are left
+// t_d = A_d a_s of every token: 16 rows by 8 tokens, K split over the warps that are left.  td holds a part's T rows
+// of kMaxR behind another's: split * T <= 16 / ntt * 8 ntt = 128 rows.
 __device__ __forceinline__ int few_td(const FewArgs &A, float *td) {
   const int lane = threadIdx.x & 31, warp = warp_id(), k1 = A.k + 1;
   const int rt = (A.r + 15) / 16, ntt = (A.T + 7) / 8, nb = A.I / 32;
@@ -968,8 +942,8 @@ __device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, u
   const int lo = (int)((long long)A.d * blockIdx.x / gridDim.x), hi = (int)((long long)A.d * (blockIdx.x + 1) / gridDim.x);
   if (lo >= hi) return;
   const int G = A.I / 64, NB = A.I / 128, k1 = A.k + 1, nplace = P.nplace;
-  float *td = reinterpret_cast<float *>(area), *out = reinterpret_cast<float *>(area + kFewRedBytes);
-  float *sums = reinterpret_cast<float *>(area + kFewRedBytes + A.out_bytes);
+  float *td = reinterpret_cast<float *>(area), *out = reinterpret_cast<float *>(area + kFewTdBytes);
+  float *sums = reinterpret_cast<float *>(area + kFewTdBytes + A.out_bytes);
   const uint32_t ring = smem_at(sums) + ((A.dn_rows * G * 4 + 15) & ~15) + warp * A.dn_ring;
   bool first = true;
 #pragma unroll 1
@@ -1027,8 +1001,8 @@ __device__ __forceinline__ void few_phase3(const FewArgs &A, const FewPlan &P, u
       const FewOps O{kFewDnHead, smem_at(sums), kFewDnRow, G * 4};
       const int m4 = max(s0, min(s1, P.n4));
       auto cursor = [&](int a, int b) { return FewCursor<false>{a + team, 0, (b - a - team + step - 1) >> (4 - lg)}; };
-      if (m4 < s1) few_stream<false, true, 1>(A, P, O, p0, cursor(m4, s1), step, 0, W, r0, nr, zero, ring, o);
-      if (s0 < m4) few_stream<false, false, 1>(A, P, O, p0, cursor(s0, m4), step, 0, W, r0, nr, zero, ring, o);
+      if (m4 < s1) few_stream<false, true>(A, P, O, p0, cursor(m4, s1), step, 0, W, r0, nr, zero, ring, o);
+      if (s0 < m4) few_stream<false, false>(A, P, O, p0, cursor(s0, m4), step, 0, W, r0, nr, zero, ring, o);
       s0 = s1;
     }
     __syncthreads();
