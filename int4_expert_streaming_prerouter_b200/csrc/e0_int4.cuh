@@ -154,7 +154,7 @@ __device__ __forceinline__ void q8_values(uint2 w, bool e4m3, float (&v)[8]) {
 
 // Eight lanes (i = 0..7) bring one token's group of 64 channels, 8 each (16 bytes of bf16, or 8 of
 // codes with their scale), into place.  All 32 lanes of the warp call these together.
-__device__ __forceinline__ void act_group_bf16(uint4 w, int i, int tok, int grp, const ActDst &D, bool put) {
+__device__ __forceinline__ void act_group_bf16(uint4 w, int i, int tok, int grp, const ActDst &D) {
   const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
   float v[8], m = 0.f;
 #pragma unroll
@@ -177,8 +177,7 @@ __device__ __forceinline__ void act_group_bf16(uint4 w, int i, int tok, int grp,
   const float s8 = fmaf(16.0f, (v[1] + v[3]) + (v[5] + v[7]), (v[0] + v[2]) + (v[4] + v[6]));
   const float s = group_sum(s8, 8) * 0x1p-24f * factor;
   static_assert(kActUnit == 4096.0f, "factor is 2^(eb - 142) 2^24 / kActUnit, the factor of the sum 2^(eb - 142) / kActUnit");
-  if (put)
-    D.put(tok, grp, i, make_uint4(half2_of(v[0], v[4]), half2_of(v[1], v[5]), half2_of(v[2], v[6]), half2_of(v[3], v[7])), factor, s);
+  D.put(tok, grp, i, make_uint4(half2_of(v[0], v[4]), half2_of(v[1], v[5]), half2_of(v[2], v[6]), half2_of(v[3], v[7])), factor, s);
 }
 
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
@@ -188,7 +187,7 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
 }
 
 // Codes times 32 (odd channels times 2): exact in fp16; the factor is scale 2^24 / 2^5 / 2^12.
-__device__ __forceinline__ void act_group_int8(uint2 w, float scale, int i, int tok, int grp, const ActDst &D, bool put) {
+__device__ __forceinline__ void act_group_int8(uint2 w, float scale, int i, int tok, int grp, const ActDst &D) {
   constexpr uint32_t X32 = 0x50005000u, X2 = 0x40004000u;             // 32, 2
   constexpr uint32_t O32 = 0xF880F880u, O2 = 0xE880E880u;             // -1152 * 32, -1152 * 2
   // a byte b + 128 under 0x64 is the fp16 number 1024 + 128 + b
@@ -200,10 +199,10 @@ __device__ __forceinline__ void act_group_int8(uint2 w, float scale, int i, int 
   n += __shfl_xor_sync(0xffffffffu, n, 1);
   n += __shfl_xor_sync(0xffffffffu, n, 2);
   n += __shfl_xor_sync(0xffffffffu, n, 4);
-  if (put) D.put(tok, grp, i, p, scale * (0x1p19f / kActUnit), (float)n * (scale * (1.0f / kActUnit)));
+  D.put(tok, grp, i, p, scale * (0x1p19f / kActUnit), (float)n * (scale * (1.0f / kActUnit)));
 }
 
-__device__ __forceinline__ void act_group_e4m3(uint2 w, float scale, int i, int tok, int grp, const ActDst &D, bool put) {
+__device__ __forceinline__ void act_group_e4m3(uint2 w, float scale, int i, int tok, int grp, const ActDst &D) {
   constexpr uint32_t X32 = 0x50005000u, X2 = 0x40004000u;
   uint32_t h[4];
   float v[8];
@@ -217,7 +216,7 @@ __device__ __forceinline__ void act_group_e4m3(uint2 w, float scale, int i, int 
   const uint4 p = make_uint4(hfma2(__byte_perm(h[0], h[2], 0x5410), X32, none), hfma2(__byte_perm(h[0], h[2], 0x7632), X2, none),
                              hfma2(__byte_perm(h[1], h[3], 0x5410), X32, none), hfma2(__byte_perm(h[1], h[3], 0x7632), X2, none));
   const float s = group_sum(sum8(v), 8);
-  if (put) D.put(tok, grp, i, p, scale * (0x1p19f / kActUnit), s * (scale * (1.0f / kActUnit)));
+  D.put(tok, grp, i, p, scale * (0x1p19f / kActUnit), s * (scale * (1.0f / kActUnit)));
 }
 
 // ---------------------------------------------------------------------------------------
@@ -237,7 +236,7 @@ __device__ __forceinline__ void act_group_e4m3(uint2 w, float scale, int i, int 
 // reads and the matrix instructions.  Ring depths 3 and 2: pair 18.3 us at
 // one token and 65521 rows, with a depth of 2 19.9 (4: no change); wide needs the room for activations.
 //
-// Two forms.  Pair (up to 4 tokens, N tiles of 4): the 8 columns of a matrix instruction are 4 tokens
+// Two forms.  Pair (up to 4 tokens, N = 1): the 8 columns of a matrix instruction are 4 tokens
 // restricted to one group of 64 and the same 4 restricted to the next (zeros elsewhere), so a lane
 // takes 16 consecutive bytes of a row and one fold serves both groups.  Wide (N tiles of 8 tokens): 8
 // bytes of a row a lane, a fold per group.  The accumulators of a lane are rows l / 4 and l / 4 + 8,
@@ -379,7 +378,7 @@ __device__ __forceinline__ void lin_mul128(uint32_t w0, uint32_t w1, uint32_t ws
   }
 }
 
-// y[tok][row] from the whole sum, with the LoRA where it has not been added yet
+// y[tok][row] = v
 __device__ __forceinline__ void lin_store(const LinearArgs &L, int tok, int row, float v) {
   const long long at = (long long)tok * L.y_stride + row;
   if (L.y_f32)
@@ -584,9 +583,9 @@ __global__ void __launch_bounds__(kLinThreads, 1) k_int4_linear(const __grid_con
 #pragma unroll
           for (int j = 0; j < 4; j++) {
             if (tk[j] >= nt) break;                     // (the same for the whole warp)
-            if (L.x_type == ACT_BF16) act_group_bf16(w[j], i, tk[j], gr[j], D, true);
-            else if (L.x_type == ACT_INT8) act_group_int8(make_uint2(w[j].x, w[j].y), s[j], i, tk[j], gr[j], D, true);
-            else act_group_e4m3(make_uint2(w[j].x, w[j].y), s[j], i, tk[j], gr[j], D, true);
+            if (L.x_type == ACT_BF16) act_group_bf16(w[j], i, tk[j], gr[j], D);
+            else if (L.x_type == ACT_INT8) act_group_int8(make_uint2(w[j].x, w[j].y), s[j], i, tk[j], gr[j], D);
+            else act_group_e4m3(make_uint2(w[j].x, w[j].y), s[j], i, tk[j], gr[j], D);
           }
         } while (ct < nt);
       }
