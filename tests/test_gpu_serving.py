@@ -220,6 +220,25 @@ def test_add_rmsnorm_rows_farther_apart_than_32_bits():
     same(f64(out[1]), x)
 
 
+def exact_root_rows(d, rng):
+    """Rows of a and b whose mean square is c^2, and gammas that are multiples of c: x = h gamma / c is a number of 9 or
+    10 bits, so ties between bf16 values abound.  (h, gamma) per (a, b, c)."""
+    for a, b, c in ((1, 7, 5), (7, 17, 13), (7, 23, 17), (17, 31, 25), (1, 41, 29), (23, 47, 37), (31, 49, 41), (49, 71, 61)):
+        h = np.where(np.arange(d) % 2, a, b) * 2.0 ** rng.integers(-9, 9, (4, 1)) * rng.choice([-1, 1], (4, d))
+        yield h, c * rng.integers(1, 255 // c + 1, d) * 2.0 ** rng.integers(-6, 7, d)
+
+
+@pytest.mark.parametrize("d", [64, 1000, 2048, 20002])
+def test_add_rmsnorm_ties(d):
+    """Quotients that are exactly halfway between two bf16 values go to the even one."""
+    ties = 0
+    for h, gamma in exact_root_rows(d, np.random.default_rng(d)):
+        x = h * gamma / np.sqrt((h * h).mean(1, keepdims=True))
+        ties += (np.abs(np.ldexp(np.frexp(x)[0], 9)) % 2 == 1).sum()
+        run_norm(torch.from_numpy(h).to(BF16).cuda(), torch.from_numpy(gamma).to(BF16).cuda(), None, 0.0, None, 0)
+    assert ties > d
+
+
 def wide_range_rows(d=2048):
     """Rows whose norm leaves fp32's normal range on the way: (h, gamma)."""
     rng = np.random.default_rng(7)
@@ -457,6 +476,26 @@ def test_int4_linear_token_that_is_not_finite_stays_alone(T):
     lin(x, y=y)
     assert not torch.isfinite(y[1:3]).any()
     assert torch.equal(y[:1], clean[:1]) and torch.equal(y[3:], clean[3:])
+
+
+@pytest.mark.parametrize("T", [3, 7, 20])
+@pytest.mark.parametrize("fmt", [torch.int8, E4M3])
+def test_int4_linear_scales_that_are_not_finite_stay_alone(T, fmt):
+    """A group without a finite largest, as add_rmsnorm writes it: codes 0, scale NaN; and scales of 0 and infinity."""
+    import int4_expert_streaming_prerouter_b200 as e0
+    m = int4_mat(50, 512, 64, 8, r=4)
+    x, s, _ = acts(T, 512, "int8" if fmt == torch.int8 else "e4m3", 64, 9)
+    lin = e0.Int4Linear(**m)
+    clean = lin(x, x_scale=s, y=torch.empty((T, 50), dtype=F32, device="cuda"))
+    s[1, 3] = float("nan")
+    s[2, 7] = float("inf")
+    x.view(torch.int8)[1, 192:256] = 0
+    y = lin(x, x_scale=s, y=torch.empty_like(clean))
+    assert not torch.isfinite(y[1:3]).any()
+    assert torch.equal(y[:1], clean[:1]) and torch.equal(y[3:], clean[3:])
+    x.view(torch.int8)[0] = 0
+    s[0] = 0
+    assert (lin(x, x_scale=s, y=y)[0] == 0).all()
 
 
 def test_int4_linear_rows_apart():
