@@ -2331,9 +2331,12 @@ extern "C" int e0_moe_layer_few(const e0_dims *dims, const e0_layer *layer, cons
   A.dn_ring = (rest - A.out_bytes - (A.dn_rows * sum_bytes + 15) / 16 * 16) / kFewWarps / 16 * 16;
   if (A.gu_rows < kFewSeg || A.dn_rows < std::min(places, kFewSeg))
     return fail(E0_ERR_INVALID_ARG, "moe_layer_few: dims too large for the shared memory");
-  // tokens of a block in phase 1: 1, 2 or 4, until a block's share of the rows is 2 or less
+  // tokens of a block in phase 1: 1, 2 or 4, until a block's share of the rows is 2 or less and every token has a
+  // block (64 tokens by 4 are 16 blocks, as many as a device must have SMs)
   const int rows = D.n_experts + (any ? 2 * D.lora_rank : 0);
-  for (A.tpb = 1; A.tpb < kFewNorm && (long long)rows * ((T + A.tpb - 1) / A.tpb) > 2 * nsm; A.tpb *= 2) {}
+  static_assert(kFewMaxT / kFewNorm <= kFewWarps, "fewer SMs than kFewWarps are refused above");
+  const auto blocks = [&]() { return (T + A.tpb - 1) / A.tpb; };
+  for (A.tpb = 1; A.tpb < kFewNorm && ((long long)rows * blocks() > 2 * nsm || blocks() > nsm); A.tpb *= 2) {}
   A.lora16 = !misaligned(Y.lora_Bg, 16) && !misaligned(Y.lora_Bu, 16) && !misaligned(Y.lora_Bd, 16);
   CK(cudaFuncSetAttribute(k_moe_few, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   void *args[] = {&A};
