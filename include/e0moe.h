@@ -331,7 +331,8 @@ typedef struct {
 } e0_int4_mat;
 
 /* y = W x + lora_scale B (A x) for T tokens ([G] "Birleştirilmemiş Adaptör Yürütme": the
- * adapter stays unmerged).  Products are exact, sums fp32, y rounded once.  A token with a
+ * adapter stays unmerged).  Products are exact (but for bf16 channels below 2^-28 of the largest of their 64,
+ * off by 2^-36 of that one at most), sums fp32, y rounded once.  A token with a
  * NaN or an infinity in x has outputs that are not finite; other tokens are not affected.
  * x         [T, k]: bf16, or 8-bit codes (int8, e4m3) times x_scale; rows x_stride elements
  *           apart, a multiple of 8; 16-byte aligned (8-bit: 8).

@@ -15,10 +15,12 @@
 // Each expert's weights are read once per 8 tokens that chose it, from L2 after the first time.
 //
 // Measured (256 experts, d = 2048, I = 512, 4 a token, LoRA of rank 16; a captured launch among
-// others): 21.8 us for 1 token, 38.9 for 8, 52.8 for 16, 100 for 64 (291 MB of weights, 2.9 TB/s).
-// One token is five steps of latency (the norm and router 4.3, three barriers 1.3 each, the plan 2.8,
-// gate and up 3 to 4.5, down and combine 4.5); 64 are bound by the integer work on the codes: gate
-// and up 41 us, 4.7 TB/s, down 29 us.
+// others): 21.3 us for 1 token, 22.3 for 2, 39 for 8, 51 for 16, 99 for 64 (291 MB of weights, 2.9
+// TB/s); 64 tokens over 16 experts 55.7.
+// One token is a chain of latencies (the norm and router 4.3, two barriers of 1.3, the plan 2.8,
+// gate and up 3 to 4.5, down and combine 4.5); 64 are the streams' instructions (gate and up about 41
+// us, 4.7 TB/s, down about 29 us) and 30 us of norm, routing, sums and three barriers: over the whole
+// launch issue slots and shared-memory wavefronts 51 %, integer pipe 35 %, tensor pipe 16 %.
 //
 // A launch with few tokens is a chain of latencies, code fetches among them: the streaming loops
 // exist in two forms for each of the two products and no more, and what they call at the end

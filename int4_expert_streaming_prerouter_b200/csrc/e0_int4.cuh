@@ -14,7 +14,8 @@
 // The activations are brought to fp16 per token and group of 64 by a power of two that takes
 // the largest of the group to [2^15, 2^16): exact for every bf16 value down to 2^-28 of the
 // group's largest, and off by at most 2^-36 of the largest below that.  8-bit activations are
-// exact.
+// exact.  Against 64 bits the fp32 logits of 2048 channels are off by 1.1e-7 of their size, as fp32
+// sums of the products in another order are.
 #pragma once
 #include <cooperative_groups.h>
 #include "e0_device.cuh"
@@ -230,10 +231,11 @@ __device__ __forceinline__ void act_group_e4m3(uint2 w, float scale, int i, int 
 // each adds up a part of the rows over the cluster's shared memory.
 //
 // Measured (a captured launch among others): 2048 x 2048 with LoRA at one token 6.3 us, 5120 x 2048 at
-// 8 int8 tokens 6.4, 65521 x 2048 at one token 18.4 (3.9 TB/s), 8192 x 4096 at 32 e4m3 tokens 20.5.
+// 8 int8 tokens 6.1, 65521 x 2048 at one token 18.5 (3.9 TB/s), 8192 x 4096 at 32 e4m3 tokens 20.4.
 // The small ones are the latency of a launch, the activations (3.3 us before the first tile) and one
-// tile; 65521 rows by the weights and the wait for the first activations; 32 tokens by shared-memory
-// reads and the matrix instructions.  Ring depths 3 and 2: pair 18.3 us at
+// tile; 65521 rows by the weights and the wait for the first activations; 32 tokens by latency (a tile
+// of four stages a warp, one stage ahead: no unit above half its rate, issue slots 47 %, shared-memory
+// wavefronts 40 %, tensor pipe 22 %, on 132 of the SMs).  Ring depths 3 and 2: pair 18.3 us at
 // one token and 65521 rows, with a depth of 2 19.9 (4: no change); wide needs the room for activations.
 //
 // Two forms.  Pair (up to 4 tokens, N = 1): the 8 columns of a matrix instruction are 4 tokens
